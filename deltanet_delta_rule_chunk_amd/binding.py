@@ -10,6 +10,7 @@ the library is missing it raises: there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -33,9 +34,14 @@ EXPORTS = ("deltanet_chunk_fwd", "deltanet_chunk_fwd_workspace_bytes", "deltanet
            "deltanet_kda_chunk_fwd", "deltanet_kda_chunk_fwd_workspace_bytes",
            "deltanet_kda_decode_step", "deltanet_chunk_bwd", "deltanet_chunk_bwd_workspace_bytes",
            "deltanet_status_string", "deltanet_last_hip_error", "deltanet_version",
-           "deltanet_profile_start", "deltanet_profile_stop", "deltanet_chunk_fwd_noalloc")
+           "deltanet_profile_start", "deltanet_profile_stop", "deltanet_chunk_fwd_noalloc",
+           "deltanet_linear_chunk_fwd", "deltanet_linear_chunk_fwd_workspace_bytes",
+           "deltanet_linear_chunk_bwd", "deltanet_linear_chunk_bwd_workspace_bytes",
+           "deltanet_linear_decode_step", "deltanet_qk_norm_rope", "deltanet_qk_norm_rope_bwd",
+           "deltanet_qk_norm_rope_bwd_workspace_bytes")
 PROFILE_SLOTS = ("chunk_prep", "chunk_scan", "decode", "features", "bwd_prep", "bwd_fwd_scan",
-                 "bwd_scan", "bwd_cc", "bwd_qk")
+                 "bwd_scan", "bwd_cc", "bwd_qk", "linear_state", "linear_out", "linear_bwd",
+                 "linear_decode", "qk_norm_rope", "qk_norm_rope_bwd")
 
 _lib = None
 
@@ -93,6 +99,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.deltanet_chunk_bwd.restype = i
     lib.deltanet_chunk_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     lib.deltanet_chunk_bwd_workspace_bytes.restype = sz
+    f = ctypes.c_float
+    lib.deltanet_linear_chunk_fwd.argtypes = [vp] * 7 + [i] * 8 + [vp, sz, vp]
+    lib.deltanet_linear_chunk_fwd.restype = i
+    lib.deltanet_linear_chunk_bwd.argtypes = [vp] * 12 + [i] * 7 + [vp, sz, vp]
+    lib.deltanet_linear_chunk_bwd.restype = i
+    lib.deltanet_linear_decode_step.argtypes = [vp] * 6 + [i] * 7 + [vp]
+    lib.deltanet_linear_decode_step.restype = i
+    lib.deltanet_qk_norm_rope.argtypes = [vp] * 9 + [i] + [vp] * 2 + [i] * 8 + [f, i, vp]
+    lib.deltanet_qk_norm_rope.restype = i
+    lib.deltanet_qk_norm_rope_bwd.argtypes = ([vp] * 9 + [i] + [vp] * 8 + [i] * 8
+                                              + [f, i, vp, sz, vp])
+    lib.deltanet_qk_norm_rope_bwd.restype = i
+    for name in ("linear_chunk_fwd", "linear_chunk_bwd"):
+        fn = getattr(lib, f"deltanet_{name}_workspace_bytes")
+        fn.argtypes, fn.restype = [i] * 7, sz
+    lib.deltanet_qk_norm_rope_bwd_workspace_bytes.argtypes = [i] * 6
+    lib.deltanet_qk_norm_rope_bwd_workspace_bytes.restype = sz
     lib.deltanet_status_string.argtypes = [i]
     lib.deltanet_status_string.restype = ctypes.c_char_p
     lib.deltanet_last_hip_error.argtypes = []
@@ -458,6 +481,315 @@ def gated_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: 
                       beta: torch.Tensor, S: torch.Tensor, **kw) -> torch.Tensor:
     """Gated decode step: ``decode_step`` with the per-(b, h) decay alpha."""
     return decode_step(q, k, v, beta, S, alpha=alpha, **kw)
+
+
+def _on(device: torch.device):
+    """The device made current for a call on its tensors (a null stream names
+    the current device's)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, device: torch.device, stream):
+    """(pointer, bytes, keeper) of the caller's workspace or a new one."""
+    if given is None:
+        if need == 0:
+            return None, 0, None
+        given = _alloc(need, torch.uint8, device, stream)
+    elif given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def linear_workspace_bytes(B: int, H: int, L: int, d_k: int, d_v: int,
+                           in_dtype: torch.dtype = torch.bfloat16, H_qk: Optional[int] = None,
+                           backward: bool = False) -> int:
+    """Workspace of ``linear_chunk_fwd`` (``linear_chunk_bwd``) for these sizes."""
+    lib = load()
+    fn = (lib.deltanet_linear_chunk_bwd_workspace_bytes if backward
+          else lib.deltanet_linear_chunk_fwd_workspace_bytes)
+    return int(fn(B, H, H if H_qk is None else H_qk, L, d_k, d_v, _code(in_dtype)))
+
+
+def _check_linear(q, k, v, log_decay, states, dims=4):
+    """Shapes of the gated linear recurrence's inputs, ``[B, H, L, d]`` or (one
+    token, ``dims`` = 3) ``[B, H, d]``; ``states`` are (tensor, name) pairs."""
+    if q.dim() != dims or v.dim() != dims:
+        raise ValueError(f"q and v must have {dims} dimensions (got {tuple(q.shape)}, {tuple(v.shape)})")
+    dev, tok, d_k = q.device, tuple(q.shape[2:-1]), q.shape[-1]
+    B, H_qk, (H, d_v) = q.shape[0], q.shape[1], (v.shape[1], v.shape[-1])
+    _check(q, "q", (B, H_qk, *tok, d_k), device=dev)
+    _check(k, "k", (B, H_qk, *tok, d_k), q.dtype, dev)
+    _check(v, "v", (B, H, *tok, d_v), q.dtype, dev)
+    if log_decay is not None:
+        _check(log_decay, "log_decay", (B, H, *tok), torch.float32, dev)
+    for t, n in states:
+        if t is not None:
+            _check(t, n, (B, H, d_k, d_v), torch.float32, dev)
+    return B, H, H_qk, d_k, d_v
+
+
+def linear_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: Optional[torch.Tensor] = None, S0: Optional[torch.Tensor] = None,
+                     *, out_dtype: torch.dtype = torch.float32, o: Optional[torch.Tensor] = None,
+                     S_final: Optional[torch.Tensor] = None, want_state: bool = True,
+                     workspace: Optional[torch.Tensor] = None, stream=None
+                     ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence over a sequence (``deltanet_linear_chunk_fwd``):
+    ``S = e^g S + k^T v``, ``o = q S``.  q,k ``[B,H_qk,L,d_k]``, v ``[B,H,L,d_v]``
+    (fp32 or bf16, same dtype; H a multiple of H_qk, head h reads q and k of
+    head ``h // (H // H_qk)``), log_decay ``[B,H,L]`` fp32 (``-inf`` wipes the
+    state exactly) or None, S0 ``[B,H,d_k,d_v]`` fp32 or None.  Returns
+    ``(o, S_final)``; S_final is None when ``want_state`` is False."""
+    lib = load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S0, "S0"), (S_final, "S_final")))
+    dev, L = q.device, q.shape[2]
+    with _on(dev):
+        if o is None:
+            o = _alloc((B, H, L, d_v), out_dtype, dev, stream)
+        _check(o, "o", (B, H, L, d_v), out_dtype, dev)
+        if S_final is None and want_state:
+            S_final = _alloc((B, H, d_k, d_v), torch.float32, dev, stream)
+        need = linear_workspace_bytes(B, H, L, d_k, d_v, q.dtype, H_qk)
+        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
+        st = lib.deltanet_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
+                                           _ptr(o), _ptr(S_final), B, H, H_qk, L, d_k, d_v,
+                                           _code(q.dtype), _code(out_dtype), ws, ws_bytes,
+                                           _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_linear_chunk_fwd")
+    return o, S_final
+
+
+def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: Optional[torch.Tensor], S0: Optional[torch.Tensor],
+                     dO: torch.Tensor, dS_final: Optional[torch.Tensor] = None, *,
+                     want_dS0: bool = True, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of ``linear_chunk_fwd`` (``deltanet_linear_chunk_bwd``) from dO
+    ``[B,H,L,d_v]`` (the inputs' dtype) and dS_final ``[B,H,d_k,d_v]`` fp32 or
+    None.  Returns ``(dq, dk, dv, dlog_decay, dS0)``: dq, dk, dv in the inputs'
+    dtype, dlog_decay (None without log_decay) and dS0 (None when ``want_dS0``
+    is False) in fp32."""
+    lib = load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S0, "S0"), (dS_final, "dS_final")))
+    dev, L = q.device, q.shape[2]
+    _check(dO, "dO", (B, H, L, d_v), q.dtype, dev)
+    with _on(dev):
+        dq, dk = (_alloc(q.shape, q.dtype, dev, stream) for _ in range(2))
+        dv = _alloc(v.shape, q.dtype, dev, stream)
+        dg = None if log_decay is None else _alloc(log_decay.shape, torch.float32, dev, stream)
+        dS0 = _alloc((B, H, d_k, d_v), torch.float32, dev, stream) if want_dS0 else None
+        need = linear_workspace_bytes(B, H, L, d_k, d_v, q.dtype, H_qk, backward=True)
+        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
+        st = lib.deltanet_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
+                                           _ptr(dO), _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv),
+                                           _ptr(dg), _ptr(dS0), B, H, H_qk, L, d_k, d_v,
+                                           _code(q.dtype), ws, ws_bytes, _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_linear_chunk_bwd")
+    return dq, dk, dv, dg, dS0
+
+
+class _LinearRule(torch.autograd.Function):
+    """``linear_chunk_fwd`` (o in the inputs' dtype) with its gradient from
+    ``linear_chunk_bwd``, which needs only the inputs."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, S0):
+        o, S_final = linear_chunk_fwd(q, k, v, log_decay, S0, out_dtype=v.dtype)
+        ctx.save_for_backward(q, k, v, log_decay, S0)
+        return o, S_final
+
+    @staticmethod
+    def backward(ctx, dO, dS_final):
+        q, k, v, log_decay, S0 = ctx.saved_tensors
+        want_dS0 = S0 is not None and ctx.needs_input_grad[4]
+        return linear_chunk_bwd(q, k, v, log_decay, S0, dO.contiguous(), dS_final.contiguous(),
+                                want_dS0=want_dS0)
+
+
+def linear_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                log_decay: Optional[torch.Tensor] = None, S0: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable gated linear recurrence for training: ``(o, S_final)`` as
+    ``linear_chunk_fwd`` returns them (o in the inputs' dtype), with gradients
+    for every input from ``deltanet_linear_chunk_bwd``."""
+    return _LinearRule.apply(q, k, v, log_decay, S0)
+
+
+def linear_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       log_decay: Optional[torch.Tensor], S: torch.Tensor, *,
+                       out_dtype: torch.dtype = torch.float32, o: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """One token of the gated linear recurrence (``deltanet_linear_decode_step``):
+    updates S ``[B,H,d_k,d_v]`` in place and returns o ``[B,H,d_v]`` = q S_new.
+    q,k ``[B,H_qk,d_k]``, v ``[B,H,d_v]``, log_decay ``[B,H]`` fp32 or None."""
+    lib = load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S, "S"),), dims=3)
+    dev = q.device
+    with _on(dev):
+        if o is None:
+            o = _alloc((B, H, d_v), out_dtype, dev, stream)
+        _check(o, "o", (B, H, d_v), out_dtype, dev)
+        st = lib.deltanet_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S),
+                                             _ptr(o), B, H, H_qk, d_k, d_v, _code(q.dtype),
+                                             _code(out_dtype), _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_linear_decode_step")
+    return o
+
+
+def _check_rows(t: torch.Tensor, name: str, shape, dtype, device):
+    """A tensor of rows at any strides over its other dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU (got {t.device})")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _strides(t: torch.Tensor):
+    return (ctypes.c_longlong * 3)(*t.stride()[:3])
+
+
+def _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, sections):
+    """Checks shared by both directions; (sizes, leading arguments, section counts)."""
+    if q_raw.dim() != 4 or k_raw.dim() != 4:
+        raise ValueError("q_raw and k_raw must be [B, H, L, d]")
+    dev, (B, H_q, L, d) = q_raw.device, q_raw.shape
+    H_k = k_raw.shape[1]
+    _check_rows(q_raw, "q_raw", (B, H_q, L, d), q_raw.dtype, dev)
+    _check_rows(k_raw, "k_raw", (B, H_k, L, d), q_raw.dtype, dev)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _check(t, n, (d,), torch.float32, dev)
+    d_rot, axes, counts = 0, 1, None
+    if inv_freq is not None:
+        d_rot = 2 * inv_freq.numel()
+        _check(inv_freq, "inv_freq", (d_rot // 2,), torch.float32, dev)
+        if positions is None:
+            raise ValueError("positions are required with inv_freq")
+        axes = positions.shape[0] if positions.dim() == 3 else 1
+        _check(positions, "positions", (axes, B, L) if positions.dim() == 3 else (B, L),
+               torch.int32, dev)
+        if sections is None and axes > 1:
+            raise ValueError("several position axes need sections")
+        if sections is not None:
+            if len(sections) != axes:
+                raise ValueError(f"{len(sections)} sections for {axes} position axes")
+            counts = (ctypes.c_int * axes)(*sections)
+    lead = (_ptr(q_raw), _strides(q_raw), _ptr(k_raw), _strides(k_raw), _ptr(q_weight),
+            _ptr(k_weight), _ptr(positions) if d_rot else None, _ptr(inv_freq), counts, axes)
+    return (B, H_q, H_k, L, d, d_rot), lead
+
+
+def qk_norm_rope(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torch.Tensor],
+                 inv_freq: Optional[torch.Tensor], *, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, sections=None, eps: float = 1e-6,
+                 norm: bool = True, interleaved: bool = False, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Per-head RMS norm of q and k and rotation by position in one pass
+    (``deltanet_qk_norm_rope``).  q_raw ``[B,H_q,L,d]``, k_raw ``[B,H_k,L,d]``
+    (fp32 or bf16) at any strides with contiguous rows, so views of a fused
+    projection are read in place; weights ``[d]`` fp32 or None; positions
+    ``[B,L]`` or ``[axes,B,L]`` int32; inv_freq ``[d_rot/2]`` fp32 (None: no
+    rotation); ``sections``: rotated pairs per position axis.  Returns dense
+    ``(q_hat, k_hat)`` in the inputs' dtype."""
+    lib = load()
+    (B, H_q, H_k, L, d, d_rot), lead = _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight,
+                                                 k_weight, sections)
+    dev = q_raw.device
+    with _on(dev):
+        qh = _alloc((B, H_q, L, d), q_raw.dtype, dev, stream)
+        kh = _alloc((B, H_k, L, d), q_raw.dtype, dev, stream)
+        st = lib.deltanet_qk_norm_rope(*lead, _ptr(qh), _ptr(kh), B, H_q, H_k, L, d, d_rot,
+                                       int(norm), int(interleaved), eps, _code(q_raw.dtype),
+                                       _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_qk_norm_rope")
+    return qh, kh
+
+
+def _like_rows(t: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor of t's shape: token rows ([B, L, H, d] in memory) if t's
+    heads lie inside its token rows, dense otherwise."""
+    B, H, L, d = t.shape
+    if t.stride(1) < t.stride(2):
+        return _alloc((B, L, H, d), t.dtype, t.device, stream).transpose(1, 2)
+    return _alloc((B, H, L, d), t.dtype, t.device, stream)
+
+
+def qk_norm_rope_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torch.Tensor],
+                     inv_freq: Optional[torch.Tensor], dq_hat: torch.Tensor, dk_hat: torch.Tensor,
+                     *, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, sections=None, eps: float = 1e-6,
+                     norm: bool = True, interleaved: bool = False,
+                     dq_raw: Optional[torch.Tensor] = None, dk_raw: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of ``qk_norm_rope`` (``deltanet_qk_norm_rope_bwd``).  dq_hat,
+    dk_hat are dense, in the inputs' dtype.  Returns ``(dq_raw, dk_raw,
+    dq_weight, dk_weight)``; the weights' gradients (fp32) are None where the
+    weight is.  ``dq_raw``, ``dk_raw`` may be given, at any strides (the parts
+    of a fused projection's gradient)."""
+    lib = load()
+    (B, H_q, H_k, L, d, d_rot), lead = _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight,
+                                                 k_weight, sections)
+    dev, t = q_raw.device, q_raw.dtype
+    _check(dq_hat, "dq_hat", (B, H_q, L, d), t, dev)
+    _check(dk_hat, "dk_hat", (B, H_k, L, d), t, dev)
+    with _on(dev):
+        dq_raw = _like_rows(q_raw, stream) if dq_raw is None else dq_raw
+        dk_raw = _like_rows(k_raw, stream) if dk_raw is None else dk_raw
+        _check_rows(dq_raw, "dq_raw", (B, H_q, L, d), t, dev)
+        _check_rows(dk_raw, "dk_raw", (B, H_k, L, d), t, dev)
+        dw = [None if w is None else _alloc((d,), torch.float32, dev, stream)
+              for w in (q_weight, k_weight)]
+        need = int(lib.deltanet_qk_norm_rope_bwd_workspace_bytes(B, H_q, H_k, L, d, _code(t)))
+        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
+        st = lib.deltanet_qk_norm_rope_bwd(*lead, _ptr(dq_hat), _ptr(dk_hat), _ptr(dq_raw),
+                                           _strides(dq_raw), _ptr(dk_raw), _strides(dk_raw),
+                                           _ptr(dw[0]), _ptr(dw[1]), B, H_q, H_k, L, d, d_rot,
+                                           int(norm), int(interleaved), eps, _code(t), ws,
+                                           ws_bytes, _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_qk_norm_rope_bwd")
+    return dq_raw, dk_raw, dw[0], dw[1]
+
+
+class _RotaryQK(torch.autograd.Function):
+    """``qk_norm_rope`` with its gradient from ``qk_norm_rope_bwd``."""
+
+    @staticmethod
+    def forward(ctx, q_raw, k_raw, q_weight, k_weight, positions, inv_freq, how):
+        ctx.save_for_backward(q_raw, k_raw, q_weight, k_weight, positions, inv_freq)
+        ctx.how = how
+        return qk_norm_rope(q_raw, k_raw, positions, inv_freq, q_weight=q_weight,
+                            k_weight=k_weight, **how)
+
+    @staticmethod
+    def backward(ctx, dq_hat, dk_hat):
+        q_raw, k_raw, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        return (*qk_norm_rope_bwd(q_raw, k_raw, positions, inv_freq, dq_hat.contiguous(),
+                                  dk_hat.contiguous(), q_weight=q_weight, k_weight=k_weight,
+                                  **ctx.how), None, None, None)
+
+
+def rotary_qk(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torch.Tensor],
+              inv_freq: Optional[torch.Tensor], *, q_weight: Optional[torch.Tensor] = None,
+              k_weight: Optional[torch.Tensor] = None, sections=None, eps: float = 1e-6,
+              norm: bool = True, interleaved: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable ``qk_norm_rope`` for training, with gradients for q_raw,
+    k_raw and the weights from ``deltanet_qk_norm_rope_bwd``."""
+    return _RotaryQK.apply(q_raw, k_raw, q_weight, k_weight, positions, inv_freq,
+                           dict(sections=sections, eps=eps, norm=norm, interleaved=interleaved))
 
 
 def profile_start() -> None:

@@ -86,7 +86,13 @@ enum ProfSlot {
   kSlotBwdScan = 6,
   kSlotBwdCc = 7,
   kSlotBwdQk = 8,
-  kNumSlots = 9
+  kSlotLinearState = 9,
+  kSlotLinearOut = 10,
+  kSlotLinearBwd = 11,
+  kSlotLinearDecode = 12,
+  kSlotQkNormRope = 13,
+  kSlotQkNormRopeBwd = 14,
+  kNumSlots = 15
 };
 
 // Records a HIP event on `s` before (end = false) or after (end = true) the
@@ -120,6 +126,73 @@ hipError_t launch_kda_chunk_fwd(const ChunkArgs& a);
 // Bytes of the gated form's per-chunk log-decay table; it sits at the end of
 // the workspace, after the kernels' other scratch.
 size_t gated_log_decay_bytes(int B, int H, int L, int C);
+
+// The gated linear recurrence (dn_linear.hip, dn_linear_bwd.hip,
+// dn_linear_decode.hip).  Head h reads q and k of head h / (H / H_qk).
+struct LinearArgs {
+  const void *q, *k, *v;
+  const float* log_decay;  // [B,H,L] or null (no decay)
+  const float* S0;         // may be null (zero state)
+  void* o;
+  float* S_final;          // may be null
+  int B, H, H_qk, L, d_k, d_v, in_dtype, out_dtype;
+  void* workspace;         // at least linear_workspace_bytes(...) bytes
+  hipStream_t stream;
+};
+size_t linear_workspace_bytes(int B, int H, int L, int d_k, int d_v);
+hipError_t launch_linear_fwd(const LinearArgs& a);
+
+struct LinearBwdArgs {
+  const void *q, *k, *v;
+  const float* log_decay;  // or null
+  const float* S0;         // or null
+  const void* dO;          // [B,H,L,d_v] in_dtype
+  const float* dS_final;   // or null (zero)
+  void *dq, *dk, *dv;      // in_dtype
+  float* dlog_decay;       // or null (not written)
+  float* dS0;              // or null (not written)
+  int B, H, H_qk, L, d_k, d_v, in_dtype;
+  void* workspace;         // at least linear_bwd_workspace_bytes(...) bytes
+  hipStream_t stream;
+};
+size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v);
+hipError_t launch_linear_bwd(const LinearBwdArgs& a);
+
+struct LinearDecodeArgs {
+  const void *q, *k, *v;
+  const float* log_decay;  // [B,H] or null
+  float* S;
+  void* o;
+  int B, H, H_qk, d_k, d_v, in_dtype, out_dtype;
+  hipStream_t stream;
+};
+hipError_t launch_linear_decode(const LinearDecodeArgs& a);
+
+// Per-head norm of q and k and rotation by position (dn_qk_norm_rope.hip).
+constexpr int kMaxAxes = 4;
+struct Rows {
+  const void* p;
+  long long sb, sh, sl;  // strides in elements
+};
+struct QkNormRopeArgs {
+  Rows x[2];               // raw q, k
+  const float* weight[2];  // [d] or null (ones)
+  const int* positions;    // [axes][B][L]
+  const float* inv_freq;   // [d_rot / 2]
+  int ends[kMaxAxes];      // axis a rotates pairs up to ends[a] (exclusive)
+  void* y[2];              // forward: [B][H][L][d]; backward: the gradients given there (read)
+  Rows dx[2];              // backward: gradients of x (written)
+  float* dw[2];            // backward: [d] or null
+  int H[2];
+  int B, L, d, d_rot, norm, interleaved, dtype;
+  float eps;
+  void* workspace;         // backward: at least qk_norm_rope_bwd_workspace_bytes(...) bytes
+  hipStream_t stream;
+};
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a);
+long long qk_norm_rope_max_tokens(int heads, int d);
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int L, int d);
+hipError_t launch_qk_norm_rope_bwd(const QkNormRopeArgs& a);
 
 // The fixed per-GPU scratch area of the allocation-free forward
 // (dn_noalloc.hip): its size, and its address on the device `stream` belongs

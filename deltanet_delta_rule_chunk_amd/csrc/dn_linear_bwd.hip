@@ -1,0 +1,213 @@
+// dn_linear_bwd.hip -- the gated linear recurrence's backward.
+//
+// The vector gradients are three walks of the forward's output kernel
+// (dn_linear.h):
+//     dq = F(dO, v, k) on S^T,  dv = R(k, q, dO) on dS,  dk = R(v, dO, q) on dS^T.
+//
+// The decay's gradient.  With c_t the product <S_{t-1}, dS_t> e^{g_t} of the
+// state before token t with the gradient it receives through token t,
+//     d g_t = sum over pairs (write i < t, read r >= t) of the pair's term
+//           + what reads r >= t take from before the pairs' reach
+//           + what the state that leaves keeps of it,
+// which splits by 64-row chunks with no difference of unlike sizes in it:
+//     d g_t =  sum_{r >= t} (x_r + m_r)  +  sum_{i < t} y_i  +  D_c
+//   x_r = q_r . (dq_r's part from the entering state)        (walk of dq)
+//   y_i = k_i . (dk_i's part from the exit gradient)         (walk of dk)
+//   m_r = sum_{i<r} P_ri (dO_r . v_i) - sum_{s>r} P_sr (dO_s . v_r)  (walk of dq:
+//         summed over r >= t, the pairs that cross t)
+//   D_c = e^{G_C} <S_c, dS_c'>: entering state against exit gradient.
+// D follows from chunk to chunk: <S_{c+1}, dS_c'> = D_{c+1} + sum x (chunk
+// c+1) = D_c + sum y (chunk c), anchored at the segments' ends, where both
+// states are at hand.  A token's own pair (r = i) never enters, so a strong
+// decay, whose gradient is small beside q . dq, keeps its accuracy.  The sums
+// over rows and chunks are taken in fp64; they are a few bytes per token.
+//
+// Heads that share q and k: each state head's dq and dk go to the workspace
+// in fp32, and a last kernel adds the group's in head order and rounds once.
+
+#include "dn_linear.h"
+
+namespace dn {
+namespace lin {
+
+struct DecayGradArgs {
+  const float *g, *x, *y, *m;
+  const float* S;      // [BH][nseg + 1][N]: slot s + 1 = the state that leaves segment s
+  const float* X;      // [BH][nseg][N]: the reversed walk's state behind segment s (nseg > 1)
+  const float* dS;     // [BH][N] or null: gradient of the last state
+  float* dg;
+  int L, BH, N;
+  Split s;
+};
+
+// One workgroup per (head, segment), from the segment's last chunk back, one
+// wave per chunk.
+static __global__ __launch_bounds__(NTHR) void decay_grad_kernel(DecayGradArgs a) {
+  __shared__ double part[4], tx[4], ty[4];
+  const int bh = blockIdx.x / a.s.nseg, seg = blockIdx.x % a.s.nseg;
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const bool end = seg == a.s.nseg - 1;
+  const float* X = end ? (a.dS ? a.dS + (size_t)bh * a.N : nullptr)
+                       : a.X + ((size_t)bh * a.s.nseg + seg) * a.N;
+  double acc = 0.0;
+  if (X) {
+    const float* S = a.S + ((size_t)bh * (a.s.nseg + 1) + seg + 1) * a.N;
+    for (int i = threadIdx.x * 4; i < a.N; i += NTHR * 4) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(S + i), v = *reinterpret_cast<const f32x4*>(X + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc += (double)u[e] * (double)v[e];
+    }
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
+  if (l == 0) part[w] = acc;
+  __syncthreads();
+  // <state that leaves the chunk at hand, its gradient>
+  double held = (part[0] + part[1]) + (part[2] + part[3]);
+  const int c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc);
+  // (The reversed walk's states are gradients of the state after a segment's
+  // first token; the decay in front of that token stands between.)
+  if (!end) held *= exp2_hw((float)log2_decay(a.g[(size_t)bh * a.L + c1 * C]));
+  for (int top = c1; top > c0; top -= 4) {
+    const int c = top - 1 - w;  // wave 0 takes the last chunk
+    const bool on = c >= c0;
+    const size_t at = ((size_t)bh * a.s.nc + (on ? c : c0)) * C + l;
+    const double x = on ? a.x[at] : 0.0, y = on ? a.y[at] : 0.0, m = on ? a.m[at] : 0.0;
+    const double sx = wave_scan(x + m), sy = wave_scan(y);
+    double ax = x;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) ax += __shfl_xor(ax, off, 64);
+    const double all = __shfl(sx, 63, 64), ay = __shfl(sy, 63, 64);
+    __syncthreads();  // the previous round's totals are read
+    if (l == 0) tx[w] = ax, ty[w] = ay;
+    __syncthreads();
+    double D = held;
+    for (int i = 0; i < 4; ++i) {
+      D -= ty[i];
+      if (i == w) break;
+      D += tx[i];
+    }
+    for (int i = 0; i < 4; ++i) held += tx[i] - ty[i];
+    const int t = c * C + l;
+    if (on && t < a.L) {
+      const size_t i = (size_t)bh * a.L + t;
+      const double v = (all - sx + x + m) + (sy - y) + D;
+      a.dg[i] = log2_decay(a.g[i]) <= kWipe2 ? 0.f : (float)v;
+    }
+  }
+}
+
+// out[u] = sum over the group's members of in[u grp + m], rounded once.
+template <typename OT>
+__global__ __launch_bounds__(256) void group_sum_kernel(const float* in, OT* out, size_t per_head, int grp, size_t n) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const size_t u = i / per_head;
+  const float* p = in + u * grp * per_head + (i - u * per_head);
+  f32x4 x = *reinterpret_cast<const f32x4*>(p);
+  for (int m = 1; m < grp; ++m) x += *reinterpret_cast<const f32x4*>(p + (size_t)m * per_head);
+  store4(out + i, x);
+}
+
+struct BwdWs {
+  size_t S, X, dS, dX, x, y, m, dq, dk, total;  // byte offsets
+};
+static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v) {
+  const size_t BH = (size_t)B * H, N = (size_t)d_k * d_v * 4;
+  const Split s = split_of((int)BH, L);
+  const size_t rows = BH * s.nc * C * 4, vec = H == H_qk ? 0 : BH * L * d_k * 4;
+  BwdWs w{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at += (n + 255) & ~(size_t)255;
+    return p;
+  };
+  w.S = take(BH * (s.nseg + 1) * N);
+  w.X = take(s.nseg > 1 ? BH * s.nseg * N : 0);
+  w.dS = take(BH * s.nseg * 8);
+  w.dX = take(BH * s.nseg * 8);
+  w.x = take(rows);
+  w.y = take(rows);
+  w.m = take(rows);
+  w.dq = take(vec);
+  w.dk = take(vec);
+  w.total = at;
+  return w;
+}
+
+template <typename IT, typename OT, int DK, int DV>
+static hipError_t backward(const LinearBwdArgs& a) {
+  const int BH = a.B * a.H, grp = a.H / a.H_qk;
+  const Split s = split_of(BH, a.L);
+  const BwdWs o = bwd_ws(a.B, a.H, a.H_qk, a.L, DK, DV);
+  const int N = DK * DV;
+  char* const base = static_cast<char*>(a.workspace);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+  auto d = [&](size_t off) { return reinterpret_cast<double*>(base + off); };
+  hipError_t e;
+  if (s.nseg > 1) {
+    StateArgs st{{a.k, grp}, {a.v, 1}, a.log_decay, f(o.S), d(o.dS), s.nseg + 1, a.L, BH, grp, 0, s.nseg - 1, s};
+    if ((e = launch_state<IT, DK, DV, false>(st, a.stream)) != hipSuccess) return e;
+    CombineArgs cs{f(o.S), d(o.dS), a.S0, s.nseg + 1, s.nseg, N};
+    if ((e = launch_combine<false>(cs, BH, a.stream)) != hipSuccess) return e;
+    StateArgs sx{{a.q, grp}, {a.dO, 1}, a.log_decay, f(o.X), d(o.dX), s.nseg, a.L, BH, grp, 1, s.nseg - 1, s};
+    if ((e = launch_state<IT, DK, DV, true>(sx, a.stream)) != hipSuccess) return e;
+    CombineArgs cx{f(o.X), d(o.dX), a.dS_final, s.nseg, s.nseg, N};
+    if ((e = launch_combine<true>(cx, BH, a.stream)) != hipSuccess) return e;
+  }
+  // The last state is wanted only against its own gradient.
+  float* last = a.dS_final ? f(o.S) + (size_t)s.nseg * N : nullptr;
+  const bool shared = grp > 1;
+  OutArgs q{{a.dO, 1}, {a.v, 1}, {a.k, grp}, {a.q, grp}, a.log_decay, f(o.S), a.S0,
+            shared ? (void*)f(o.dq) : a.dq, last, (long long)(s.nseg + 1) * N, f(o.x), f(o.m), s.nseg + 1,
+            a.L, BH, grp, s};
+  if ((e = launch_out<IT, OT, DV, DK, false, kPairs>(q, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
+  OutArgs v{{a.k, grp}, {a.q, grp}, {a.dO, 1}, {nullptr, 1}, a.log_decay, f(o.X), a.dS_final,
+            a.dv, a.dS0, N, nullptr, nullptr, s.nseg, a.L, BH, grp, s};
+  if ((e = launch_out<IT, IT, DK, DV, true, kNone>(v, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
+  OutArgs k{{a.v, 1}, {a.dO, 1}, {a.q, grp}, {a.k, grp}, a.log_decay, f(o.X), a.dS_final,
+            shared ? (void*)f(o.dk) : a.dk, nullptr, 0, f(o.y), nullptr, s.nseg, a.L, BH, grp, s};
+  if ((e = launch_out<IT, OT, DV, DK, true, kDots>(k, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
+  if (shared) {
+    const size_t n = (size_t)a.B * a.H_qk * a.L * DK, per = (size_t)a.L * DK;
+    const dim3 grid((unsigned)((n / 4 + 255) / 256));
+    for (int i = 0; i < 2; ++i) {
+      hipLaunchKernelGGL((group_sum_kernel<IT>), grid, dim3(256), 0, a.stream, f(i ? o.dk : o.dq),
+                         static_cast<IT*>(i ? a.dk : a.dq), per, grp, n);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  if (!a.dlog_decay) return hipSuccess;
+  DecayGradArgs g{a.log_decay, f(o.x), f(o.y), f(o.m), f(o.S), f(o.X), a.dS_final, a.dlog_decay, a.L, BH, N, s};
+  prof_mark(kSlotLinearBwd, false, a.stream);
+  hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(BH * s.nseg)), dim3(NTHR), 0, a.stream, g);
+  e = hipGetLastError();
+  prof_mark(kSlotLinearBwd, true, a.stream);
+  return e;
+}
+
+template <int DK, int DV>
+static hipError_t backward_d(const LinearBwdArgs& a) {
+  if (a.in_dtype == 0) return backward<float, float, DK, DV>(a);
+  return a.H == a.H_qk ? backward<bf16, bf16, DK, DV>(a) : backward<bf16, float, DK, DV>(a);
+}
+
+}  // namespace lin
+
+size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v) {
+  return L == 0 ? 0 : lin::bwd_ws(B, H, H_qk, L, d_k, d_v).total;
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs& a) {
+  if (a.L == 0)
+    return a.dS0 && a.dS0 != a.dS_final
+               ? lin::launch_copy_state(a.dS0, a.dS_final, (size_t)a.B * a.H * a.d_k * a.d_v, a.stream)
+               : hipSuccess;
+  if (a.d_k == 64 && a.d_v == 64) return lin::backward_d<64, 64>(a);
+  if (a.d_k == 64 && a.d_v == 128) return lin::backward_d<64, 128>(a);
+  if (a.d_k == 128 && a.d_v == 64) return lin::backward_d<128, 64>(a);
+  return lin::backward_d<128, 128>(a);
+}
+
+}  // namespace dn

@@ -1,0 +1,94 @@
+// dn_linear_decode.hip -- one token of the gated linear recurrence on gfx950:
+//     S <- e^g S + k^T v,   o = q S.
+//
+// Bound by HBM: per head it reads and writes the 4 d_k d_v byte state and
+// does 4 d_k d_v flops on it.  Nothing in the step waits for a sum over the
+// state: each element is read, updated, multiplied by its q and written.
+//
+// A work item is a head, or a slice of a head's columns; thread (rg, cg) of a
+// 256-thread workgroup holds 4 adjacent columns of rows rg, rg + ROWG, ....
+// The partial sums of o meet in LDS.
+
+#include "dn_common.h"
+#include "dn_launch.h"
+
+namespace dn {
+namespace lin {
+
+typedef float vf4 __attribute__((ext_vector_type(4)));
+
+template <int DK, int DV, int NSL, typename IT, typename OT>
+__global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, const IT* __restrict__ k,
+                                                     const IT* __restrict__ v, const float* __restrict__ g,
+                                                     float* __restrict__ S, OT* __restrict__ o, int grp) {
+  constexpr int W = DV / NSL, COLG = W / 4, ROWG = 256 / COLG, RPT = DK / ROWG;
+  static_assert(COLG * 4 * NSL == DV && RPT * ROWG == DK, "tile shape");
+  __shared__ float ks[DK], qs[DK];
+  __shared__ vf4 red[ROWG][COLG];
+  const int tid = threadIdx.x, cg = tid % COLG, rg = tid / COLG;
+  const int bh = blockIdx.x / NSL, c0 = blockIdx.x % NSL * W;
+  float* const Sh = S + (size_t)bh * (DK * DV) + c0 + cg * 4;
+  vf4 s[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) s[i] = *reinterpret_cast<const vf4*>(Sh + (size_t)(rg + i * ROWG) * DV);
+  const size_t row = (size_t)(bh / grp) * DK;
+  for (int i = tid; i < DK; i += 256) {
+    ks[i] = to_f32(k[row + i]);
+    qs[i] = to_f32(q[row + i]);
+  }
+  vf4 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = to_f32(v[(size_t)bh * DV + c0 + cg * 4 + e]);
+  const float a = g ? expf(g[bh]) : 1.f;
+  __syncthreads();
+  vf4 acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = rg + i * ROWG;
+    s[i] = a * s[i] + ks[r] * x;
+    acc += qs[r] * s[i];
+    __builtin_nontemporal_store(s[i], reinterpret_cast<vf4*>(Sh + (size_t)r * DV));
+  }
+  red[rg][cg] = acc;
+  __syncthreads();
+  if (tid < W) {
+    float y = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWG; ++r) y += red[r][tid / 4][tid % 4];
+    o[(size_t)bh * DV + c0 + tid] = from_f32<OT>(y);
+  }
+}
+
+template <int DK, int DV, typename IT, typename OT>
+static hipError_t launch(const LinearDecodeArgs& a) {
+  const int BH = a.B * a.H;
+  prof_mark(kSlotLinearDecode, false, a.stream);
+#define DN_LAUNCH(NSL)                                                                            \
+  hipLaunchKernelGGL((decode_kernel<DK, DV, NSL, IT, OT>), dim3((unsigned)BH * NSL), dim3(256), 0, \
+                     a.stream, static_cast<const IT*>(a.q), static_cast<const IT*>(a.k),          \
+                     static_cast<const IT*>(a.v), a.log_decay, a.S, static_cast<OT*>(a.o), a.H / a.H_qk)
+  if (BH < 512) DN_LAUNCH(4);
+  else DN_LAUNCH(1);
+#undef DN_LAUNCH
+  hipError_t e = hipGetLastError();
+  prof_mark(kSlotLinearDecode, true, a.stream);
+  return e;
+}
+
+template <int DK, int DV>
+static hipError_t launch_d(const LinearDecodeArgs& a) {
+  if (a.in_dtype == 1)
+    return a.out_dtype == 1 ? launch<DK, DV, bf16, bf16>(a) : launch<DK, DV, bf16, float>(a);
+  return a.out_dtype == 1 ? launch<DK, DV, float, bf16>(a) : launch<DK, DV, float, float>(a);
+}
+
+}  // namespace lin
+
+hipError_t launch_linear_decode(const LinearDecodeArgs& a) {
+  if (a.d_k == 64 && a.d_v == 64) return lin::launch_d<64, 64>(a);
+  if (a.d_k == 64 && a.d_v == 128) return lin::launch_d<64, 128>(a);
+  if (a.d_k == 128 && a.d_v == 64) return lin::launch_d<128, 64>(a);
+  return lin::launch_d<128, 128>(a);
+}
+
+}  // namespace dn

@@ -301,6 +301,138 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
                                   int B, int H, int d_k, int d_v, dn_dtype in_dtype, dn_dtype out_dtype,
                                   hipStream_t stream);
 
+/*
+ * The gated linear recurrence: the additive write with a decay, per (b, h)
+ * and token t, in order,
+ *     S   = e^{g_t} S + k_t^T v_t
+ *     o_t = q_t S                      (read after the write, no scale)
+ * It is the printed chunked linear-attention form of the page above, section
+ * "DeltaNet (Parallelizing linear transformers with delta rule)", with the
+ * decay of the Gated DeltaNet article on the state: the delta rule without
+ * its read before the write.
+ *
+ *   q, k     : [B, H_qk, L, d_k] in_dtype.  State head h reads q and k of head
+ *              h / (H / H_qk); H must be a multiple of H_qk (H_qk = H: every
+ *              head its own).
+ *   v        : [B, H, L, d_v] in_dtype
+ *   log_decay: [B, H, L] fp32, the decay's natural logarithm, or NULL (no
+ *              decay).  0 keeps the state, -inf wipes it exactly: a log decay
+ *              of -inf at its first token separates a document from the one
+ *              before it in the same row.  Values above 0 are not checked
+ *              (the product is then no decay).
+ *   S0       : [B, H, d_k, d_v] fp32 or NULL (zero state)
+ *   o        : [B, H, L, d_v] out_dtype, written
+ *   S_final  : [B, H, d_k, d_v] fp32 or NULL; may be the buffer of S0.
+ *   L >= 0 (L = 0 copies S0, or zeros, to S_final).  d_k, d_v in {64, 128}.
+ * The result does not depend on how the sequence is cut into chunks, so
+ * there is no chunk argument.  bf16 inputs run on the bf16 matrix cores, every
+ * fp32 operand as a sum of bf16 pieces; fp32 inputs on the fp32 ones.  A
+ * non-finite q, k or v row makes the outputs of its 64-token chunk and the
+ * states after it non-finite.  workspace, workspace_bytes, stream, status
+ * codes and every other rule: as for deltanet_chunk_fwd; the workspace holds
+ * one fp32 state per segment that the sequence is cut into, and may be 0
+ * bytes.
+ */
+int deltanet_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* S0, void* o, float* S_final,
+                              int B, int H, int H_qk, int L, int d_k, int d_v,
+                              dn_dtype in_dtype, dn_dtype out_dtype,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace deltanet_linear_chunk_fwd needs (0 also if the sizes are
+ * invalid or unsupported). */
+size_t deltanet_linear_chunk_fwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v,
+                                                 dn_dtype in_dtype);
+
+/*
+ * Its gradient, from the gradients of o and S_final:
+ *   dO        : [B, H, L, d_v] in_dtype;  dS_final: [B, H, d_k, d_v] fp32 or NULL (zero)
+ *   dq, dk    : [B, H_qk, L, d_k] in_dtype (heads that share q and k are added in fp32)
+ *   dv        : [B, H, L, d_v] in_dtype
+ *   dlog_decay: [B, H, L] fp32, the gradient of log_decay (exactly 0 where
+ *               log_decay is -inf), or NULL (not written; required to be NULL
+ *               when log_decay is)
+ *   dS0       : [B, H, d_k, d_v] fp32 or NULL (not written)
+ * Nothing from a forward call is needed.  Outputs may not overlap inputs or
+ * one another.
+ */
+int deltanet_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* S0, const void* dO, const float* dS_final,
+                              void* dq, void* dk, void* dv, float* dlog_decay, float* dS0,
+                              int B, int H, int H_qk, int L, int d_k, int d_v, dn_dtype in_dtype,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace deltanet_linear_chunk_bwd needs (0 if the sizes are
+ * invalid or unsupported). */
+size_t deltanet_linear_chunk_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v,
+                                                 dn_dtype in_dtype);
+
+/* One token of the gated linear recurrence, S updated in place; o = q S_new.
+ * q, k: [B, H_qk, d_k], v, o: [B, H, d_v], log_decay: [B, H] fp32 or NULL. */
+int deltanet_linear_decode_step(const void* q, const void* k, const void* v, const float* log_decay,
+                                float* S, void* o, int B, int H, int H_qk, int d_k, int d_v,
+                                dn_dtype in_dtype, dn_dtype out_dtype, hipStream_t stream);
+
+/*
+ * Per-head norm of q and k and rotation by position, in one pass (the map in
+ * front of a core that deltanet_feature_prep's silu and L2 norm are for the
+ * delta rule).  For each row x of d_k elements:
+ *     n = x / sqrt(mean(x^2) + eps) o weight         (norm = 0: n = x o weight)
+ *     pair j of n's first d_rot elements is turned by p inv_freq[j] radians:
+ *       (a, b) -> (a cos - b sin, a sin + b cos)
+ * Pair j is elements (j, j + d_rot / 2), or (2 j, 2 j + 1) when interleaved;
+ * elements from d_rot on are not turned.  p is the token's position on pair
+ * j's axis: axis a owns sections[a] pairs, in order (one axis: all of them).
+ *
+ *   q_raw, k_raw  : rows (b, h, l) of [B, H_q, L, d_k] and [B, H_k, L, d_k], dtype, at
+ *                   strides[0] b + strides[1] h + strides[2] l elements (strides NULL:
+ *                   dense).  So q and k can be read out of a fused projection's rows.
+ *                   Strides are >= 0 and keep every row 16-byte aligned; 0 repeats a row.
+ *                   H_k may be 0 (q only).
+ *   q_weight, k_weight: [d_k] fp32 or NULL (ones)
+ *   positions     : [n_axes, B, L] int32;  inv_freq: [d_rot / 2] fp32;
+ *   sections      : HOST array of n_axes counts adding up to d_rot / 2 (NULL for one axis)
+ *                   Both device pointers may be NULL when d_rot = 0 (no rotation).
+ *   q_hat, k_hat  : [B, H_q, L, d_k], [B, H_k, L, d_k] dtype, dense, written
+ *   d_k in {64, 128}; d_rot a multiple of 8, 0 .. d_k; n_axes 1 .. 4; eps >= 0.
+ * Evaluated in fp32, angles in fp64 (any int32 position).  Rows beyond ~1e19
+ * overflow their fp32 sum of squares (the row then maps to zeros).
+ */
+int deltanet_qk_norm_rope(const void* q_raw, const long long* q_strides,
+                          const void* k_raw, const long long* k_strides,
+                          const float* q_weight, const float* k_weight,
+                          const int* positions, const float* inv_freq,
+                          const int* sections, int n_axes, void* q_hat, void* k_hat,
+                          int B, int H_q, int H_k, int L, int d_k, int d_rot,
+                          int norm, int interleaved, float eps, dn_dtype dtype, hipStream_t stream);
+
+/*
+ * Its gradient, from dq_hat, dk_hat ([B, H, L, d_k] dtype, dense):
+ *   dq_raw, dk_raw: rows at strides of their own (NULL: dense), written; their rows may
+ *                   not share elements, and may be the q and k parts of one buffer of
+ *                   token rows (equal batch and token strides, q and k apart in the row)
+ *   dq_weight, dk_weight: [d_k] fp32 or NULL (not written), summed over all rows
+ *                   in an order that does not change from call to call
+ * The rest as above.
+ */
+int deltanet_qk_norm_rope_bwd(const void* q_raw, const long long* q_strides,
+                              const void* k_raw, const long long* k_strides,
+                              const float* q_weight, const float* k_weight,
+                              const int* positions, const float* inv_freq,
+                              const int* sections, int n_axes,
+                              const void* dq_hat, const void* dk_hat,
+                              void* dq_raw, const long long* dq_strides,
+                              void* dk_raw, const long long* dk_strides,
+                              float* dq_weight, float* dk_weight,
+                              int B, int H_q, int H_k, int L, int d_k, int d_rot,
+                              int norm, int interleaved, float eps, dn_dtype dtype,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace deltanet_qk_norm_rope_bwd needs (0 also if the sizes are
+ * invalid or unsupported). */
+size_t deltanet_qk_norm_rope_bwd_workspace_bytes(int B, int H_q, int H_k, int L, int d_k,
+                                                 dn_dtype dtype);
+
 /* Static, NUL-terminated description of a status code. */
 const char* deltanet_status_string(int status);
 
@@ -319,8 +451,10 @@ int deltanet_last_hip_error(void);
  * prep and scan kernels at 128-token chunks, counted together), 6 = reverse
  * state pass, 7 = per-chunk matrix gradients, 8 = dq / dk; for bf16 inputs one
  * kernel computes both the matrix gradients and dq / dk and is counted in
- * slot 8).  Recording adds two
- * event records per launch.
+ * slot 8; the gated linear recurrence's: 9 = segment sums and their
+ * combination, 10 = outputs, 11 = the backward's walks and decay gradient,
+ * 12 = decode; the q / k norm with rotation: 13 = forward, 14 = backward).
+ * Recording adds two event records per launch.
  * deltanet_profile_start() creates the thread's events up front (4096,
  * enough for 2048 launches; more are created as needed), so it can take a
  * few milliseconds the first time; it returns DN_ERR_HIP if that fails.
