@@ -37,10 +37,13 @@
 // through LDS as operand fragments.
 //
 // Precision.  bf16 q, k, v (and dO) enter products as they are.  An fp32
-// operand enters as a sum of bf16 pieces: 2 pieces (16 bits) where the result
-// is stored in bf16, whose own rounding is 256 times coarser, and 3 pieces
-// (24 bits, all of fp32) where it reaches an fp32 result: the state, and what
-// the gradients of the decay are summed from.  fp32 inputs run the same
+// operand enters as a sum of bf16 pieces: 3 pieces (24 bits, all of fp32) where
+// it reaches an fp32 result through long sums: the rows added to the state, the
+// state read for an fp32 output or for what the decay's gradient is summed
+// from; 2 pieces (16 bits) for the state read for a bf16 output, whose own
+// rounding is 256 times coarser, and for P, whose sums span one chunk (a third
+// piece of P would cost the second workgroup of each CU its LDS; it leaves
+// 2^-17 of a term).  fp32 inputs run the same
 // kernels on the fp32 matrix instruction, with nothing split.  Log decays are
 // summed in fp64: a difference of two sums keeps the accuracy of the short
 // sum between them however long the chunk's own is.
@@ -77,15 +80,27 @@ __device__ __forceinline__ double log2_decay(float g) {
 
 // ---- operands ------------------------------------------------------------------
 //
-// A fragment holds, per lane (g = lane / 16, i = lane % 16), 8 values of row
-// (or column) i of a 16 x 32 operand: contraction slots 4 g + e and
-// 16 + 4 g + e, e = 0 .. 3.
+// A fragment holds, per lane (g = lane / 16, i = lane % 16), the 8 values of
+// row (or column) i of a 16 x 32 operand in contraction slots e = 0 .. 7.  Two
+// slot orders are in use:
+//   over a row's elements:  8 g + e, so a fragment is 8 adjacent elements;
+//   over rows (tokens):     4 g + e and 16 + 4 g + e - 4, what two stacked
+//                           accumulator tiles hold ("d4" of dn_mfma.h).
+// The state's accumulator tiles (2 kb, 2 kb + 1) then hold, in their rows
+// 4 g + e, the state's rows 32 kb + 8 g + e and 32 kb + 8 g + 4 + e, so that
+// they too are read in the first order: see state_row().
 
 struct F32x8 {
   float v[8];
 };
 
-// LDS tile of C rows x D and its fragments.
+// Row of the state in accumulator tile kt, lane group g, element 0 (the
+// elements are 4 adjacent rows).
+__device__ __forceinline__ int state_row(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
+
+// LDS tile of C rows x D, in 16-byte pieces XOR-swizzled by a function of the
+// row so that row reads (16 rows, one piece) and column reads (4 or 16 rows,
+// pieces 2 apart) spread over the banks.  Pieces arrive straight from HBM.
 template <typename IT, int D>
 struct Tile;
 
@@ -93,67 +108,67 @@ template <int D>
 struct Tile<bf16, D> {
   typedef bf16x8 Frag;
   static constexpr int bytes = C * D * 2;
-  static constexpr int PPR = D / 8;  // 16-byte pieces per row
+  static constexpr int PPR = D / 8;  // pieces per row
   unsigned char* p;
+  static __device__ __forceinline__ int swizzle(int row) { return kswz<D>(row); }
   __device__ __forceinline__ uint16_t* e(int off) const { return reinterpret_cast<uint16_t*>(p) + off; }
-  __device__ __forceinline__ void put(int row, int piece, uint4 x) const {
-    *reinterpret_cast<uint4*>(e(koff<D>(row, piece))) = x;
-  }
-  // Row r0 + i, contraction over columns 32 kb ..
+  // Row r0 + i, contraction over elements 32 kb ..
   __device__ __forceinline__ Frag row(int r0, int kb) const {
-    const int l = threadIdx.x & 63, g = l >> 4, r = r0 + (l & 15);
-    const int ch = 4 * kb + (g >> 1), h = 4 * (g & 1);
-    const uint2 a = *reinterpret_cast<const uint2*>(e(koff<D>(r, ch) + h));
-    const uint2 b = *reinterpret_cast<const uint2*>(e(koff<D>(r, ch + 2) + h));
-    return as_bf16x8(a, b);
+    const int l = threadIdx.x & 63;
+    return as_bf16x8(*reinterpret_cast<const uint4*>(e(koff<D>(r0 + (l & 15), 4 * kb + (l >> 4)))));
   }
   __device__ __forceinline__ uint2 tr(int off) const {
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(e(off))));
   }
-  // Column c0 + i, contraction over rows 32 tb ..  (transposing reads: lane
-  // 4 m + a of a 16-lane group addresses row m, columns 4 a .. + 3).
-  __device__ __forceinline__ Frag col(int c0, int tb) const {
-    const int l = threadIdx.x & 63, g = l >> 4, i = l & 15, m = i >> 2, a = i & 3;
-    const int r = 32 * tb + 4 * g + m, ch = (c0 >> 3) + (a >> 1), h = 4 * (a & 1);
-    return as_bf16x8(tr(koff<D>(r, ch) + h), tr(koff<D>(r + 16, ch) + h));
+  // Column c(i), contraction over rows 32 tb .. (transposing reads: lane
+  // 4 m + a of a 16-lane group addresses row m, 4 columns; lane 4 a + b receives
+  // its column b of every row).
+  __device__ __forceinline__ Frag cols(int piece, int half, int tb) const {
+    const int l = threadIdx.x & 63, r = 32 * tb + 4 * (l >> 4) + ((l & 15) >> 2);
+    return as_bf16x8(tr(koff<D>(r, piece) + 4 * half), tr(koff<D>(r + 16, piece) + 4 * half));
   }
-  // Columns c .. c + 3 (c % 4 == 0) of a row, as fp32.
-  __device__ __forceinline__ f32x4 four(int row, int c) const {
-    const uint2 a = *reinterpret_cast<const uint2*>(e(koff<D>(row, c >> 3) + (c & 4)));
-    return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
-                 __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u)};
+  // ... of adjacent columns c0 + i.
+  __device__ __forceinline__ Frag col(int c0, int tb) const {
+    const int a = threadIdx.x & 3;
+    return cols((c0 >> 3) + (a >> 1), a & 1, tb);
+  }
+  // ... of the columns that are the state's rows in accumulator tile kt.
+  __device__ __forceinline__ Frag state_col(int kt, int tb) const {
+    return cols(4 * (kt >> 1) + (threadIdx.x & 3), kt & 1, tb);
   }
 };
 
 template <int D>
 struct Tile<float, D> {
   typedef F32x8 Frag;
-  static constexpr int P = D + 4;  // row pitch: column reads of 4 row groups miss each other's banks
-  static constexpr int bytes = C * P * 4;
+  static constexpr int bytes = C * D * 4;
   static constexpr int PPR = D / 4;
   unsigned char* p;
-  __device__ __forceinline__ float* e(int off) const { return reinterpret_cast<float*>(p) + off; }
-  __device__ __forceinline__ void put(int row, int piece, uint4 x) const {
-    *reinterpret_cast<uint4*>(e(row * P + 4 * piece)) = x;
+  static __device__ __forceinline__ int swizzle(int row) {
+    return ((row >> 2) & 1) | ((row & 3) << 1) | (row & 8);
   }
+  __device__ __forceinline__ float* e(int off) const { return reinterpret_cast<float*>(p) + off; }
+  __device__ __forceinline__ static int off(int row, int c) { return row * D + (((c >> 2) ^ swizzle(row)) << 2) + (c & 3); }
   __device__ __forceinline__ Frag row(int r0, int kb) const {
-    const int l = threadIdx.x & 63, g = l >> 4, off = (r0 + (l & 15)) * P + 32 * kb + 4 * g;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(e(off));
-    const f32x4 b = *reinterpret_cast<const f32x4*>(e(off + 16));
+    const int l = threadIdx.x & 63, r = r0 + (l & 15), c = 32 * kb + 8 * (l >> 4);
+    const f32x4 a = *reinterpret_cast<const f32x4*>(e(off(r, c)));
+    const f32x4 b = *reinterpret_cast<const f32x4*>(e(off(r, c + 4)));
     return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
   }
-  __device__ __forceinline__ Frag col(int c0, int tb) const {
-    const int l = threadIdx.x & 63, g = l >> 4, off = (32 * tb + 4 * g) * P + c0 + (l & 15);
+  __device__ __forceinline__ Frag at_col(int c, int tb) const {
+    const int r = 32 * tb + 4 * ((threadIdx.x & 63) >> 4);
     Frag f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      f.v[x] = *e(off + x * P);
-      f.v[4 + x] = *e(off + (16 + x) * P);
+      f.v[x] = *e(off(r + x, c));
+      f.v[4 + x] = *e(off(r + 16 + x, c));
     }
     return f;
   }
-  __device__ __forceinline__ f32x4 four(int row, int c) const {
-    return *reinterpret_cast<const f32x4*>(e(row * P + c));
+  __device__ __forceinline__ Frag col(int c0, int tb) const { return at_col(c0 + (threadIdx.x & 15), tb); }
+  __device__ __forceinline__ Frag state_col(int kt, int tb) const {
+    const int i = threadIdx.x & 15;
+    return at_col(state_row(kt, i >> 2) + (i & 3), tb);
   }
 };
 
@@ -275,25 +290,51 @@ __device__ __forceinline__ double fill_decays(Decays* d, float g) {
 
 // ---- staging ---------------------------------------------------------------------
 
-// The next chunk's rows of one tensor on their way to LDS.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes per lane from a buffer straight into LDS at lds + 16 lane; the
+// range check of the descriptor `r` makes rows past the end zeros.  Written in
+// assembly so that the compiler does not order LDS reads of other buffers
+// behind it: the caller waits with wait_loads() and a barrier before reading.
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r) : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// A chunk's rows of one tensor on their way to an LDS tile: wave w fills rows
+// 16 w .. + 15, a wave's lanes 64 adjacent pieces of LDS at a time; each lane
+// fetches the piece that the swizzle puts there.
 template <typename IT, int D, bool REV>
 struct Stage {
   typedef Tile<IT, D> T;
-  static constexpr int N = C * T::PPR / NTHR;  // 16-byte pieces per thread
-  uint4 x[N];
-  // `base` is the head's first row.
-  __device__ __forceinline__ void load(const IT* base, int c, int L) {
-    const int rows = min(C, L - c * C);
-    const rsrc_t r = make_rsrc(base + (size_t)c * C * D, (uint32_t)(rows * D * sizeof(IT)));
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = bload16(r, (i * NTHR + threadIdx.x) * 16, 0);
-  }
-  __device__ __forceinline__ void store(T t) const {
+  static constexpr int N = C * T::PPR / NTHR;  // pieces per lane
+  static constexpr int RPI = 64 / T::PPR;      // rows per 64 pieces
+  uint32_t voff[N];
+  __device__ __forceinline__ Stage() {
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = i * NTHR + threadIdx.x, row = e / T::PPR;
-      t.put(REV ? C - 1 - row : row, e % T::PPR, x[i]);
+      const int row = (C / 4) * w + i * RPI + l / T::PPR, piece = (l % T::PPR) ^ T::swizzle(row);
+      voff[i] = (uint32_t)((REV ? C - 1 - row : row) * D * (int)sizeof(IT) + piece * 16);
     }
+  }
+  // `base` is the head's first row.
+  __device__ __forceinline__ void load(const IT* base, int c, int L, T t) const {
+    const int rows = min(C, L - c * C);
+    const uint64_t a = reinterpret_cast<uint64_t>(base + (size_t)c * C * D);
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffff;
+    r[2] = __builtin_amdgcn_readfirstlane(rows * D * (int)sizeof(IT));
+    r[3] = 0x00020000;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(lds_address(t.p) + (threadIdx.x >> 6) * (T::bytes / 4)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) load_to_lds(r, voff[i], lds + i * 1024);
   }
 };
 
@@ -381,7 +422,7 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16][DV / 64], Tile
     }
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt) {
-      const auto a = K.col(16 * kt, tb);
+      const auto a = K.state_col(kt, tb);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) st[kt][ct] = mma(a, y[ct], st[kt][ct]);
     }
@@ -389,7 +430,7 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16][DV / 64], Tile
 }
 
 // fp32 state (row-major [DK][DV], or [DV][DK] when TRANS) <-> this wave's
-// accumulators: rows 16 kt + 4 g + e, column j.
+// accumulators: rows state_row() + e, column j.
 template <int DK, int DV, bool TRANS>
 __device__ __forceinline__ void load_state(f32x4 (&st)[DK / 16][DV / 64], const float* S) {
   const int l = threadIdx.x & 63, g = l >> 4, w = threadIdx.x >> 6;
@@ -397,7 +438,7 @@ __device__ __forceinline__ void load_state(f32x4 (&st)[DK / 16][DV / 64], const 
   for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
     for (int ct = 0; ct < DV / 64; ++ct) {
-      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = 16 * kt + 4 * g;
+      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = state_row(kt, g);
       if (!S) {
         st[kt][ct] = zero4();
       } else if (TRANS) {
@@ -415,7 +456,7 @@ __device__ __forceinline__ void store_state(const f32x4 (&st)[DK / 16][DV / 64],
   for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
     for (int ct = 0; ct < DV / 64; ++ct) {
-      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = 16 * kt + 4 * g;
+      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = state_row(kt, g);
       const f32x4 x = st[kt][ct] * scale;
       if (TRANS) {
         *reinterpret_cast<f32x4*>(S + (size_t)j * DK + k0) = x;
@@ -435,15 +476,15 @@ __device__ __forceinline__ void value_frags(typename Tile<IT, DV>::Frag (&vf)[C 
     for (int ct = 0; ct < DV / 64; ++ct) vf[tb][ct] = V.col(w * (DV / 4) + 16 * ct, tb);
 }
 
+// Two sets of tiles: a chunk's rows arrive while the one before is used.
 template <typename IT, int DK, int DV>
-constexpr int state_lds() { return Tile<IT, DK>::bytes + Tile<IT, DV>::bytes + (int)sizeof(Decays); }
+constexpr int state_lds() { return 2 * (Tile<IT, DK>::bytes + Tile<IT, DV>::bytes + (int)sizeof(Decays)); }
 
 template <typename IT, int DK, int DV, bool REV>
 __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void state_kernel(StateArgs a) {
+  constexpr int TB = Tile<IT, DK>::bytes + Tile<IT, DV>::bytes;
   extern __shared__ __align__(16) unsigned char smem[];
-  const Tile<IT, DK> K{smem};
-  const Tile<IT, DV> V{smem + Tile<IT, DK>::bytes};
-  Decays* const dec = reinterpret_cast<Decays*>(smem + Tile<IT, DK>::bytes + Tile<IT, DV>::bytes);
+  Decays* const tables = reinterpret_cast<Decays*>(smem + 2 * TB);
 
   int bh, seg;
   if (!item_of(blockIdx.x, a.BH, a.grp, a.count, bh, seg)) return;
@@ -454,29 +495,33 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void state_kernel(St
   const float* g = a.g ? a.g + (size_t)bh * L : nullptr;
   const int n = c1 - c0;
   auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
-  const bool last_wave = threadIdx.x >= NTHR - 64;
+  const bool tables_wave = threadIdx.x >= NTHR - 64;
 
   f32x4 st[DK / 16][DV / 64];
   load_state<DK, DV, false>(st, nullptr);
-  Stage<IT, DK, REV> sk;
-  Stage<IT, DV, REV> sv;
-  sk.load(k, chunk(0), L);
-  sv.load(v, chunk(0), L);
-  float gn = load_decay<REV>(g, chunk(0), L);
+  const Stage<IT, DK, REV> sk;
+  const Stage<IT, DV, REV> sv;
+  auto load = [&](int i) {
+    unsigned char* const at = smem + (i & 1) * TB;
+    sk.load(k, chunk(i), L, Tile<IT, DK>{at});
+    sv.load(v, chunk(i), L, Tile<IT, DV>{at + Tile<IT, DK>::bytes});
+  };
   double sum = 0.0;
+  load(0);
+  if (tables_wave) sum += fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
   for (int i = 0; i < n; ++i) {
-    sk.store(K);
-    sv.store(V);
-    if (last_wave) sum += fill_decays(dec, gn);
+    wait_loads();
     __syncthreads();
-    const int cn = chunk(min(i + 1, n - 1));
-    sk.load(k, cn, L);
-    sv.load(v, cn, L);
-    gn = load_decay<REV>(g, cn, L);
+    float gn = 0.f;
+    if (i + 1 < n) {
+      if (tables_wave) gn = load_decay<REV>(g, chunk(i + 1), L);
+      load(i + 1);
+    }
+    unsigned char* const at = smem + (i & 1) * TB;
     typename Tile<IT, DV>::Frag vf[C / 32][DV / 64];
-    value_frags<IT, DV>(vf, V);
-    update_state<IT, DK, DV>(st, K, vf, dec);
-    __syncthreads();
+    value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes});
+    update_state<IT, DK, DV>(st, Tile<IT, DK>{at}, vf, &tables[i & 1]);
+    if (i + 1 < n && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
   }
   store_state<DK, DV, false>(st, a.states + ((size_t)bh * a.slots + seg) * (DK * DV), 1.f);
   if (threadIdx.x == NTHR - 1) a.decays[(size_t)bh * a.s.nseg + seg] = sum;
@@ -626,31 +671,57 @@ __device__ __forceinline__ void store4<bf16>(bf16* p, f32x4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-// Bytes of LDS: the tiles, P, the decay tables of this chunk and the next,
-// and the sums.
+// Bytes of LDS: four tile buffers, P, the decay tables of this chunk and the
+// next, and the sums.
 template <typename IT, typename OT, int DK, int DV, int EXTRA>
 struct OutLds {
-  // Pieces of an fp32 operand (see "Precision" above): P and the state where
-  // they only reach the output; the state where it reaches the row sums.
-  static constexpr int NSP = sizeof(OT) == 2 || EXTRA != kNone ? 2 : 3;
+  // Pieces of an fp32 operand (see "Precision" above): of P, of the state.
+  static constexpr int NSP = 2;
   static constexpr int NSS = sizeof(OT) == 2 && EXTRA == kNone ? 2 : 3;
-  static constexpr int K = Tile<IT, DK>::bytes;
-  static constexpr int V = K + Tile<IT, DK>::bytes;
-  static constexpr int W = V + Tile<IT, DV>::bytes;
-  static constexpr int P = W + (EXTRA != kNone ? Tile<IT, DV>::bytes : 0);
+  static constexpr int tile = Tile<IT, (DK > DV ? DK : DV)>::bytes;
+  static constexpr int P = 4 * tile;
   static constexpr int D = P + PBuf<IT, NSP>::bytes;
   static constexpr int S = D + 2 * (int)sizeof(Decays);
   static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums) : 0);
 };
 
+// Rows of w straight from HBM (rows past the end read as zeros).
+template <typename IT>
+__device__ __forceinline__ f32x4 row4(rsrc_t r, uint32_t at);
+template <>
+__device__ __forceinline__ f32x4 row4<float>(rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(f32x4, bload16(r, at, 0));
+}
+template <>
+__device__ __forceinline__ f32x4 row4<bf16>(rsrc_t r, uint32_t at) {
+  const uint2 a = bload8(r, at, 0);
+  return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
+               __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u)};
+}
+template <typename IT, int D>
+__device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row, int kb) {
+  const uint32_t at = (uint32_t)(row * D + 32 * kb + 8 * ((threadIdx.x & 63) >> 4)) * sizeof(IT);
+  if constexpr (sizeof(IT) == 2) {
+    return as_bf16x8(bload16(r, at, 0));
+  } else {
+    const f32x4 a = row4<float>(r, at), b = row4<float>(r, at + 16);
+    return F32x8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+  }
+}
+
+// A chunk takes two phases with a barrier behind each:
+//   1  P (from Q, K) and Q S;                       V arrives, and the next Q
+//   2  P V, the output, the state's update (K, V);  the next K arrives
+// Four tile buffers suffice: the next Q goes where V was a chunk ago, the next
+// K where Q is no longer read, the next V where K is no longer read.
 template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
 __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutArgs a) {
   using LD = OutLds<IT, OT, DK, DV, EXTRA>;
   constexpr int NRT = C / 16, CT = DV / 64, NSP = LD::NSP, NSS = LD::NSS;
   constexpr bool TRANS = EXTRA != kNone;  // dq and dk walk the transposed state
+  typedef Tile<IT, DK> TK;
+  typedef Tile<IT, DV> TV;
   extern __shared__ __align__(16) unsigned char smem[];
-  const Tile<IT, DK> Q{smem}, K{smem + LD::K};
-  const Tile<IT, DV> V{smem + LD::V}, W{smem + LD::W};
   const PBuf<IT, NSP> P{smem + LD::P};
   Decays* const tables = reinterpret_cast<Decays*>(smem + LD::D);
   Sums* const sums = reinterpret_cast<Sums*>(smem + LD::S);
@@ -681,69 +752,70 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
   if (w == 0) P.put(pfrag(0, 0), 1, zero4());
   if (w == 1) P.put(pfrag(2, 1), 1, zero4());
 
+  const Stage<IT, DK, REV> sk;
+  const Stage<IT, DV, REV> sv;
+  unsigned char *bq = smem, *bk = smem + LD::tile, *bv = smem + 2 * LD::tile, *bf = smem + 3 * LD::tile;
+  sk.load(q, chunk(0), L, TK{bq});
+  sk.load(k, chunk(0), L, TK{bk});
+  if (w == 3) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
   f32x4 st[DK / 16][CT];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
   load_state<DK, DV, TRANS>(st, S);
+  wait_loads();
+  __syncthreads();
 
-  Stage<IT, DK, REV> sq, sk;
-  Stage<IT, DV, REV> sv, sw;
-  auto load = [&](int c) {
-    sq.load(q, c, L);
-    sk.load(k, c, L);
-    sv.load(v, c, L);
-    if (EXTRA != kNone) sw.load(wp, c, L);
+  // A chunk's pair sums, once every wave has left its own.
+  auto store_pairs = [&](int c) {
+    float y = 0.f;
+    for (int x = 0; x < NRT; ++x) {
+      if (x <= lg) y += sums->out[tri(lg, x)][li];
+      if (x >= lg) y -= sums->key[tri(x, lg)][li];
+    }
+    a.pairs[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] = y;
   };
-  load(chunk(0));
-  float gn = load_decay<REV>(g, chunk(0), L);
-  if (w == 3) fill_decays(&tables[0], gn);
 
   for (int ci = 0; ci < n; ++ci) {
     const int c = chunk(ci);
+    const bool more = ci + 1 < n;
     const Decays* dec = &tables[ci & 1];
-    sq.store(Q);
-    sk.store(K);
-    sv.store(V);
-    if (EXTRA != kNone) sw.store(W);
-    __syncthreads();
-    const int cn = chunk(min(ci + 1, n - 1));
-    load(cn);
-    gn = load_decay<REV>(g, cn, L);
+    const TK Q{bq}, K{bk};
+    const TV V{bv};
+    sv.load(v, c, L, V);
+    if (more) sk.load(q, chunk(ci + 1), L, TK{bf});
+    rsrc_t wr;
+    f32x4 wd[NRT][CT];
+    float gn = 0.f;
+    if (w == 3 && more) gn = load_decay<REV>(g, chunk(ci + 1), L);
+    if constexpr (EXTRA != kNone) {
+      wr = make_rsrc(wp + (size_t)c * C * DV, (uint32_t)(min(C, L - c * C) * DV * (int)sizeof(IT)));
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          wd[rt][ct] = row4<IT>(wr, (uint32_t)((REV ? C - 1 - 16 * rt - li : 16 * rt + li) * DV + w * (DV / 4) +
+                                               16 * ct + 4 * lg) * sizeof(IT));
+    }
+    if (EXTRA == kPairs && w == 0 && ci > 0) store_pairs(chunk(ci - 1));
 
     // P^T tiles: rows are key rows 16 it + 4 lg + e, the column is output row
     // 16 rt + li.
+    f32x4 p[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
       const int rt = prt[x], it = pit[x];
+      p[x] = zero4();
       if (rt < 0) continue;
-      f32x4 p = zero4();
 #pragma unroll
-      for (int kb = 0; kb < DK / 32; ++kb) p = mma(K.row(16 * it, kb), Q.row(16 * rt, kb), p);
+      for (int kb = 0; kb < DK / 32; ++kb) p[x] = mma(K.row(16 * it, kb), Q.row(16 * rt, kb), p[x]);
       const int r = 16 * rt + li;
       const double Gr = dec->G[r];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * it + 4 * lg + e;
-        p[e] = i <= r ? p[e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
+        p[x][e] = i <= r ? p[x][e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
       }
-      P.put(pfrag(rt, it >> 1), it & 1, p);
-      if (EXTRA == kPairs) {
-        // Pair terms: P_ri (w_r . v_i), i < r.
-        f32x4 y = zero4();
-#pragma unroll
-        for (int kb = 0; kb < DV / 32; ++kb) y = mma(V.row(16 * it, kb), W.row(16 * rt, kb), y);
-        float col = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * it + 4 * lg + e;
-          const float m = i < r ? p[e] * y[e] : 0.f;
-          col += m;
-          const float row = sum_lanes16(m);
-          if (li == 0) sums->key[tri(rt, it)][4 * lg + e] = row;
-        }
-        col = sum_groups(col);
-        if (lg == 0) sums->out[tri(rt, it)][li] = col;
-      }
+      P.put(pfrag(rt, it >> 1), it & 1, p[x]);
     }
 
     // Output tiles (rows: this wave's columns, column: row 16 rt + li), first
@@ -776,10 +848,9 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         acc[rt][ct] *= f;
-        if (EXTRA != kNone) {
-          const f32x4 y = W.four(16 * rt + li, w * (DV / 4) + 16 * ct + 4 * lg);
+        if constexpr (EXTRA != kNone) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * y[e];
+          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * wd[rt][ct][e];
         }
       }
       if (EXTRA != kNone) {
@@ -787,19 +858,52 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
         if (lg == 0) sums->dots[w][16 * rt + li] = dot;
       }
     }
+    wait_loads();
     __syncthreads();
 
     // ... then what comes from the chunk's own rows.
-    typename Tile<IT, DV>::Frag vf[C / 32][CT];
+    if (more) sk.load(k, chunk(ci + 1), L, TK{bq});
+    typename TV::Frag vf[C / 32][CT];
     value_frags<IT, DV>(vf, V);
 #pragma unroll
-    for (int rt = 0; rt < NRT; ++rt) {
+    for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
       for (int kb = 0; kb <= rt / 2; ++kb) {
         const auto b = P.get(pfrag(rt, kb));
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mma(vf[kb][ct], b, acc[rt][ct]);
       }
+    if (EXTRA != kNone && w == 0)
+      a.dots[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] =
+          (sums->dots[0][lane] + sums->dots[1][lane]) + (sums->dots[2][lane] + sums->dots[3][lane]);
+    if constexpr (EXTRA == kPairs) {
+      // Pair terms: P_ri (w_r . v_i), i < r.
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const int rt = prt[x], it = pit[x];
+        if (rt < 0) continue;
+        f32x4 y = zero4();
+#pragma unroll
+        for (int kb = 0; kb < DV / 32; ++kb)
+          y = mma(V.row(16 * it, kb), row_frag<IT, DV>(wr, REV ? C - 1 - 16 * rt - li : 16 * rt + li, kb), y);
+        const int r = 16 * rt + li;
+        float col = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = 16 * it + 4 * lg + e < r ? p[x][e] * y[e] : 0.f;
+          col += m;
+          const float row = sum_lanes16(m);
+          if (li == 0) sums->key[tri(rt, it)][4 * lg + e] = row;
+        }
+        col = sum_groups(col);
+        if (lg == 0) sums->out[tri(rt, it)][li] = col;
+      }
+    }
+    update_state<IT, DK, DV>(st, K, vf, dec);
+    if (w == 3 && more) fill_decays(&tables[(ci + 1) & 1], gn);
+    wait_loads();
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
       const int t = token_of<REV>(c, 16 * rt + li);
       if (t < L) {
 #pragma unroll
@@ -807,23 +911,14 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
           store4(out + (size_t)t * DV + w * (DV / 4) + 16 * ct + 4 * lg, acc[rt][ct]);
       }
     }
-    if (EXTRA != kNone && w == 0) {
-      const size_t at = (size_t)bh * a.s.nc * C + token_of<REV>(c, lane);
-      a.dots[at] = (sums->dots[0][lane] + sums->dots[1][lane]) + (sums->dots[2][lane] + sums->dots[3][lane]);
-      if (EXTRA == kPairs) {
-        const int tile = lane >> 4;
-        float y = 0.f;
-        for (int x = 0; x < NRT; ++x) {
-          if (x <= tile) y += sums->out[tri(tile, x)][li];
-          if (x >= tile) y -= sums->key[tri(x, tile)][li];
-        }
-        a.pairs[at] = y;
-      }
-    }
-    update_state<IT, DK, DV>(st, K, vf, dec);
-    if (w == 3) fill_decays(&tables[(ci + 1) & 1], gn);
     __syncthreads();
+    unsigned char* const free = bv;
+    bv = bk;
+    bk = bq;
+    bq = bf;
+    bf = free;
   }
+  if (EXTRA == kPairs && w == 0) store_pairs(chunk(n - 1));
 
   if (a.last && seg == (REV ? 0 : a.s.nseg - 1)) {
     // Reversed, the walk ends with the gradient of the state after token 0;
