@@ -172,6 +172,14 @@ struct Tile<float, D> {
   }
 };
 
+// Two bf16 values packed from fp32.  (Opaque to the optimiser, which would
+// otherwise convert the low value a second time for its use as fp32.)
+__device__ __forceinline__ uint32_t pack_once(float a, float b) {
+  uint32_t u = pack_bf16(a, b);
+  asm("" : "+v"(u));
+  return u;
+}
+
 // An operand made of fp32 values: NS bf16 pieces, or the values themselves.
 template <typename IT, int NS>
 struct Made;
@@ -189,7 +197,7 @@ struct Made<bf16, NS> {
       uint32_t u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        u[i] = pack_bf16(r[2 * i], r[2 * i + 1]);
+        u[i] = pack_once(r[2 * i], r[2 * i + 1]);
         if (s + 1 < NS) {
           r[2 * i] -= __uint_as_float(u[i] << 16);
           r[2 * i + 1] -= __uint_as_float(u[i] & 0xffff0000u);
@@ -267,21 +275,42 @@ __device__ __forceinline__ float load_decay(const float* g, int c, int L) {
   return g && t < L ? g[t] : 0.f;
 }
 
+// Lane moves within the vector ALUs (no LDS round trip).  CTRL: 0x110 + n
+// moves by n lanes up within each 16, 0x120 + n turns each 16 by n, 0x142 and
+// 0x143 hand lane 15 of a 16 to the next and lane 31 to the upper 32.  Lanes
+// that receive nothing get 0.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp(int x) { return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false); }
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = dpp<CTRL, ROWS>((int)(uint32_t)u), hi = dpp<CTRL, ROWS>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, x))); }
+
 // Inclusive sums over a wave's 64 lanes.
 __device__ __forceinline__ double wave_scan(double x) {
-  const int l = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double y = __shfl_up(x, off, 64);
-    if (l >= off) x += y;
-  }
+  x += dpp<0x111>(x);
+  x += dpp<0x112>(x);
+  x += dpp<0x114>(x);
+  x += dpp<0x118>(x);
+  x += dpp<0x142, 0xa>(x);
+  x += dpp<0x143, 0xc>(x);
   return x;
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // One wave fills a chunk's table from its rows' log decays; returns the sum.
 __device__ __forceinline__ double fill_decays(Decays* d, float g) {
   const int l = threadIdx.x & 63;
-  const double G = wave_scan(log2_decay(g)), last = __shfl(G, 63, 64);
+  const double G = wave_scan(log2_decay(g)), last = lane_value(G, 63);
   d->G[l] = G;
   d->up[l] = exp2_hw((float)(last - G));
   if (l == 63) d->total = exp2_hw((float)G);
@@ -358,12 +387,15 @@ struct Split {
 // Enough segments for two workgroups on each of the 256 CUs, none of them
 // shorter than kMinChunks chunks (a segment costs a state's write and two
 // reads, 4 d_k d_v bytes each, against the rows it spares a walk).
-constexpr int kWorkgroups = 512, kMinChunks = 4;
+// None is longer than kMaxChunks, which bounds how far the decay's gradient is
+// carried from an exact value.
+constexpr int kWorkgroups = 512, kMinChunks = 4, kMaxChunks = 256;
 inline Split split_of(int BH, int L) {
   Split s;
   s.nc = cdiv(L, C);
   s.cps = cdiv(s.nc, cdiv(kWorkgroups, BH));
   if (s.cps < kMinChunks) s.cps = kMinChunks;
+  if (s.cps > kMaxChunks) s.cps = kMaxChunks;
   s.nseg = cdiv(s.nc, s.cps);
   return s;
 }
@@ -611,7 +643,7 @@ struct PBuf<bf16, NS> {
   __device__ __forceinline__ void put(int f, int half, f32x4 x) const {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      uint2 u = make_uint2(pack_once(x[0], x[1]), pack_once(x[2], x[3]));
       *at(f, s, half) = u;
       x[0] -= __uint_as_float(u.x << 16);
       x[1] -= __uint_as_float(u.x & 0xffff0000u);
@@ -657,8 +689,10 @@ __device__ __forceinline__ float sum_groups(float x) {  // over the 4 lane group
   return x;
 }
 __device__ __forceinline__ float sum_lanes16(float x) {  // over the 16 lanes of a group
-#pragma unroll
-  for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off, 64);
+  x += dpp<0x128>(x);
+  x += dpp<0x124>(x);
+  x += dpp<0x122>(x);
+  x += dpp<0x121>(x);
   return x;
 }
 
@@ -685,27 +719,35 @@ struct OutLds {
   static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums) : 0);
 };
 
-// Rows of w straight from HBM (rows past the end read as zeros).
+// Four adjacent elements of a row of w straight from HBM (rows past the end
+// read as zeros).
 template <typename IT>
-__device__ __forceinline__ f32x4 row4(rsrc_t r, uint32_t at);
+struct Four;
 template <>
-__device__ __forceinline__ f32x4 row4<float>(rsrc_t r, uint32_t at) {
-  return __builtin_bit_cast(f32x4, bload16(r, at, 0));
-}
+struct Four<float> {
+  f32x4 x;
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = __builtin_bit_cast(f32x4, bload16(r, at, 0)); }
+  __device__ __forceinline__ f32x4 get() const { return x; }
+};
 template <>
-__device__ __forceinline__ f32x4 row4<bf16>(rsrc_t r, uint32_t at) {
-  const uint2 a = bload8(r, at, 0);
-  return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
-               __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u)};
-}
+struct Four<bf16> {
+  uint2 x;
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = bload8(r, at, 0); }
+  __device__ __forceinline__ f32x4 get() const {
+    return f32x4{__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                 __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u)};
+  }
+};
 template <typename IT, int D>
 __device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row, int kb) {
   const uint32_t at = (uint32_t)(row * D + 32 * kb + 8 * ((threadIdx.x & 63) >> 4)) * sizeof(IT);
   if constexpr (sizeof(IT) == 2) {
     return as_bf16x8(bload16(r, at, 0));
   } else {
-    const f32x4 a = row4<float>(r, at), b = row4<float>(r, at + 16);
-    return F32x8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    Four<float> a, b;
+    a.load(r, at);
+    b.load(r, at + 16);
+    return F32x8{{a.x[0], a.x[1], a.x[2], a.x[3], b.x[0], b.x[1], b.x[2], b.x[3]}};
   }
 }
 
@@ -739,15 +781,14 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
 
-  // This wave's tiles of P (output tile rt, key tile it <= rt): 10 over 4 waves.
-  constexpr int kRt[4][3] = {{3, 3, 0}, {3, 3, 2}, {2, 2, -1}, {1, 1, -1}};
-  constexpr int kIt[4][3] = {{0, 1, 0}, {2, 3, 0}, {1, 2, -1}, {0, 1, -1}};
-  int prt[3], pit[3];
-#pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    prt[x] = w == 0 ? kRt[0][x] : w == 1 ? kRt[1][x] : w == 2 ? kRt[2][x] : kRt[3][x];
-    pit[x] = w == 0 ? kIt[0][x] : w == 1 ? kIt[1][x] : w == 2 ? kIt[2][x] : kIt[3][x];
-  }
+  // This wave's tiles of P (output tile rt, key tile it <= rt), 10 over 4
+  // waves: two of one rt, and on waves 2 and 3 a third, so that the decay
+  // table's wave (1) has time for it.
+  //   wave 0: (3,0) (3,1)   1: (3,2) (3,3)   2: (2,0) (2,1) (2,2)   3: (1,0) (1,1) (0,0)
+  const int prt = w < 2 ? 3 : w == 2 ? 2 : 1, pit = w == 1 ? 2 : 0;
+  const int prt2 = w == 2 ? 2 : 0, pit2 = w == 2 ? 2 : 0;
+  const bool third = w >= 2;
+  constexpr int kTableWave = 1;
   // The tiles above the diagonal that share a fragment with one below.
   if (w == 0) P.put(pfrag(0, 0), 1, zero4());
   if (w == 1) P.put(pfrag(2, 1), 1, zero4());
@@ -757,7 +798,7 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
   unsigned char *bq = smem, *bk = smem + LD::tile, *bv = smem + 2 * LD::tile, *bf = smem + 3 * LD::tile;
   sk.load(q, chunk(0), L, TK{bq});
   sk.load(k, chunk(0), L, TK{bk});
-  if (w == 3) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
+  if (w == kTableWave) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
   f32x4 st[DK / 16][CT];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
@@ -781,42 +822,54 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
     const Decays* dec = &tables[ci & 1];
     const TK Q{bq}, K{bk};
     const TV V{bv};
-    sv.load(v, c, L, V);
-    if (more) sk.load(q, chunk(ci + 1), L, TK{bf});
     rsrc_t wr;
-    f32x4 wd[NRT][CT];
-    float gn = 0.f;
-    if (w == 3 && more) gn = load_decay<REV>(g, chunk(ci + 1), L);
+    Four<IT> wd[NRT][CT];
+    auto w_row = [&](int r) { return REV ? C - 1 - r : r; };
     if constexpr (EXTRA != kNone) {
       wr = make_rsrc(wp + (size_t)c * C * DV, (uint32_t)(min(C, L - c * C) * DV * (int)sizeof(IT)));
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-          wd[rt][ct] = row4<IT>(wr, (uint32_t)((REV ? C - 1 - 16 * rt - li : 16 * rt + li) * DV + w * (DV / 4) +
-                                               16 * ct + 4 * lg) * sizeof(IT));
+          wd[rt][ct].load(wr, (uint32_t)(w_row(16 * rt + li) * DV + w * (DV / 4) + 16 * ct + 4 * lg) * sizeof(IT));
+    }
+    sv.load(v, c, L, V);
+    if (more) sk.load(q, chunk(ci + 1), L, TK{bf});
+    float gn = 0.f;
+    if (w == kTableWave && more) gn = load_decay<REV>(g, chunk(ci + 1), L);
+    typename TV::Frag wf[EXTRA == kPairs ? DV / 32 : 1];
+    if constexpr (EXTRA == kPairs) {
+#pragma unroll
+      for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb);
     }
     if (EXTRA == kPairs && w == 0 && ci > 0) store_pairs(chunk(ci - 1));
 
     // P^T tiles: rows are key rows 16 it + 4 lg + e, the column is output row
     // 16 rt + li.
-    f32x4 p[3];
+    f32x4 p[3] = {zero4(), zero4(), zero4()};
 #pragma unroll
-    for (int x = 0; x < 3; ++x) {
-      const int rt = prt[x], it = pit[x];
-      p[x] = zero4();
-      if (rt < 0) continue;
+    for (int kb = 0; kb < DK / 32; ++kb) {
+      const auto b = Q.row(16 * prt, kb);
+      p[0] = mma(K.row(16 * pit, kb), b, p[0]);
+      p[1] = mma(K.row(16 * pit + 16, kb), b, p[1]);
+    }
+    if (third) {
 #pragma unroll
-      for (int kb = 0; kb < DK / 32; ++kb) p[x] = mma(K.row(16 * it, kb), Q.row(16 * rt, kb), p[x]);
+      for (int kb = 0; kb < DK / 32; ++kb) p[2] = mma(K.row(16 * pit2, kb), Q.row(16 * prt2, kb), p[2]);
+    }
+    auto decay_tile = [&](f32x4& x, int rt, int it) {
       const int r = 16 * rt + li;
       const double Gr = dec->G[r];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * it + 4 * lg + e;
-        p[x][e] = i <= r ? p[x][e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
+        x[e] = i <= r ? x[e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
       }
-      P.put(pfrag(rt, it >> 1), it & 1, p[x]);
-    }
+      P.put(pfrag(rt, it >> 1), it & 1, x);
+    };
+    decay_tile(p[0], prt, pit);
+    decay_tile(p[1], prt, pit + 1);
+    if (third) decay_tile(p[2], prt2, pit2);
 
     // Output tiles (rows: this wave's columns, column: row 16 rt + li), first
     // what comes from the entering state.
@@ -849,8 +902,9 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
       for (int ct = 0; ct < CT; ++ct) {
         acc[rt][ct] *= f;
         if constexpr (EXTRA != kNone) {
+          const f32x4 y = wd[rt][ct].get();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * wd[rt][ct][e];
+          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * y[e];
         }
       }
       if (EXTRA != kNone) {
@@ -878,29 +932,39 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
           (sums->dots[0][lane] + sums->dots[1][lane]) + (sums->dots[2][lane] + sums->dots[3][lane]);
     if constexpr (EXTRA == kPairs) {
       // Pair terms: P_ri (w_r . v_i), i < r.
-#pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        const int rt = prt[x], it = pit[x];
-        if (rt < 0) continue;
-        f32x4 y = zero4();
-#pragma unroll
-        for (int kb = 0; kb < DV / 32; ++kb)
-          y = mma(V.row(16 * it, kb), row_frag<IT, DV>(wr, REV ? C - 1 - 16 * rt - li : 16 * rt + li, kb), y);
-        const int r = 16 * rt + li;
+      auto pair_sums = [&](const f32x4& x, f32x4 y, int rt, int it) {
+        const int r = 16 * rt + li, t = tri(rt, it);
         float col = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float m = 16 * it + 4 * lg + e < r ? p[x][e] * y[e] : 0.f;
+          const float m = 16 * it + 4 * lg + e < r ? x[e] * y[e] : 0.f;
           col += m;
           const float row = sum_lanes16(m);
-          if (li == 0) sums->key[tri(rt, it)][4 * lg + e] = row;
+          if (li == 0) sums->key[t][4 * lg + e] = row;
         }
         col = sum_groups(col);
-        if (lg == 0) sums->out[tri(rt, it)][li] = col;
+        if (lg == 0) sums->out[t][li] = col;
+      };
+      f32x4 y[3] = {zero4(), zero4(), zero4()};
+#pragma unroll
+      for (int kb = 0; kb < DV / 32; ++kb) {
+        y[0] = mma(V.row(16 * pit, kb), wf[kb], y[0]);
+        y[1] = mma(V.row(16 * pit + 16, kb), wf[kb], y[1]);
       }
+      if (third) {
+        if (w == 3) {
+#pragma unroll
+          for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb);
+        }
+#pragma unroll
+        for (int kb = 0; kb < DV / 32; ++kb) y[2] = mma(V.row(16 * pit2, kb), wf[kb], y[2]);
+        pair_sums(p[2], y[2], prt2, pit2);
+      }
+      pair_sums(p[0], y[0], prt, pit);
+      pair_sums(p[1], y[1], prt, pit + 1);
     }
     update_state<IT, DK, DV>(st, K, vf, dec);
-    if (w == 3 && more) fill_decays(&tables[(ci + 1) & 1], gn);
+    if (w == kTableWave && more) fill_decays(&tables[(ci + 1) & 1], gn);
     wait_loads();
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {

@@ -17,10 +17,14 @@
 //         summed over r >= t, the pairs that cross t)
 //   D_c = e^{G_C} <S_c, dS_c'>: entering state against exit gradient.
 // D follows from chunk to chunk: <S_{c+1}, dS_c'> = D_{c+1} + sum x (chunk
-// c+1) = D_c + sum y (chunk c), anchored at the segments' ends, where both
-// states are at hand.  A token's own pair (r = i) never enters, so a strong
-// decay, whose gradient is small beside q . dq, keeps its accuracy.  The sums
-// over rows and chunks are taken in fp64; they are a few bytes per token.
+// c+1) = D_c + sum y (chunk c), anchored at both ends of each segment, where
+// both states are at hand.  Walked from one end the roundings of the sums would
+// reach the other as an offset; the difference found there is handed back to
+// the chunks in proportion to the squares of the sums passed on the way, which
+// is the best estimate if those are what the roundings go by.  A token's own
+// pair (r = i) never enters, so a strong decay, whose gradient is small beside
+// q . dq, keeps its accuracy.  The sums over rows and chunks are taken in fp64;
+// they are a few bytes per token.
 //
 // Heads that share q and k: each state head's dq and dk go to the workspace
 // in fp32, and a last kernel adds the group's in head order and rounds once.
@@ -32,68 +36,100 @@ namespace lin {
 
 struct DecayGradArgs {
   const float *g, *x, *y, *m;
-  const float* S;      // [BH][nseg + 1][N]: slot s + 1 = the state that leaves segment s
+  const float* S;      // [BH][nseg + 1][N]: slot s = the state that enters segment s
   const float* X;      // [BH][nseg][N]: the reversed walk's state behind segment s (nseg > 1)
+  const float *S0, *dS0;  // [BH][N]: the first state and its gradient; S0 null: zero; dS0 null: not known
   const float* dS;     // [BH][N] or null: gradient of the last state
   float* dg;
   int L, BH, N;
   Split s;
 };
 
-// One workgroup per (head, segment), from the segment's last chunk back, one
-// wave per chunk.
-static __global__ __launch_bounds__(NTHR) void decay_grad_kernel(DecayGradArgs a) {
-  __shared__ double part[4], tx[4], ty[4];
+constexpr int kGradThreads = 1024;
+
+// <u, v> over a workgroup, every thread's answer.
+static __device__ double dot_states(const float* u, const float* v, int n, double* part) {
+  double acc = 0.0;
+  for (int i = threadIdx.x * 4; i < n; i += kGradThreads * 4) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(u + i), b = *reinterpret_cast<const f32x4*>(v + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc += (double)a[e] * (double)b[e];
+  }
+  acc = lane_value(wave_scan(acc), 63);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
+  __syncthreads();
+  double sum = 0.0;
+  for (int i = 0; i < kGradThreads / 64; ++i) sum += part[i];
+  return sum;
+}
+
+// One workgroup per (head, segment).
+static __global__ __launch_bounds__(kGradThreads) void decay_grad_kernel(DecayGradArgs a) {
+  __shared__ double part[kGradThreads / 64], tx[kMaxChunks], ty[kMaxChunks], carry[kMaxChunks];
   const int bh = blockIdx.x / a.s.nseg, seg = blockIdx.x % a.s.nseg;
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
   const bool end = seg == a.s.nseg - 1;
-  const float* X = end ? (a.dS ? a.dS + (size_t)bh * a.N : nullptr)
-                       : a.X + ((size_t)bh * a.s.nseg + seg) * a.N;
-  double acc = 0.0;
-  if (X) {
-    const float* S = a.S + ((size_t)bh * (a.s.nseg + 1) + seg + 1) * a.N;
-    for (int i = threadIdx.x * 4; i < a.N; i += NTHR * 4) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(S + i), v = *reinterpret_cast<const f32x4*>(X + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc += (double)u[e] * (double)v[e];
+  const size_t row0 = ((size_t)bh * a.s.nc + c0) * C, tok0 = (size_t)bh * a.L;
+  const float* S = a.S + (size_t)bh * (a.s.nseg + 1) * a.N;
+  const float* X = a.X + (size_t)bh * a.s.nseg * a.N;
+  // The reversed walk's states are gradients of the state after the token
+  // behind them; that token's decay stands between.
+  const auto first_decay = [&](int c) { return (double)exp2_hw((float)log2_decay(a.g[tok0 + (size_t)c * C])); };
+
+  // <state that leaves the segment, its gradient>, and the same at its start
+  // (nothing is known there only if S0 is given and dS0 not asked for).
+  double held = 0.0, enter = 0.0;
+  bool known = true;
+  if (end) {
+    if (a.dS) held = dot_states(S + (size_t)a.s.nseg * a.N, a.dS + (size_t)bh * a.N, a.N, part);
+  } else {
+    held = dot_states(S + (size_t)(seg + 1) * a.N, X + (size_t)seg * a.N, a.N, part) * first_decay(c1);
+  }
+  if (seg > 0) {
+    enter = dot_states(S + (size_t)seg * a.N, X + (size_t)(seg - 1) * a.N, a.N, part) * first_decay(c0);
+  } else if (a.S0) {
+    known = a.dS0 != nullptr;
+    if (known) enter = dot_states(a.S0 + (size_t)bh * a.N, a.dS0 + (size_t)bh * a.N, a.N, part);
+  }
+
+  for (int i = w; i < n; i += kGradThreads / 64) {
+    const size_t at = row0 + (size_t)i * C + l;
+    const double x = wave_scan(a.x[at]), y = wave_scan(a.y[at]);
+    if (l == 63) tx[i] = x, ty[i] = y;
+  }
+  __syncthreads();
+  // carry[i]: <state that leaves chunk i, its gradient>, from the segment's
+  // end: held + sum over later chunks of x - y; then the correction.
+  if (w == 0) {
+    double run = held, passed = 0.0;  // uniform over the wave
+    for (int hi = n; hi > 0; hi -= 64) {
+      const int i = hi - 1 - l;  // lane 0: the last chunk
+      const bool on = i >= 0;
+      const double x = on ? tx[i] : 0.0, y = on ? ty[i] : 0.0;
+      const double d = wave_scan(x - y), v = wave_scan(x * x + y * y);
+      if (on) {
+        carry[i] = run + d - (x - y);
+        tx[i] = passed + v - (x * x + y * y);  // squares passed from the end to here
+      }
+      run += lane_value(d, 63);
+      passed += lane_value(v, 63);
+    }
+    if (known && passed > 0.0) {
+      const double off = (enter - run) / passed;
+      for (int i = l; i < n; i += 64) carry[i] += off * tx[i];
     }
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
-  if (l == 0) part[w] = acc;
   __syncthreads();
-  // <state that leaves the chunk at hand, its gradient>
-  double held = (part[0] + part[1]) + (part[2] + part[3]);
-  const int c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc);
-  // (The reversed walk's states are gradients of the state after a segment's
-  // first token; the decay in front of that token stands between.)
-  if (!end) held *= exp2_hw((float)log2_decay(a.g[(size_t)bh * a.L + c1 * C]));
-  for (int top = c1; top > c0; top -= 4) {
-    const int c = top - 1 - w;  // wave 0 takes the last chunk
-    const bool on = c >= c0;
-    const size_t at = ((size_t)bh * a.s.nc + (on ? c : c0)) * C + l;
-    const double x = on ? a.x[at] : 0.0, y = on ? a.y[at] : 0.0, m = on ? a.m[at] : 0.0;
-    const double sx = wave_scan(x + m), sy = wave_scan(y);
-    double ax = x;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) ax += __shfl_xor(ax, off, 64);
-    const double all = __shfl(sx, 63, 64), ay = __shfl(sy, 63, 64);
-    __syncthreads();  // the previous round's totals are read
-    if (l == 0) tx[w] = ax, ty[w] = ay;
-    __syncthreads();
-    double D = held;
-    for (int i = 0; i < 4; ++i) {
-      D -= ty[i];
-      if (i == w) break;
-      D += tx[i];
-    }
-    for (int i = 0; i < 4; ++i) held += tx[i] - ty[i];
-    const int t = c * C + l;
-    if (on && t < a.L) {
-      const size_t i = (size_t)bh * a.L + t;
-      const double v = (all - sx + x + m) + (sy - y) + D;
-      a.dg[i] = log2_decay(a.g[i]) <= kWipe2 ? 0.f : (float)v;
-    }
+  for (int i = w; i < n; i += kGradThreads / 64) {
+    const size_t at = row0 + (size_t)i * C + l;
+    const int t = (c0 + i) * C + l;
+    const double x = (double)a.x[at] + (double)a.m[at], y = a.y[at];
+    const double sx = wave_scan(x), sy = wave_scan(y);
+    // sum_{r >= t} (x_r + m_r) - sum_{i >= t} y_i + <the state that leaves>
+    const double v = (lane_value(sx, 63) - sx + x) - (lane_value(sy, 63) - sy + y) + carry[i];
+    if (t < a.L) a.dg[tok0 + t] = log2_decay(a.g[tok0 + t]) <= kWipe2 ? 0.f : (float)v;
   }
 }
 
@@ -179,9 +215,9 @@ static hipError_t backward(const LinearBwdArgs& a) {
     }
   }
   if (!a.dlog_decay) return hipSuccess;
-  DecayGradArgs g{a.log_decay, f(o.x), f(o.y), f(o.m), f(o.S), f(o.X), a.dS_final, a.dlog_decay, a.L, BH, N, s};
+  DecayGradArgs g{a.log_decay, f(o.x), f(o.y), f(o.m), f(o.S), f(o.X), a.S0, a.dS0, a.dS_final, a.dlog_decay, a.L, BH, N, s};
   prof_mark(kSlotLinearBwd, false, a.stream);
-  hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(BH * s.nseg)), dim3(NTHR), 0, a.stream, g);
+  hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(BH * s.nseg)), dim3(kGradThreads), 0, a.stream, g);
   e = hipGetLastError();
   prof_mark(kSlotLinearBwd, true, a.stream);
   return e;
