@@ -27,13 +27,13 @@
 // the state entering every segment, and the output kernel walks each segment
 // from there.  With one segment the output kernel runs alone.
 //
-// Output kernel: 4 waves; wave w owns DV / 4 columns of the state, which stay
+// Output kernel: wave w owns 16 columns of the state, which stay
 // in fp32 MFMA accumulators for the whole segment and never pass through LDS:
 // the accumulator layout of two stacked 16 x 16 tiles is the operand layout
 // of the next product (the "d4" slot order of dn_mfma.h), so Q S takes the
 // state straight from the accumulators.  Outputs are formed as transposed
 // tiles (S^T Q^T + V^T P^T): a lane then holds 4 consecutive columns of one
-// row.  P is formed once per workgroup (10 tiles over the 4 waves) and passed
+// row.  P is formed once per workgroup (10 tiles over its waves) and passed
 // through LDS as operand fragments.
 //
 // Precision.  bf16 q, k, v (and dO) enter products as they are.  An fp32
@@ -60,8 +60,9 @@
 namespace dn {
 namespace lin {
 
-constexpr int C = 64;       // rows of a chunk
-constexpr int NTHR = 256;   // 4 waves
+constexpr int C = 64;  // rows of a chunk
+// Waves of a workgroup: each owns 16 columns of the state.
+__host__ __device__ constexpr int waves(int DV) { return DV / 16; }
 constexpr double kLog2e = 1.4426950408889634074;
 // Log decays (base 2) are floored here: 2^-220 is zero in fp32, so a wipe
 // (-inf) is exact and differences of sums stay finite.
@@ -113,8 +114,7 @@ struct Tile<bf16, D> {
   static __device__ __forceinline__ int swizzle(int row) { return kswz<D>(row); }
   __device__ __forceinline__ uint16_t* e(int off) const { return reinterpret_cast<uint16_t*>(p) + off; }
   // Row r0 + i, contraction over elements 32 kb ..
-  __device__ __forceinline__ Frag row(int r0, int kb) const {
-    const int l = threadIdx.x & 63;
+  __device__ __forceinline__ Frag row(int r0, int kb, int l) const {
     return as_bf16x8(*reinterpret_cast<const uint4*>(e(koff<D>(r0 + (l & 15), 4 * kb + (l >> 4)))));
   }
   __device__ __forceinline__ uint2 tr(int off) const {
@@ -123,18 +123,17 @@ struct Tile<bf16, D> {
   // Column c(i), contraction over rows 32 tb .. (transposing reads: lane
   // 4 m + a of a 16-lane group addresses row m, 4 columns; lane 4 a + b receives
   // its column b of every row).
-  __device__ __forceinline__ Frag cols(int piece, int half, int tb) const {
-    const int l = threadIdx.x & 63, r = 32 * tb + 4 * (l >> 4) + ((l & 15) >> 2);
+  __device__ __forceinline__ Frag cols(int piece, int half, int tb, int l) const {
+    const int r = 32 * tb + 4 * (l >> 4) + ((l & 15) >> 2);
     return as_bf16x8(tr(koff<D>(r, piece) + 4 * half), tr(koff<D>(r + 16, piece) + 4 * half));
   }
   // ... of adjacent columns c0 + i.
-  __device__ __forceinline__ Frag col(int c0, int tb) const {
-    const int a = threadIdx.x & 3;
-    return cols((c0 >> 3) + (a >> 1), a & 1, tb);
+  __device__ __forceinline__ Frag col(int c0, int tb, int l) const {
+    return cols((c0 >> 3) + ((l & 3) >> 1), l & 1, tb, l);
   }
   // ... of the columns that are the state's rows in accumulator tile kt.
-  __device__ __forceinline__ Frag state_col(int kt, int tb) const {
-    return cols(4 * (kt >> 1) + (threadIdx.x & 3), kt & 1, tb);
+  __device__ __forceinline__ Frag state_col(int kt, int tb, int l) const {
+    return cols(4 * (kt >> 1) + (l & 3), kt & 1, tb, l);
   }
 };
 
@@ -149,14 +148,14 @@ struct Tile<float, D> {
   }
   __device__ __forceinline__ float* e(int off) const { return reinterpret_cast<float*>(p) + off; }
   __device__ __forceinline__ static int off(int row, int c) { return row * D + (((c >> 2) ^ swizzle(row)) << 2) + (c & 3); }
-  __device__ __forceinline__ Frag row(int r0, int kb) const {
-    const int l = threadIdx.x & 63, r = r0 + (l & 15), c = 32 * kb + 8 * (l >> 4);
+  __device__ __forceinline__ Frag row(int r0, int kb, int l) const {
+    const int r = r0 + (l & 15), c = 32 * kb + 8 * (l >> 4);
     const f32x4 a = *reinterpret_cast<const f32x4*>(e(off(r, c)));
     const f32x4 b = *reinterpret_cast<const f32x4*>(e(off(r, c + 4)));
     return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
   }
-  __device__ __forceinline__ Frag at_col(int c, int tb) const {
-    const int r = 32 * tb + 4 * ((threadIdx.x & 63) >> 4);
+  __device__ __forceinline__ Frag at_col(int c, int tb, int l) const {
+    const int r = 32 * tb + 4 * (l >> 4);
     Frag f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -165,10 +164,10 @@ struct Tile<float, D> {
     }
     return f;
   }
-  __device__ __forceinline__ Frag col(int c0, int tb) const { return at_col(c0 + (threadIdx.x & 15), tb); }
-  __device__ __forceinline__ Frag state_col(int kt, int tb) const {
-    const int i = threadIdx.x & 15;
-    return at_col(state_row(kt, i >> 2) + (i & 3), tb);
+  __device__ __forceinline__ Frag col(int c0, int tb, int l) const { return at_col(c0 + (l & 15), tb, l); }
+  __device__ __forceinline__ Frag state_col(int kt, int tb, int l) const {
+    const int i = l & 15;
+    return at_col(state_row(kt, i >> 2) + (i & 3), tb, l);
   }
 };
 
@@ -335,20 +334,21 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// A chunk's rows of one tensor on their way to an LDS tile: wave w fills rows
-// 16 w .. + 15, a wave's lanes 64 adjacent pieces of LDS at a time; each lane
+// A chunk's rows of one tensor on their way to an LDS tile: each of NW waves
+// fills C / NW rows, its lanes 64 adjacent pieces of LDS at a time; each lane
 // fetches the piece that the swizzle puts there.
-template <typename IT, int D, bool REV>
+template <typename IT, int D, int NW, bool REV>
 struct Stage {
   typedef Tile<IT, D> T;
-  static constexpr int N = C * T::PPR / NTHR;  // pieces per lane
-  static constexpr int RPI = 64 / T::PPR;      // rows per 64 pieces
+  static constexpr int N = C * T::PPR / (64 * NW);  // pieces per lane
+  static constexpr int RPI = 64 / T::PPR;           // rows per 64 pieces
+  static_assert(N * RPI * NW == C, "whole rows per wave");
   uint32_t voff[N];
   __device__ __forceinline__ Stage() {
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = (C / 4) * w + i * RPI + l / T::PPR, piece = (l % T::PPR) ^ T::swizzle(row);
+      const int row = (C / NW) * w + i * RPI + l / T::PPR, piece = (l % T::PPR) ^ T::swizzle(row);
       voff[i] = (uint32_t)((REV ? C - 1 - row : row) * D * (int)sizeof(IT) + piece * 16);
     }
   }
@@ -361,7 +361,7 @@ struct Stage {
     r[1] = __builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffff;
     r[2] = __builtin_amdgcn_readfirstlane(rows * D * (int)sizeof(IT));
     r[3] = 0x00020000;
-    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(lds_address(t.p) + (threadIdx.x >> 6) * (T::bytes / 4)));
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(lds_address(t.p) + (threadIdx.x >> 6) * (T::bytes / NW)));
 #pragma unroll
     for (int i = 0; i < N; ++i) load_to_lds(r, voff[i], lds + i * 1024);
   }
@@ -427,93 +427,80 @@ struct StateArgs {
   Split s;
 };
 
-// S += K^T diag(up) V after S *= total, on this wave's columns.
-template <typename IT, int DK, int DV>
-__device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16][DV / 64], Tile<IT, DK> K,
-                                             const typename Tile<IT, DV>::Frag (&vf)[C / 32][DV / 64],
-                                             const Decays* d) {
-  constexpr int CT = DV / 64;
-  const int g = (threadIdx.x & 63) >> 4;
+// S = total S + K^T diag(up) V on this wave's columns.
+template <typename IT, int DK>
+__device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> K,
+                                             const typename Tile<IT, 64>::Frag (&vf)[C / 32], const Decays* d, int l) {
+  const int g = l >> 4;
   const float total = d->total;
 #pragma unroll
-  for (int kt = 0; kt < DK / 16; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) st[kt][ct] *= total;
+  for (int kt = 0; kt < DK / 16; ++kt) st[kt] *= total;
 #pragma unroll
   for (int tb = 0; tb < C / 32; ++tb) {
     const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d->up[32 * tb + 4 * g]);
     const f32x4 u1 = *reinterpret_cast<const f32x4*>(&d->up[32 * tb + 16 + 4 * g]);
-    Made<IT, 3> y[CT];
+    float x[8];
+    to_floats(vf[tb], x);
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      float x[8];
-      to_floats(vf[tb][ct], x);
+    for (int e = 0; e < 4; ++e) x[e] *= u0[e], x[4 + e] *= u1[e];
+    const Made<IT, 3> y(x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] *= u0[e], x[4 + e] *= u1[e];
-      y[ct] = Made<IT, 3>(x);
-    }
-#pragma unroll
-    for (int kt = 0; kt < DK / 16; ++kt) {
-      const auto a = K.state_col(kt, tb);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) st[kt][ct] = mma(a, y[ct], st[kt][ct]);
-    }
+    for (int kt = 0; kt < DK / 16; ++kt) st[kt] = mma(K.state_col(kt, tb, l), y, st[kt]);
   }
 }
 
 // fp32 state (row-major [DK][DV], or [DV][DK] when TRANS) <-> this wave's
 // accumulators: rows state_row() + e, column j.
 template <int DK, int DV, bool TRANS>
-__device__ __forceinline__ void load_state(f32x4 (&st)[DK / 16][DV / 64], const float* S) {
-  const int l = threadIdx.x & 63, g = l >> 4, w = threadIdx.x >> 6;
+__device__ __forceinline__ void load_state(f32x4 (&st)[DK / 16], const float* S) {
+  const int l = threadIdx.x & 63, g = l >> 4, j = (threadIdx.x >> 6) * 16 + (l & 15);
 #pragma unroll
-  for (int kt = 0; kt < DK / 16; ++kt)
+  for (int kt = 0; kt < DK / 16; ++kt) {
+    const int k0 = state_row(kt, g);
+    if (!S) {
+      st[kt] = zero4();
+    } else if (TRANS) {
+      st[kt] = *reinterpret_cast<const f32x4*>(S + (size_t)j * DK + k0);
+    } else {
 #pragma unroll
-    for (int ct = 0; ct < DV / 64; ++ct) {
-      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = state_row(kt, g);
-      if (!S) {
-        st[kt][ct] = zero4();
-      } else if (TRANS) {
-        st[kt][ct] = *reinterpret_cast<const f32x4*>(S + (size_t)j * DK + k0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st[kt][ct][e] = S[(size_t)(k0 + e) * DV + j];
-      }
+      for (int e = 0; e < 4; ++e) st[kt][e] = S[(size_t)(k0 + e) * DV + j];
     }
+  }
 }
 template <int DK, int DV, bool TRANS>
-__device__ __forceinline__ void store_state(const f32x4 (&st)[DK / 16][DV / 64], float* S, float scale) {
-  const int l = threadIdx.x & 63, g = l >> 4, w = threadIdx.x >> 6;
+__device__ __forceinline__ void store_state(const f32x4 (&st)[DK / 16], float* S, float scale) {
+  const int l = threadIdx.x & 63, g = l >> 4, j = (threadIdx.x >> 6) * 16 + (l & 15);
 #pragma unroll
-  for (int kt = 0; kt < DK / 16; ++kt)
+  for (int kt = 0; kt < DK / 16; ++kt) {
+    const int k0 = state_row(kt, g);
+    const f32x4 x = st[kt] * scale;
+    if (TRANS) {
+      *reinterpret_cast<f32x4*>(S + (size_t)j * DK + k0) = x;
+    } else {
 #pragma unroll
-    for (int ct = 0; ct < DV / 64; ++ct) {
-      const int j = w * (DV / 4) + 16 * ct + (l & 15), k0 = state_row(kt, g);
-      const f32x4 x = st[kt][ct] * scale;
-      if (TRANS) {
-        *reinterpret_cast<f32x4*>(S + (size_t)j * DK + k0) = x;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[(size_t)(k0 + e) * DV + j] = x[e];
-      }
+      for (int e = 0; e < 4; ++e) S[(size_t)(k0 + e) * DV + j] = x[e];
     }
+  }
 }
 
 template <typename IT, int DV>
-__device__ __forceinline__ void value_frags(typename Tile<IT, DV>::Frag (&vf)[C / 32][DV / 64], Tile<IT, DV> V) {
-  const int w = threadIdx.x >> 6;
+__device__ __forceinline__ void value_frags(typename Tile<IT, DV>::Frag (&vf)[C / 32], Tile<IT, DV> V, int w, int l) {
 #pragma unroll
-  for (int tb = 0; tb < C / 32; ++tb)
-#pragma unroll
-    for (int ct = 0; ct < DV / 64; ++ct) vf[tb][ct] = V.col(w * (DV / 4) + 16 * ct, tb);
+  for (int tb = 0; tb < C / 32; ++tb) vf[tb] = V.col(w * 16, tb, l);
 }
+
+// Waves per SIMD to compile for: two workgroups per CU with bf16 tiles, one
+// with fp32 tiles.
+template <typename IT>
+__host__ __device__ constexpr int simd_waves(int DV) { return waves(DV) / 4 * (sizeof(IT) == 2 ? 2 : 1); }
 
 // Two sets of tiles: a chunk's rows arrive while the one before is used.
 template <typename IT, int DK, int DV>
 constexpr int state_lds() { return 2 * (Tile<IT, DK>::bytes + Tile<IT, DV>::bytes + (int)sizeof(Decays)); }
 
 template <typename IT, int DK, int DV, bool REV>
-__global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void state_kernel(StateArgs a) {
+__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void state_kernel(StateArgs a) {
+  constexpr int NW = waves(DV);
   constexpr int TB = Tile<IT, DK>::bytes + Tile<IT, DV>::bytes;
   extern __shared__ __align__(16) unsigned char smem[];
   Decays* const tables = reinterpret_cast<Decays*>(smem + 2 * TB);
@@ -527,12 +514,12 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void state_kernel(St
   const float* g = a.g ? a.g + (size_t)bh * L : nullptr;
   const int n = c1 - c0;
   auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
-  const bool tables_wave = threadIdx.x >= NTHR - 64;
+  const bool tables_wave = threadIdx.x >= 64 * NW - 64;
 
-  f32x4 st[DK / 16][DV / 64];
+  f32x4 st[DK / 16];
   load_state<DK, DV, false>(st, nullptr);
-  const Stage<IT, DK, REV> sk;
-  const Stage<IT, DV, REV> sv;
+  const Stage<IT, DK, NW, REV> sk;
+  const Stage<IT, DV, NW, REV> sv;
   auto load = [&](int i) {
     unsigned char* const at = smem + (i & 1) * TB;
     sk.load(k, chunk(i), L, Tile<IT, DK>{at});
@@ -550,13 +537,13 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void state_kernel(St
       load(i + 1);
     }
     unsigned char* const at = smem + (i & 1) * TB;
-    typename Tile<IT, DV>::Frag vf[C / 32][DV / 64];
-    value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes});
-    update_state<IT, DK, DV>(st, Tile<IT, DK>{at}, vf, &tables[i & 1]);
+    typename Tile<IT, DV>::Frag vf[C / 32];
+    value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes}, threadIdx.x >> 6, threadIdx.x & 63);
+    update_state<IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], threadIdx.x & 63);
     if (i + 1 < n && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
   }
   store_state<DK, DV, false>(st, a.states + ((size_t)bh * a.slots + seg) * (DK * DV), 1.f);
-  if (threadIdx.x == NTHR - 1) a.decays[(size_t)bh * a.s.nseg + seg] = sum;
+  if (threadIdx.x == 64 * NW - 1) a.decays[(size_t)bh * a.s.nseg + seg] = sum;
 }
 
 // ---- the combine kernel --------------------------------------------------------------
@@ -625,49 +612,56 @@ struct OutArgs {
 };
 
 // P's lower triangle as operand fragments (columns: output rows; contraction:
-// key rows): fragment (rt, kb), kb <= rt / 2, holds key tiles 2 kb, 2 kb + 1.
-__host__ __device__ constexpr int pfrag(int rt, int kb) { return (rt >> 1) * ((rt >> 1) + 1) + (rt & 1) * ((rt >> 1) + 1) + kb; }
-constexpr int kPFrags = 6;
-static_assert(pfrag(0, 0) == 0 && pfrag(1, 0) == 1 && pfrag(2, 0) == 2 && pfrag(2, 1) == 3 &&
-              pfrag(3, 0) == 4 && pfrag(3, 1) == 5, "six fragments");
+// key rows): fragment (rt, kb), kb <= rt / 2, holds key tiles 2 kb and 2 kb + 1;
+// of fragments (0, 0) and (2, 1) the second is above the diagonal, and absent.
+// at(): units of a half fragment before it.
+__host__ __device__ constexpr int pat(int rt, int kb) {
+  return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? (kb ? 5 : 3) : (kb ? 8 : 6);
+}
+__host__ __device__ constexpr bool pwhole(int rt, int kb) { return 2 * kb + 1 <= rt; }
 
 template <typename IT, int NS>
 struct PBuf;
 template <int NS>
 struct PBuf<bf16, NS> {
-  static constexpr int bytes = kPFrags * NS * 64 * 16;
+  static constexpr int plane = 10 * 512;
+  static constexpr int bytes = NS * plane;
   unsigned char* p;
-  __device__ __forceinline__ uint2* at(int f, int s, int half) const {
-    return reinterpret_cast<uint2*>(p + ((f * NS + s) * 64 + (threadIdx.x & 63)) * 16) + half;
-  }
-  __device__ __forceinline__ void put(int f, int half, f32x4 x) const {
+  __device__ __forceinline__ void put(int rt, int it, f32x4 x, int l) const {
+    const int kb = it >> 1;
+    unsigned char* const at = p + pat(rt, kb) * 512 + (pwhole(rt, kb) ? l * 16 + (it & 1) * 8 : l * 8);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       uint2 u = make_uint2(pack_once(x[0], x[1]), pack_once(x[2], x[3]));
-      *at(f, s, half) = u;
-      x[0] -= __uint_as_float(u.x << 16);
-      x[1] -= __uint_as_float(u.x & 0xffff0000u);
-      x[2] -= __uint_as_float(u.y << 16);
-      x[3] -= __uint_as_float(u.y & 0xffff0000u);
+      *reinterpret_cast<uint2*>(at + s * plane) = u;
+      if (s + 1 < NS) {
+        x[0] -= __uint_as_float(u.x << 16);
+        x[1] -= __uint_as_float(u.x & 0xffff0000u);
+        x[2] -= __uint_as_float(u.y << 16);
+        x[3] -= __uint_as_float(u.y & 0xffff0000u);
+      }
     }
   }
-  __device__ __forceinline__ Made<bf16, NS> get(int f) const {
+  __device__ __forceinline__ Made<bf16, NS> get(int rt, int kb, int l) const {
+    const unsigned char* const at = p + pat(rt, kb) * 512;
     Made<bf16, NS> m;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) m.p[s] = as_bf16x8(*reinterpret_cast<const uint4*>(at(f, s, 0)));
+    for (int s = 0; s < NS; ++s)
+      m.p[s] = pwhole(rt, kb) ? as_bf16x8(*reinterpret_cast<const uint4*>(at + s * plane + l * 16))
+                              : as_bf16x8(*reinterpret_cast<const uint2*>(at + s * plane + l * 8), make_uint2(0, 0));
     return m;
   }
 };
 template <int NS>
 struct PBuf<float, NS> {
-  static constexpr int bytes = kPFrags * 64 * 32;
+  static constexpr int bytes = 10 * 1024;
   unsigned char* p;
-  __device__ __forceinline__ f32x4* at(int f, int half) const {
-    return reinterpret_cast<f32x4*>(p + (f * 2 + half) * 1024) + (threadIdx.x & 63);
+  __device__ __forceinline__ f32x4* at(int rt, int kb, int half, int l) const {
+    return reinterpret_cast<f32x4*>(p + (pat(rt, kb) + half) * 1024) + l;
   }
-  __device__ __forceinline__ void put(int f, int half, f32x4 x) const { *at(f, half) = x; }
-  __device__ __forceinline__ Made<float, NS> get(int f) const {
-    const f32x4 a = *at(f, 0), b = *at(f, 1);
+  __device__ __forceinline__ void put(int rt, int it, f32x4 x, int l) const { *at(rt, it >> 1, it & 1, l) = x; }
+  __device__ __forceinline__ Made<float, NS> get(int rt, int kb, int l) const {
+    const f32x4 a = *at(rt, kb, 0, l), b = pwhole(rt, kb) ? *at(rt, kb, 1, l) : zero4();
     Made<float, NS> m;
     m.p = F32x8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
     return m;
@@ -676,8 +670,9 @@ struct PBuf<float, NS> {
 
 // Sums for the decay's gradient, gathered per chunk without atomics: every
 // writer has a slot of its own.
+template <int NW>
 struct Sums {
-  float dots[4][C];   // by wave
+  float dots[NW][C];  // by wave
   float out[10][16];  // pair terms of an output tile's rows, by tile of P
   float key[10][16];  // ... of a key tile's rows
 };
@@ -716,7 +711,7 @@ struct OutLds {
   static constexpr int P = 4 * tile;
   static constexpr int D = P + PBuf<IT, NSP>::bytes;
   static constexpr int S = D + 2 * (int)sizeof(Decays);
-  static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums) : 0);
+  static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums<waves(DV)>) : 0);
 };
 
 // Four adjacent elements of a row of w straight from HBM (rows past the end
@@ -726,27 +721,27 @@ struct Four;
 template <>
 struct Four<float> {
   f32x4 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = __builtin_bit_cast(f32x4, bload16(r, at, 0)); }
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at, uint32_t more) { x = __builtin_bit_cast(f32x4, bload16(r, at, more)); }
   __device__ __forceinline__ f32x4 get() const { return x; }
 };
 template <>
 struct Four<bf16> {
   uint2 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = bload8(r, at, 0); }
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at, uint32_t more) { x = bload8(r, at, more); }
   __device__ __forceinline__ f32x4 get() const {
     return f32x4{__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
                  __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u)};
   }
 };
 template <typename IT, int D>
-__device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row, int kb) {
-  const uint32_t at = (uint32_t)(row * D + 32 * kb + 8 * ((threadIdx.x & 63) >> 4)) * sizeof(IT);
+__device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row, int kb, int lane) {
+  const uint32_t at = (uint32_t)(row * D + 32 * kb + 8 * (lane >> 4)) * sizeof(IT);
   if constexpr (sizeof(IT) == 2) {
     return as_bf16x8(bload16(r, at, 0));
   } else {
     Four<float> a, b;
-    a.load(r, at);
-    b.load(r, at + 16);
+    a.load(r, at, 0);
+    b.load(r, at + 16, 0);
     return F32x8{{a.x[0], a.x[1], a.x[2], a.x[3], b.x[0], b.x[1], b.x[2], b.x[3]}};
   }
 }
@@ -757,16 +752,16 @@ __device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row
 // Four tile buffers suffice: the next Q goes where V was a chunk ago, the next
 // K where Q is no longer read, the next V where K is no longer read.
 template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
-__global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutArgs a) {
+__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel(OutArgs a) {
   using LD = OutLds<IT, OT, DK, DV, EXTRA>;
-  constexpr int NRT = C / 16, CT = DV / 64, NSP = LD::NSP, NSS = LD::NSS;
+  constexpr int NW = waves(DV), NRT = C / 16, NSP = LD::NSP, NSS = LD::NSS;
   constexpr bool TRANS = EXTRA != kNone;  // dq and dk walk the transposed state
   typedef Tile<IT, DK> TK;
   typedef Tile<IT, DV> TV;
   extern __shared__ __align__(16) unsigned char smem[];
   const PBuf<IT, NSP> P{smem + LD::P};
   Decays* const tables = reinterpret_cast<Decays*>(smem + LD::D);
-  Sums* const sums = reinterpret_cast<Sums*>(smem + LD::S);
+  Sums<NW>* const sums = reinterpret_cast<Sums<NW>*>(smem + LD::S);
 
   int bh, seg;
   if (!item_of(blockIdx.x, a.BH, a.grp, a.s.nseg, bh, seg)) return;
@@ -777,29 +772,27 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
   const IT* wp = EXTRA != kNone ? a.w.head<IT>(bh, L, DV) : nullptr;
   const float* g = a.g ? a.g + (size_t)bh * L : nullptr;
   OT* out = static_cast<OT*>(a.out) + (size_t)bh * L * DV;
-  const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
 
-  // This wave's tiles of P (output tile rt, key tile it <= rt), 10 over 4
-  // waves: two of one rt, and on waves 2 and 3 a third, so that the decay
-  // table's wave (1) has time for it.
-  //   wave 0: (3,0) (3,1)   1: (3,2) (3,3)   2: (2,0) (2,1) (2,2)   3: (1,0) (1,1) (0,0)
-  const int prt = w < 2 ? 3 : w == 2 ? 2 : 1, pit = w == 1 ? 2 : 0;
-  const int prt2 = w == 2 ? 2 : 0, pit2 = w == 2 ? 2 : 0;
-  const bool third = w >= 2;
-  constexpr int kTableWave = 1;
-  // The tiles above the diagonal that share a fragment with one below.
-  if (w == 0) P.put(pfrag(0, 0), 1, zero4());
-  if (w == 1) P.put(pfrag(2, 1), 1, zero4());
+  // This wave's tiles of P (output tile rt, key tile it <= rt), 10 over the
+  // waves: NA adjacent ones of one rt, and on two waves one more; the decay
+  // table's wave is not one of those.
+  //   8 waves: (3,0) (3,1) (3,2) (3,3) (2,0) (2,1) (2,2)+(0,0) (1,0)+(1,1)
+  //   4 waves: (3,0)(3,1)  (3,2)(3,3)  (2,0)(2,1)+(2,2)  (1,0)(1,1)+(0,0)
+  constexpr int NA = NW == 8 ? 1 : 2, kTableWave = 1;
+  const int prt = NW == 8 ? (w < 4 ? 3 : w < 7 ? 2 : 1) : (w < 2 ? 3 : w == 2 ? 2 : 1);
+  const int pit = NW == 8 ? (w < 4 ? w : w < 7 ? w - 4 : 0) : (w == 1 ? 2 : 0);
+  const bool more_p = w >= NW - 2;
+  const int prt2 = NW == 8 ? (w == 7 ? 1 : 0) : (w == 2 ? 2 : 0), pit2 = prt2;
 
-  const Stage<IT, DK, REV> sk;
-  const Stage<IT, DV, REV> sv;
+  const Stage<IT, DK, NW, REV> sk;
+  const Stage<IT, DV, NW, REV> sv;
   unsigned char *bq = smem, *bk = smem + LD::tile, *bv = smem + 2 * LD::tile, *bf = smem + 3 * LD::tile;
   sk.load(q, chunk(0), L, TK{bq});
   sk.load(k, chunk(0), L, TK{bk});
   if (w == kTableWave) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
-  f32x4 st[DK / 16][CT];
+  f32x4 st[DK / 16];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
   load_state<DK, DV, TRANS>(st, S);
@@ -808,6 +801,7 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
 
   // A chunk's pair sums, once every wave has left its own.
   auto store_pairs = [&](int c) {
+    const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
     float y = 0.f;
     for (int x = 0; x < NRT; ++x) {
       if (x <= lg) y += sums->out[tri(lg, x)][li];
@@ -819,161 +813,153 @@ __global__ __launch_bounds__(NTHR, sizeof(IT) == 2 ? 2 : 1) void out_kernel(OutA
   for (int ci = 0; ci < n; ++ci) {
     const int c = chunk(ci);
     const bool more = ci + 1 < n;
+    // (kPairs: addresses are formed anew in each chunk.  Kept over the loop they
+    // do not fit beside the state, and a reload from scratch memory waits for
+    // every row on its way.)
+    int lane = threadIdx.x & 63;
+    if (EXTRA == kPairs) asm volatile("" : "+v"(lane));
+    const int lg = lane >> 4, li = lane & 15;
     const Decays* dec = &tables[ci & 1];
     const TK Q{bq}, K{bk};
     const TV V{bv};
     rsrc_t wr;
-    Four<IT> wd[NRT][CT];
+    Four<IT> wd[NRT];
     auto w_row = [&](int r) { return REV ? C - 1 - r : r; };
     if constexpr (EXTRA != kNone) {
       wr = make_rsrc(wp + (size_t)c * C * DV, (uint32_t)(min(C, L - c * C) * DV * (int)sizeof(IT)));
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          wd[rt][ct].load(wr, (uint32_t)(w_row(16 * rt + li) * DV + w * (DV / 4) + 16 * ct + 4 * lg) * sizeof(IT));
+        wd[rt].load(wr, (uint32_t)((REV ? 15 - li : li) * DV + w * 16 + 4 * lg) * sizeof(IT),
+                    16 * (REV ? NRT - 1 - rt : rt) * DV * sizeof(IT));
     }
     sv.load(v, c, L, V);
     if (more) sk.load(q, chunk(ci + 1), L, TK{bf});
     float gn = 0.f;
     if (w == kTableWave && more) gn = load_decay<REV>(g, chunk(ci + 1), L);
-    typename TV::Frag wf[EXTRA == kPairs ? DV / 32 : 1];
-    if constexpr (EXTRA == kPairs) {
-#pragma unroll
-      for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb);
-    }
     if (EXTRA == kPairs && w == 0 && ci > 0) store_pairs(chunk(ci - 1));
 
     // P^T tiles: rows are key rows 16 it + 4 lg + e, the column is output row
     // 16 rt + li.
-    f32x4 p[3] = {zero4(), zero4(), zero4()};
+    // (First, so that their way through LDS is hidden behind Q S; with the pair
+    // terms' fragments they come second, which leaves registers for both.)
+    f32x4 p[NA + 1];
+    auto make_p = [&] {
 #pragma unroll
-    for (int kb = 0; kb < DK / 32; ++kb) {
-      const auto b = Q.row(16 * prt, kb);
-      p[0] = mma(K.row(16 * pit, kb), b, p[0]);
-      p[1] = mma(K.row(16 * pit + 16, kb), b, p[1]);
-    }
-    if (third) {
+      for (int x = 0; x <= NA; ++x) p[x] = zero4();
 #pragma unroll
-      for (int kb = 0; kb < DK / 32; ++kb) p[2] = mma(K.row(16 * pit2, kb), Q.row(16 * prt2, kb), p[2]);
-    }
-    auto decay_tile = [&](f32x4& x, int rt, int it) {
-      const int r = 16 * rt + li;
-      const double Gr = dec->G[r];
+      for (int kb = 0; kb < DK / 32; ++kb) {
+        const auto b = Q.row(16 * prt, kb, lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * it + 4 * lg + e;
-        x[e] = i <= r ? x[e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
+        for (int x = 0; x < NA; ++x) p[x] = mma(K.row(16 * (pit + x), kb, lane), b, p[x]);
       }
-      P.put(pfrag(rt, it >> 1), it & 1, x);
+      if (more_p) {
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb) p[NA] = mma(K.row(16 * pit2, kb, lane), Q.row(16 * prt2, kb, lane), p[NA]);
+      }
+      auto decay_tile = [&](f32x4& x, int rt, int it) {
+        const int r = 16 * rt + li;
+        const double Gr = dec->G[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * it + 4 * lg + e;
+          x[e] = i <= r ? x[e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
+        }
+        P.put(rt, it, x, lane);
+      };
+#pragma unroll
+      for (int x = 0; x < NA; ++x) decay_tile(p[x], prt, pit + x);
+      if (more_p) decay_tile(p[NA], prt2, pit2);
     };
-    decay_tile(p[0], prt, pit);
-    decay_tile(p[1], prt, pit + 1);
-    if (third) decay_tile(p[2], prt2, pit2);
+    if (EXTRA != kPairs) make_p();
 
     // Output tiles (rows: this wave's columns, column: row 16 rt + li), first
     // what comes from the entering state.
-    f32x4 acc[NRT][CT];
+    f32x4 acc[NRT];
 #pragma unroll
-    for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = zero4();
+    for (int rt = 0; rt < NRT; ++rt) acc[rt] = zero4();
 #pragma unroll
     for (int kb = 0; kb < DK / 32; ++kb) {
-      Made<IT, NSS> s[CT];
+      const f32x4 x = st[2 * kb], y = st[2 * kb + 1];
+      const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      const Made<IT, NSS> s(z);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const f32x4 x = st[2 * kb][ct], y = st[2 * kb + 1][ct];
-        const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        s[ct] = Made<IT, NSS>(z);
-      }
-#pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) {
-        const auto b = Q.row(16 * rt, kb);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mma(s[ct], b, acc[rt][ct]);
-      }
+      for (int rt = 0; rt < NRT; ++rt) acc[rt] = mma(s, Q.row(16 * rt, kb, lane), acc[rt]);
     }
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
-      const float f = exp2_hw((float)dec->G[16 * rt + li]);
-      float dot = 0.f;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        acc[rt][ct] *= f;
-        if constexpr (EXTRA != kNone) {
-          const f32x4 y = wd[rt][ct].get();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot += acc[rt][ct][e] * y[e];
-        }
-      }
-      if (EXTRA != kNone) {
+      acc[rt] *= exp2_hw((float)dec->G[16 * rt + li]);
+      if constexpr (EXTRA != kNone) {
+        const f32x4 y = wd[rt].get();
+        float dot = (acc[rt][0] * y[0] + acc[rt][1] * y[1]) + (acc[rt][2] * y[2] + acc[rt][3] * y[3]);
         dot = sum_groups(dot);
         if (lg == 0) sums->dots[w][16 * rt + li] = dot;
       }
     }
+    typename TV::Frag wf[EXTRA == kPairs ? DV / 32 : 1];
+    if constexpr (EXTRA == kPairs) {
+#pragma unroll
+      for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb, lane);
+    }
+    if (EXTRA == kPairs) make_p();
     wait_loads();
     __syncthreads();
 
     // ... then what comes from the chunk's own rows.
     if (more) sk.load(k, chunk(ci + 1), L, TK{bq});
-    typename TV::Frag vf[C / 32][CT];
-    value_frags<IT, DV>(vf, V);
+    if (EXTRA != kNone && w == 0) {
+      float y = 0.f;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) y += sums->dots[x][lane];
+      a.dots[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] = y;
+    }
+    if constexpr (EXTRA == kPairs) {
+      // Pair terms: P_ri (w_r . v_i), i < r.
+      auto pair_sums = [&](const f32x4& x, const f32x4& y, int rt, int it) {
+        const int i = li, g4 = 4 * lg, t = tri(rt, it);
+        float col = 0.f;
+        f32x4 row;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = it < rt || g4 + e < i ? x[e] * y[e] : 0.f;
+          col += m;
+          row[e] = sum_lanes16(m);
+        }
+        if (i == 0) *reinterpret_cast<f32x4*>(&sums->key[t][g4]) = row;
+        col = sum_groups(col);
+        if (g4 == 0) sums->out[t][i] = col;
+      };
+      f32x4 y[NA + 1];
+#pragma unroll
+      for (int x = 0; x <= NA; ++x) y[x] = zero4();
+#pragma unroll
+      for (int kb = 0; kb < DV / 32; ++kb)
+#pragma unroll
+        for (int x = 0; x < NA; ++x) y[x] = mma(V.row(16 * (pit + x), kb, lane), wf[kb], y[x]);
+      if (more_p) {
+        if (prt2 != prt) {
+#pragma unroll
+          for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb, lane);
+        }
+#pragma unroll
+        for (int kb = 0; kb < DV / 32; ++kb) y[NA] = mma(V.row(16 * pit2, kb, lane), wf[kb], y[NA]);
+        pair_sums(p[NA], y[NA], prt2, pit2);
+      }
+#pragma unroll
+      for (int x = 0; x < NA; ++x) pair_sums(p[x], y[x], prt, pit + x);
+    }
+    typename TV::Frag vf[C / 32];
+    value_frags<IT, DV>(vf, V, w, lane);
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-      for (int kb = 0; kb <= rt / 2; ++kb) {
-        const auto b = P.get(pfrag(rt, kb));
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mma(vf[kb][ct], b, acc[rt][ct]);
-      }
-    if (EXTRA != kNone && w == 0)
-      a.dots[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] =
-          (sums->dots[0][lane] + sums->dots[1][lane]) + (sums->dots[2][lane] + sums->dots[3][lane]);
-    if constexpr (EXTRA == kPairs) {
-      // Pair terms: P_ri (w_r . v_i), i < r.
-      auto pair_sums = [&](const f32x4& x, f32x4 y, int rt, int it) {
-        const int r = 16 * rt + li, t = tri(rt, it);
-        float col = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = 16 * it + 4 * lg + e < r ? x[e] * y[e] : 0.f;
-          col += m;
-          const float row = sum_lanes16(m);
-          if (li == 0) sums->key[t][4 * lg + e] = row;
-        }
-        col = sum_groups(col);
-        if (lg == 0) sums->out[t][li] = col;
-      };
-      f32x4 y[3] = {zero4(), zero4(), zero4()};
-#pragma unroll
-      for (int kb = 0; kb < DV / 32; ++kb) {
-        y[0] = mma(V.row(16 * pit, kb), wf[kb], y[0]);
-        y[1] = mma(V.row(16 * pit + 16, kb), wf[kb], y[1]);
-      }
-      if (third) {
-        if (w == 3) {
-#pragma unroll
-          for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb);
-        }
-#pragma unroll
-        for (int kb = 0; kb < DV / 32; ++kb) y[2] = mma(V.row(16 * pit2, kb), wf[kb], y[2]);
-        pair_sums(p[2], y[2], prt2, pit2);
-      }
-      pair_sums(p[0], y[0], prt, pit);
-      pair_sums(p[1], y[1], prt, pit + 1);
-    }
-    update_state<IT, DK, DV>(st, K, vf, dec);
+      for (int kb = 0; kb <= rt / 2; ++kb) acc[rt] = mma(vf[kb], P.get(rt, kb, lane), acc[rt]);
+    update_state<IT, DK>(st, K, vf, dec, lane);
     if (w == kTableWave && more) fill_decays(&tables[(ci + 1) & 1], gn);
     wait_loads();
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
       const int t = token_of<REV>(c, 16 * rt + li);
-      if (t < L) {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          store4(out + (size_t)t * DV + w * (DV / 4) + 16 * ct + 4 * lg, acc[rt][ct]);
-      }
+      if (t < L) store4(out + (size_t)t * DV + w * 16 + 4 * lg, acc[rt]);
     }
     __syncthreads();
     unsigned char* const free = bv;
@@ -1008,7 +994,7 @@ hipError_t launch_state(const StateArgs& a, hipStream_t stream) {
   hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   prof_mark(kSlotLinearState, false, stream);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.count)), dim3(NTHR), lds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.count)), dim3(64 * waves(DV)), lds, stream, a);
   e = hipGetLastError();
   prof_mark(kSlotLinearState, true, stream);
   return e;
@@ -1031,7 +1017,7 @@ hipError_t launch_out(const OutArgs& a, int slot, hipStream_t stream) {
   hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   prof_mark(slot, false, stream);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.s.nseg)), dim3(NTHR), lds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.s.nseg)), dim3(64 * waves(DV)), lds, stream, a);
   e = hipGetLastError();
   prof_mark(slot, true, stream);
   return e;
