@@ -328,10 +328,38 @@ __device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t voff, uint32_t lds
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(r) : "memory");
 }
+// Waits for all of this wave's vector memory operations.  (They end in order,
+// and the compiler does not count those issued above, so any wait of its own for
+// a load into registers waits for them too: such loads are made to arrive here,
+// by passing them through keep().)
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <typename T>
+__device__ __forceinline__ void keep(T& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void keep(F32x8& x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) keep(x.v[i]);
+}
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+// A workgroup's LDS: as a pointer, and as an address for load_to_lds().
+struct Lds {
+  unsigned char* p;
+  uint32_t at;
+};
+__device__ __forceinline__ Lds dynamic_lds() {
+  extern __shared__ __align__(16) unsigned char smem[];
+  return Lds{smem, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem};
+}
+
+// Descriptor of chunk c's rows (D elements each) of a head.
+template <typename IT, int D>
+__device__ __forceinline__ i32x4 chunk_rsrc(const IT* base, int c, int L) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base + (size_t)c * C * D);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)a);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffff;
+  r[2] = __builtin_amdgcn_readfirstlane(min(C, L - c * C) * D * (int)sizeof(IT));
+  r[3] = 0x00020000;
+  return r;
 }
 
 // A chunk's rows of one tensor on their way to an LDS tile: each of NW waves
@@ -352,16 +380,10 @@ struct Stage {
       voff[i] = (uint32_t)((REV ? C - 1 - row : row) * D * (int)sizeof(IT) + piece * 16);
     }
   }
-  // `base` is the head's first row.
-  __device__ __forceinline__ void load(const IT* base, int c, int L, T t) const {
-    const int rows = min(C, L - c * C);
-    const uint64_t a = reinterpret_cast<uint64_t>(base + (size_t)c * C * D);
-    i32x4 r;
-    r[0] = __builtin_amdgcn_readfirstlane((int)a);
-    r[1] = __builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffff;
-    r[2] = __builtin_amdgcn_readfirstlane(rows * D * (int)sizeof(IT));
-    r[3] = 0x00020000;
-    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(lds_address(t.p) + (threadIdx.x >> 6) * (T::bytes / NW)));
+  // `base` is the head's first row, `tile` the tile's address in LDS.
+  __device__ __forceinline__ void load(const IT* base, int c, int L, uint32_t tile) const {
+    const i32x4 r = chunk_rsrc<IT, D>(base, c, L);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(tile + (threadIdx.x >> 6) * (T::bytes / NW)));
 #pragma unroll
     for (int i = 0; i < N; ++i) load_to_lds(r, voff[i], lds + i * 1024);
   }
@@ -499,51 +521,63 @@ template <typename IT, int DK, int DV>
 constexpr int state_lds() { return 2 * (Tile<IT, DK>::bytes + Tile<IT, DV>::bytes + (int)sizeof(Decays)); }
 
 template <typename IT, int DK, int DV, bool REV>
-__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void state_kernel(StateArgs a) {
+__device__ __forceinline__ void state_walk(const StateArgs& a, int flat, Lds m) {
+  unsigned char* const smem = m.p;
   constexpr int NW = waves(DV);
   constexpr int TB = Tile<IT, DK>::bytes + Tile<IT, DV>::bytes;
-  extern __shared__ __align__(16) unsigned char smem[];
   Decays* const tables = reinterpret_cast<Decays*>(smem + 2 * TB);
 
   int bh, seg;
-  if (!item_of(blockIdx.x, a.BH, a.grp, a.count, bh, seg)) return;
+  if (!item_of(flat, a.BH, a.grp, a.count, bh, seg)) return;
   seg += a.first;
   const int L = a.L, c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc);
   const IT* k = a.k.head<IT>(bh, L, DK);
   const IT* v = a.v.head<IT>(bh, L, DV);
   const float* g = a.g ? a.g + (size_t)bh * L : nullptr;
-  const int n = c1 - c0;
+  const int n = c1 - c0, lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   auto chunk = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
-  const bool tables_wave = threadIdx.x >= 64 * NW - 64;
+  const bool tables_wave = w == NW - 1;
 
   f32x4 st[DK / 16];
   load_state<DK, DV, false>(st, nullptr);
   const Stage<IT, DK, NW, REV> sk;
   const Stage<IT, DV, NW, REV> sv;
   auto load = [&](int i) {
-    unsigned char* const at = smem + (i & 1) * TB;
-    sk.load(k, chunk(i), L, Tile<IT, DK>{at});
-    sv.load(v, chunk(i), L, Tile<IT, DV>{at + Tile<IT, DK>::bytes});
+    const uint32_t at = m.at + (i & 1) * TB;
+    sk.load(k, chunk(i), L, at);
+    sv.load(v, chunk(i), L, at + Tile<IT, DK>::bytes);
   };
   double sum = 0.0;
   load(0);
   if (tables_wave) sum += fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
+  wait_loads();
+  __syncthreads();
   for (int i = 0; i < n; ++i) {
-    wait_loads();
-    __syncthreads();
+    const bool more = i + 1 < n;
     float gn = 0.f;
-    if (i + 1 < n) {
-      if (tables_wave) gn = load_decay<REV>(g, chunk(i + 1), L);
+    if (more) {
+      if (tables_wave) {
+        gn = load_decay<REV>(g, chunk(i + 1), L);
+        keep(gn);
+      }
       load(i + 1);
     }
     unsigned char* const at = smem + (i & 1) * TB;
     typename Tile<IT, DV>::Frag vf[C / 32];
-    value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes}, threadIdx.x >> 6, threadIdx.x & 63);
-    update_state<IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], threadIdx.x & 63);
-    if (i + 1 < n && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
+    value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes}, w, lane);
+    update_state<IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], lane);
+    if (more && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
+    wait_loads();
+    __syncthreads();
   }
   store_state<DK, DV, false>(st, a.states + ((size_t)bh * a.slots + seg) * (DK * DV), 1.f);
   if (threadIdx.x == 64 * NW - 1) a.decays[(size_t)bh * a.s.nseg + seg] = sum;
+}
+
+template <typename IT, int DK, int DV>
+__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void state_kernel(StateArgs a) {
+  state_walk<IT, DK, DV, false>(a, blockIdx.x, dynamic_lds());
 }
 
 // ---- the combine kernel --------------------------------------------------------------
@@ -561,7 +595,7 @@ struct CombineArgs {
 };
 
 template <bool REV>
-__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+__device__ __forceinline__ void combine(const CombineArgs& a) {
   const int bh = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= a.N) return;
   float* S = a.states + (size_t)bh * a.slots * a.N + e;
@@ -587,6 +621,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int s = REV ? 0 : a.nseg - 1;
   *reinterpret_cast<f32x4*>(S + (size_t)s * a.N) = run;
 }
+
+static __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) { combine<false>(a); }
 
 // ---- the output kernel ---------------------------------------------------------------
 
@@ -747,24 +783,24 @@ __device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row
 }
 
 // A chunk takes two phases with a barrier behind each:
-//   1  P (from Q, K) and Q S;                       V arrives, and the next Q
-//   2  P V, the output, the state's update (K, V);  the next K arrives
+//   1  P (from Q, K) and Q S;                       V arrives
+//   2  P V, the output, the state's update (K, V);  the next Q and K arrive
 // Four tile buffers suffice: the next Q goes where V was a chunk ago, the next
 // K where Q is no longer read, the next V where K is no longer read.
 template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
-__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel(OutArgs a) {
+__device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
+  unsigned char* const smem = m.p;
   using LD = OutLds<IT, OT, DK, DV, EXTRA>;
   constexpr int NW = waves(DV), NRT = C / 16, NSP = LD::NSP, NSS = LD::NSS;
   constexpr bool TRANS = EXTRA != kNone;  // dq and dk walk the transposed state
   typedef Tile<IT, DK> TK;
   typedef Tile<IT, DV> TV;
-  extern __shared__ __align__(16) unsigned char smem[];
   const PBuf<IT, NSP> P{smem + LD::P};
   Decays* const tables = reinterpret_cast<Decays*>(smem + LD::D);
   Sums<NW>* const sums = reinterpret_cast<Sums<NW>*>(smem + LD::S);
 
   int bh, seg;
-  if (!item_of(blockIdx.x, a.BH, a.grp, a.s.nseg, bh, seg)) return;
+  if (!item_of(flat, a.BH, a.grp, a.s.nseg, bh, seg)) return;
   const int L = a.L, c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
   const IT* q = a.q.head<IT>(bh, L, DK);
   const IT* k = a.k.head<IT>(bh, L, DK);
@@ -778,19 +814,19 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
   // This wave's tiles of P (output tile rt, key tile it <= rt), 10 over the
   // waves: NA adjacent ones of one rt, and on two waves one more; the decay
   // table's wave is not one of those.
-  //   8 waves: (3,0) (3,1) (3,2) (3,3) (2,0) (2,1) (2,2)+(0,0) (1,0)+(1,1)
+  //   8 waves: (3,0) (3,1) (3,2) (3,3) (2,0) (0,0) (2,1)+(2,2) (1,0)+(1,1)
   //   4 waves: (3,0)(3,1)  (3,2)(3,3)  (2,0)(2,1)+(2,2)  (1,0)(1,1)+(0,0)
   constexpr int NA = NW == 8 ? 1 : 2, kTableWave = 1;
-  const int prt = NW == 8 ? (w < 4 ? 3 : w < 7 ? 2 : 1) : (w < 2 ? 3 : w == 2 ? 2 : 1);
-  const int pit = NW == 8 ? (w < 4 ? w : w < 7 ? w - 4 : 0) : (w == 1 ? 2 : 0);
-  const bool more_p = w >= NW - 2;
-  const int prt2 = NW == 8 ? (w == 7 ? 1 : 0) : (w == 2 ? 2 : 0), pit2 = prt2;
+  const int prt = NW == 8 ? (w < 4 ? 3 : w == 5 ? 0 : w == 7 ? 1 : 2) : (w < 2 ? 3 : w == 2 ? 2 : 1);
+  const int pit = NW == 8 ? (w < 4 ? w : w == 6 ? 1 : 0) : (w == 1 ? 2 : 0);
+  const bool more_p = w >= NW - 2, other = NW == 4 && w == 3;  // other: of another rt
+  const int prt2 = other ? 0 : prt, pit2 = other ? 0 : pit + NA;
 
   const Stage<IT, DK, NW, REV> sk;
   const Stage<IT, DV, NW, REV> sv;
-  unsigned char *bq = smem, *bk = smem + LD::tile, *bv = smem + 2 * LD::tile, *bf = smem + 3 * LD::tile;
-  sk.load(q, chunk(0), L, TK{bq});
-  sk.load(k, chunk(0), L, TK{bk});
+  int bq = 0, bk = LD::tile, bv = 2 * LD::tile, bf = 3 * LD::tile;
+  sk.load(q, chunk(0), L, m.at + bq);
+  sk.load(k, chunk(0), L, m.at + bk);
   if (w == kTableWave) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
   f32x4 st[DK / 16];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
@@ -820,8 +856,8 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
     if (EXTRA == kPairs) asm volatile("" : "+v"(lane));
     const int lg = lane >> 4, li = lane & 15;
     const Decays* dec = &tables[ci & 1];
-    const TK Q{bq}, K{bk};
-    const TV V{bv};
+    const TK Q{smem + bq}, K{smem + bk};
+    const TV V{smem + bv};
     rsrc_t wr;
     Four<IT> wd[NRT];
     auto w_row = [&](int r) { return REV ? C - 1 - r : r; };
@@ -832,8 +868,7 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
         wd[rt].load(wr, (uint32_t)((REV ? 15 - li : li) * DV + w * 16 + 4 * lg) * sizeof(IT),
                     16 * (REV ? NRT - 1 - rt : rt) * DV * sizeof(IT));
     }
-    sv.load(v, c, L, V);
-    if (more) sk.load(q, chunk(ci + 1), L, TK{bf});
+    sv.load(v, c, L, m.at + bv);
     float gn = 0.f;
     if (w == kTableWave && more) gn = load_decay<REV>(g, chunk(ci + 1), L);
     if (EXTRA == kPairs && w == 0 && ci > 0) store_pairs(chunk(ci - 1));
@@ -895,17 +930,28 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
         if (lg == 0) sums->dots[w][16 * rt + li] = dot;
       }
     }
-    typename TV::Frag wf[EXTRA == kPairs ? DV / 32 : 1];
-    if constexpr (EXTRA == kPairs) {
+    constexpr int WF = EXTRA == kPairs ? DV / 32 : 0;
+    typename TV::Frag wf[WF + 1], wf2[NW == 4 ? WF + 1 : 1];
 #pragma unroll
-      for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb, lane);
+    for (int kb = 0; kb < WF; ++kb) {
+      wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb, lane);
+      if constexpr (NW == 4) wf2[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb, lane);
     }
     if (EXTRA == kPairs) make_p();
+    keep(gn);
+#pragma unroll
+    for (int kb = 0; kb < WF; ++kb) {
+      keep(wf[kb]);
+      if constexpr (NW == 4) keep(wf2[kb]);
+    }
     wait_loads();
     __syncthreads();
 
     // ... then what comes from the chunk's own rows.
-    if (more) sk.load(k, chunk(ci + 1), L, TK{bq});
+    if (more) {
+      sk.load(q, chunk(ci + 1), L, m.at + bf);
+      sk.load(k, chunk(ci + 1), L, m.at + bq);
+    }
     if (EXTRA != kNone && w == 0) {
       float y = 0.f;
 #pragma unroll
@@ -936,12 +982,11 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
 #pragma unroll
         for (int x = 0; x < NA; ++x) y[x] = mma(V.row(16 * (pit + x), kb, lane), wf[kb], y[x]);
       if (more_p) {
-        if (prt2 != prt) {
 #pragma unroll
-          for (int kb = 0; kb < DV / 32; ++kb) wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb, lane);
+        for (int kb = 0; kb < DV / 32; ++kb) {
+          if constexpr (NW == 4) y[NA] = mma(V.row(16 * pit2, kb, lane), wf2[kb], y[NA]);
+          else y[NA] = mma(V.row(16 * pit2, kb, lane), wf[kb], y[NA]);
         }
-#pragma unroll
-        for (int kb = 0; kb < DV / 32; ++kb) y[NA] = mma(V.row(16 * pit2, kb, lane), wf[kb], y[NA]);
         pair_sums(p[NA], y[NA], prt2, pit2);
       }
 #pragma unroll
@@ -962,7 +1007,7 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
       if (t < L) store4(out + (size_t)t * DV + w * 16 + 4 * lg, acc[rt]);
     }
     __syncthreads();
-    unsigned char* const free = bv;
+    const int free = bv;
     bv = bk;
     bk = bq;
     bq = bf;
@@ -978,6 +1023,11 @@ __global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel
   }
 }
 
+template <typename IT, typename OT, int DK, int DV>
+__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void out_kernel(OutArgs a) {
+  out_walk<IT, OT, DK, DV, false, kNone>(a, blockIdx.x, dynamic_lds());
+}
+
 // ---- launches --------------------------------------------------------------------------
 
 template <typename K>
@@ -986,38 +1036,13 @@ hipError_t allow_lds(K* kernel, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <typename IT, int DK, int DV, bool REV>
-hipError_t launch_state(const StateArgs& a, hipStream_t stream) {
-  constexpr int lds = state_lds<IT, DK, DV>();
-  static_assert(lds <= 160 * 1024, "LDS budget");
-  auto* kernel = &state_kernel<IT, DK, DV, REV>;
-  hipError_t e = allow_lds(kernel, lds);
-  if (e != hipSuccess) return e;
-  prof_mark(kSlotLinearState, false, stream);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.count)), dim3(64 * waves(DV)), lds, stream, a);
-  e = hipGetLastError();
-  prof_mark(kSlotLinearState, true, stream);
-  return e;
-}
-
-template <bool REV>
-hipError_t launch_combine(const CombineArgs& a, int BH, hipStream_t stream) {
-  prof_mark(kSlotLinearState, false, stream);
-  hipLaunchKernelGGL(combine_kernel<REV>, dim3((unsigned)cdiv(a.N, 1024), (unsigned)BH), dim3(256), 0, stream, a);
-  hipError_t e = hipGetLastError();
-  prof_mark(kSlotLinearState, true, stream);
-  return e;
-}
-
-template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
-hipError_t launch_out(const OutArgs& a, int slot, hipStream_t stream) {
-  constexpr int lds = OutLds<IT, OT, DK, DV, EXTRA>::bytes;
-  static_assert(lds <= (sizeof(IT) == 2 ? 80 : 160) * 1024, "two bf16 workgroups share a CU's LDS");
-  auto* kernel = &out_kernel<IT, OT, DK, DV, REV, EXTRA>;
-  hipError_t e = allow_lds(kernel, lds);
+// One launch of `kernel`, bracketed for the profiling hook.
+template <typename K, typename... A>
+hipError_t launch(K* kernel, int slot, long long blocks, int threads, int lds, hipStream_t stream, const A&... args) {
+  hipError_t e = lds > 65536 ? allow_lds(kernel, lds) : hipSuccess;
   if (e != hipSuccess) return e;
   prof_mark(slot, false, stream);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)items(a.BH, a.grp, a.s.nseg)), dim3(64 * waves(DV)), lds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), lds, stream, args...);
   e = hipGetLastError();
   prof_mark(slot, true, stream);
   return e;

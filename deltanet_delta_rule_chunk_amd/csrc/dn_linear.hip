@@ -27,13 +27,21 @@ static hipError_t forward(const LinearArgs& a) {
   if (s.nseg > 1) {
     double* decays = reinterpret_cast<double*>(states + (size_t)BH * s.nseg * N);
     StateArgs st{{a.k, grp}, {a.v, 1}, a.log_decay, states, decays, s.nseg, a.L, BH, grp, 0, s.nseg - 1, s};
-    if ((e = launch_state<IT, DK, DV, false>(st, a.stream)) != hipSuccess) return e;
+    e = launch(&state_kernel<IT, DK, DV>, kSlotLinearState, items(BH, grp, st.count), 64 * waves(DV),
+               state_lds<IT, DK, DV>(), a.stream, st);
+    if (e != hipSuccess) return e;
     CombineArgs cb{states, decays, a.S0, s.nseg, s.nseg, (int)N};
-    if ((e = launch_combine<false>(cb, BH, a.stream)) != hipSuccess) return e;
+    prof_mark(kSlotLinearState, false, a.stream);
+    hipLaunchKernelGGL(combine_kernel, dim3(cdiv((int)N, 1024), (unsigned)BH), dim3(256), 0, a.stream, cb);
+    e = hipGetLastError();
+    prof_mark(kSlotLinearState, true, a.stream);
+    if (e != hipSuccess) return e;
   }
   OutArgs o{{a.q, grp}, {a.k, grp}, {a.v, 1}, {nullptr, 1}, a.log_decay, states, a.S0, a.o,
             a.S_final, (long long)N, nullptr, nullptr, s.nseg, a.L, BH, grp, s};
-  return launch_out<IT, OT, DK, DV, false, kNone>(o, kSlotLinearOut, a.stream);
+  constexpr int lds = OutLds<IT, OT, DK, DV, kNone>::bytes;
+  static_assert(lds <= (sizeof(IT) == 2 ? 80 : 160) * 1024, "two bf16 workgroups share a CU's LDS");
+  return launch(&out_kernel<IT, OT, DK, DV>, kSlotLinearOut, items(BH, grp, s.nseg), 64 * waves(DV), lds, a.stream, o);
 }
 
 template <int DK, int DV>

@@ -34,6 +34,39 @@
 namespace dn {
 namespace lin {
 
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
+constexpr int walk_threads(int DK, int DV) { return 64 * max_of(waves(DK), waves(DV)); }
+
+// Segment sums of the state (k, v) and of its gradient (q, dO) side by side.
+template <typename IT, int DK, int DV>
+__global__ __launch_bounds__(64 * waves(DV), simd_waves<IT>(DV)) void bwd_state_kernel(StateArgs s, StateArgs x, int ns) {
+  const Lds m = dynamic_lds();
+  if ((int)blockIdx.x < ns) state_walk<IT, DK, DV, false>(s, blockIdx.x, m);
+  else state_walk<IT, DK, DV, true>(x, blockIdx.x - ns, m);
+}
+static __global__ __launch_bounds__(256) void bwd_combine_kernel(CombineArgs s, CombineArgs x) {
+  if (blockIdx.z == 0) combine<false>(s);
+  else combine<true>(x);
+}
+
+// The three walks side by side, the longest first.  A walk with fewer waves
+// than the launch lets the others end at once.
+template <typename IT, typename OT, int DK, int DV>
+constexpr int walks_lds() {
+  return max_of(OutLds<IT, OT, DV, DK, kPairs>::bytes,
+                max_of(OutLds<IT, IT, DK, DV, kNone>::bytes, OutLds<IT, OT, DV, DK, kDots>::bytes));
+}
+template <typename IT, typename OT, int DK, int DV>
+__global__ __launch_bounds__(walk_threads(DK, DV), simd_waves<IT>(max_of(DK, DV))) void walks_kernel(
+    OutArgs q, OutArgs k, OutArgs v, int n) {
+  const Lds m = dynamic_lds();
+  const int walk = blockIdx.x / n, flat = blockIdx.x % n;
+  if ((int)threadIdx.x >= 64 * waves(walk < 2 ? DK : DV)) return;
+  if (walk == 0) out_walk<IT, OT, DV, DK, false, kPairs>(q, flat, m);
+  else if (walk == 1) out_walk<IT, OT, DV, DK, true, kDots>(k, flat, m);
+  else out_walk<IT, IT, DK, DV, true, kNone>(v, flat, m);
+}
+
 struct DecayGradArgs {
   const float *g, *x, *y, *m;
   const float* S;      // [BH][nseg + 1][N]: slot s = the state that enters segment s
@@ -184,13 +217,18 @@ static hipError_t backward(const LinearBwdArgs& a) {
   hipError_t e;
   if (s.nseg > 1) {
     StateArgs st{{a.k, grp}, {a.v, 1}, a.log_decay, f(o.S), d(o.dS), s.nseg + 1, a.L, BH, grp, 0, s.nseg - 1, s};
-    if ((e = launch_state<IT, DK, DV, false>(st, a.stream)) != hipSuccess) return e;
-    CombineArgs cs{f(o.S), d(o.dS), a.S0, s.nseg + 1, s.nseg, N};
-    if ((e = launch_combine<false>(cs, BH, a.stream)) != hipSuccess) return e;
     StateArgs sx{{a.q, grp}, {a.dO, 1}, a.log_decay, f(o.X), d(o.dX), s.nseg, a.L, BH, grp, 1, s.nseg - 1, s};
-    if ((e = launch_state<IT, DK, DV, true>(sx, a.stream)) != hipSuccess) return e;
+    const int ns = (int)items(BH, grp, s.nseg - 1);
+    e = launch(&bwd_state_kernel<IT, DK, DV>, kSlotLinearState, 2LL * ns, 64 * waves(DV), state_lds<IT, DK, DV>(),
+               a.stream, st, sx, ns);
+    if (e != hipSuccess) return e;
+    CombineArgs cs{f(o.S), d(o.dS), a.S0, s.nseg + 1, s.nseg, N};
     CombineArgs cx{f(o.X), d(o.dX), a.dS_final, s.nseg, s.nseg, N};
-    if ((e = launch_combine<true>(cx, BH, a.stream)) != hipSuccess) return e;
+    prof_mark(kSlotLinearState, false, a.stream);
+    hipLaunchKernelGGL(bwd_combine_kernel, dim3(cdiv(N, 1024), (unsigned)BH, 2), dim3(256), 0, a.stream, cs, cx);
+    e = hipGetLastError();
+    prof_mark(kSlotLinearState, true, a.stream);
+    if (e != hipSuccess) return e;
   }
   // The last state is wanted only against its own gradient.
   float* last = a.dS_final ? f(o.S) + (size_t)s.nseg * N : nullptr;
@@ -198,13 +236,15 @@ static hipError_t backward(const LinearBwdArgs& a) {
   OutArgs q{{a.dO, 1}, {a.v, 1}, {a.k, grp}, {a.q, grp}, a.log_decay, f(o.S), a.S0,
             shared ? (void*)f(o.dq) : a.dq, last, (long long)(s.nseg + 1) * N, f(o.x), f(o.m), s.nseg + 1,
             a.L, BH, grp, s};
-  if ((e = launch_out<IT, OT, DV, DK, false, kPairs>(q, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
   OutArgs v{{a.k, grp}, {a.q, grp}, {a.dO, 1}, {nullptr, 1}, a.log_decay, f(o.X), a.dS_final,
             a.dv, a.dS0, N, nullptr, nullptr, s.nseg, a.L, BH, grp, s};
-  if ((e = launch_out<IT, IT, DK, DV, true, kNone>(v, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
   OutArgs k{{a.v, 1}, {a.dO, 1}, {a.q, grp}, {a.k, grp}, a.log_decay, f(o.X), a.dS_final,
             shared ? (void*)f(o.dk) : a.dk, nullptr, 0, f(o.y), nullptr, s.nseg, a.L, BH, grp, s};
-  if ((e = launch_out<IT, OT, DV, DK, true, kDots>(k, kSlotLinearBwd, a.stream)) != hipSuccess) return e;
+  constexpr int lds = walks_lds<IT, OT, DK, DV>();
+  static_assert(lds <= (sizeof(IT) == 2 ? 80 : 160) * 1024, "two bf16 workgroups share a CU's LDS");
+  const int n = (int)items(BH, grp, s.nseg);
+  e = launch(&walks_kernel<IT, OT, DK, DV>, kSlotLinearBwd, 3LL * n, walk_threads(DK, DV), lds, a.stream, q, k, v, n);
+  if (e != hipSuccess) return e;
   if (shared) {
     const size_t n = (size_t)a.B * a.H_qk * a.L * DK, per = (size_t)a.L * DK;
     const dim3 grid((unsigned)((n / 4 + 255) / 256));

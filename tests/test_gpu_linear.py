@@ -391,7 +391,9 @@ def test_profile_slots(gpu_lib):
     N.linear_chunk_fwd(x["q"], x["k"], x["v"], x["g"])
     N.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], None, x["dO"])
     got = N.profile_stop()
-    assert got["linear_out"][1] == 1 and got["linear_state"][1] == 6 and got["linear_bwd"][1] == 4
+    # forward: segment sums, their combination, outputs; backward: the same
+    # two, the walks and the decay's gradient
+    assert got["linear_out"][1] == 1 and got["linear_state"][1] == 4 and got["linear_bwd"][1] == 2
     assert all(ms > 0 for ms, _ in got.values())
 
 
