@@ -453,10 +453,14 @@ struct StateArgs {
 template <typename IT, int DK>
 __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> K,
                                              const typename Tile<IT, 64>::Frag (&vf)[C / 32], const Decays* d, int l) {
+  // Column fragments are read AHEAD tiles before their products, so that LDS
+  // answers meanwhile.
+  constexpr int KT = DK / 16, N = KT * (C / 32), AHEAD = 4;
   const int g = l >> 4;
-  const float total = d->total;
+  typename Tile<IT, DK>::Frag a[AHEAD];
 #pragma unroll
-  for (int kt = 0; kt < DK / 16; ++kt) st[kt] *= total;
+  for (int i = 0; i < AHEAD; ++i) a[i] = K.state_col(i % KT, i / KT, l);
+  const float total = d->total;
 #pragma unroll
   for (int tb = 0; tb < C / 32; ++tb) {
     const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d->up[32 * tb + 4 * g]);
@@ -467,7 +471,12 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> 
     for (int e = 0; e < 4; ++e) x[e] *= u0[e], x[4 + e] *= u1[e];
     const Made<IT, 3> y(x);
 #pragma unroll
-    for (int kt = 0; kt < DK / 16; ++kt) st[kt] = mma(K.state_col(kt, tb, l), y, st[kt]);
+    for (int kt = 0; kt < KT; ++kt) {
+      const int i = tb * KT + kt;
+      if (tb == 0) st[kt] *= total;
+      st[kt] = mma(a[i % AHEAD], y, st[kt]);
+      if (i + AHEAD < N) a[i % AHEAD] = K.state_col((i + AHEAD) % KT, (i + AHEAD) / KT, l);
+    }
   }
 }
 
@@ -477,11 +486,12 @@ template <int DK, int DV, bool TRANS>
 __device__ __forceinline__ void load_state(f32x4 (&st)[DK / 16], const float* S) {
   const int l = threadIdx.x & 63, g = l >> 4, j = (threadIdx.x >> 6) * 16 + (l & 15);
 #pragma unroll
+  for (int kt = 0; kt < DK / 16; ++kt) st[kt] = zero4();
+  if (!S) return;
+#pragma unroll
   for (int kt = 0; kt < DK / 16; ++kt) {
     const int k0 = state_row(kt, g);
-    if (!S) {
-      st[kt] = zero4();
-    } else if (TRANS) {
+    if (TRANS) {
       st[kt] = *reinterpret_cast<const f32x4*>(S + (size_t)j * DK + k0);
     } else {
 #pragma unroll
@@ -892,12 +902,15 @@ __device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
         for (int kb = 0; kb < DK / 32; ++kb) p[NA] = mma(K.row(16 * pit2, kb, lane), Q.row(16 * prt2, kb, lane), p[NA]);
       }
       auto decay_tile = [&](f32x4& x, int rt, int it) {
-        const int r = 16 * rt + li;
-        const double Gr = dec->G[r];
+        const double Gr = dec->G[16 * rt + li];
+        double Gi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Gi[e] = dec->G[16 * it + 4 * lg + e];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = 16 * it + 4 * lg + e;
-          x[e] = i <= r ? x[e] * exp2_hw((float)(Gr - dec->G[i])) : 0.f;
+          // (Above the diagonal the factor may be infinite: it is not used.)
+          const float f = exp2_hw((float)(Gr - Gi[e])) * x[e];
+          x[e] = it < rt || 4 * lg + e <= li ? f : 0.f;
         }
         P.put(rt, it, x, lane);
       };
@@ -912,13 +925,19 @@ __device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
     f32x4 acc[NRT];
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) acc[rt] = zero4();
+    typename TK::Frag b[NRT];
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) b[rt] = Q.row(16 * rt, 0, lane);
 #pragma unroll
     for (int kb = 0; kb < DK / 32; ++kb) {
       const f32x4 x = st[2 * kb], y = st[2 * kb + 1];
       const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
       const Made<IT, NSS> s(z);
 #pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) acc[rt] = mma(s, Q.row(16 * rt, kb, lane), acc[rt]);
+      for (int rt = 0; rt < NRT; ++rt) {
+        acc[rt] = mma(s, b[rt], acc[rt]);
+        if (kb + 1 < DK / 32) b[rt] = Q.row(16 * rt, kb + 1, lane);
+      }
     }
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
