@@ -10,8 +10,8 @@ the library is missing it raises: there is no fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -131,11 +131,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_CODES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
+
+
 def _code(dt: torch.dtype) -> int:
-    if dt == torch.float32:
-        return DN_F32
-    if dt == torch.bfloat16:
-        return DN_BF16
+    code = _CODES.get(dt)
+    if code is not None:
+        return code
     raise TypeError(f"unsupported dtype {dt} (float32 or bfloat16)")
 
 
@@ -144,6 +146,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _check(t: torch.Tensor, name: str, shape, dtype=None, device=None):
+    # One look for tensors that are right; the reasons only for those that are not.
+    if (type(t) is torch.Tensor and t.shape == shape and t.device == device
+            and (dtype is None or t.dtype is dtype) and t.is_contiguous() and t.is_cuda):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
@@ -165,9 +171,17 @@ def _raise(lib, status: int, what: str):
     raise DeltaNetError(status, what, detail)
 
 
+# The current stream's handle without a Stream object around it (1.7 us less
+# per call), where this PyTorch has it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device, stream) -> int:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None and device.index is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _alloc(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
@@ -483,25 +497,13 @@ def gated_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: 
     return decode_step(q, k, v, beta, S, alpha=alpha, **kw)
 
 
-def _on(device: torch.device):
-    """The device made current for a call on its tensors (a null stream names
-    the current device's)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _elsewhere(device: torch.device) -> bool:
+    """Whether the device is not the current one (a null stream names the
+    current device's, so a call on its tensors has to make it current)."""
+    return device.type == "cuda" and device.index != torch.cuda.current_device()
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, device: torch.device, stream):
-    """(pointer, bytes, keeper) of the caller's workspace or a new one."""
-    if given is None:
-        if need == 0:
-            return None, 0, None
-        given = _alloc(need, torch.uint8, device, stream)
-    elif given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    return given.data_ptr(), given.numel() * given.element_size(), given
-
-
+@functools.lru_cache(maxsize=1024)
 def linear_workspace_bytes(B: int, H: int, L: int, d_k: int, d_v: int,
                            in_dtype: torch.dtype = torch.bfloat16, H_qk: Optional[int] = None,
                            backward: bool = False) -> int:
@@ -512,21 +514,49 @@ def linear_workspace_bytes(B: int, H: int, L: int, d_k: int, d_v: int,
     return int(fn(B, H, H if H_qk is None else H_qk, L, d_k, d_v, _code(in_dtype)))
 
 
-def _check_linear(q, k, v, log_decay, states, dims=4):
+def _workspace(given: Optional[torch.Tensor], need: int, device: torch.device, stream):
+    """(tensor or None, pointer, bytes) of the caller's workspace or a new one."""
+    if given is None:
+        if need == 0:
+            return None, None, 0
+        given = _alloc(need, torch.uint8, device, stream)
+    elif given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _check_linear(q, k, v, log_decay, states, dims):
     """Shapes of the gated linear recurrence's inputs, ``[B, H, L, d]`` or (one
-    token, ``dims`` = 3) ``[B, H, d]``; ``states`` are (tensor, name) pairs."""
-    if q.dim() != dims or v.dim() != dims:
-        raise ValueError(f"q and v must have {dims} dimensions (got {tuple(q.shape)}, {tuple(v.shape)})")
-    dev, tok, d_k = q.device, tuple(q.shape[2:-1]), q.shape[-1]
-    B, H_qk, (H, d_v) = q.shape[0], q.shape[1], (v.shape[1], v.shape[-1])
-    _check(q, "q", (B, H_qk, *tok, d_k), device=dev)
-    _check(k, "k", (B, H_qk, *tok, d_k), q.dtype, dev)
-    _check(v, "v", (B, H, *tok, d_v), q.dtype, dev)
-    if log_decay is not None:
-        _check(log_decay, "log_decay", (B, H, *tok), torch.float32, dev)
-    for t, n in states:
-        if t is not None:
-            _check(t, n, (B, H, d_k, d_v), torch.float32, dev)
+    token, ``dims`` = 3) ``[B, H, d]``; ``states`` are (tensor or None, name)
+    pairs.  Returns (B, H, H_qk, d_k, d_v)."""
+    qs, vs = q.shape, v.shape
+    if len(qs) != dims or len(vs) != dims:
+        raise ValueError(f"q and v must have {dims} dimensions (got {tuple(qs)}, {tuple(vs)})")
+    dev, dt = q.device, q.dtype
+    B, H_qk, H, d_k, d_v = qs[0], qs[1], vs[1], qs[-1], vs[-1]
+    state = (B, H, d_k, d_v)
+    # One look at everything; the reasons only where something is wrong.
+    good = (q.is_cuda and k.shape == qs and k.dtype is dt and v.dtype is dt and vs[0] == B
+            and vs[2:-1] == qs[2:-1] and k.device == dev and v.device == dev
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and (log_decay is None or (log_decay.shape == vs[:-1] and log_decay.device == dev
+                                       and log_decay.dtype is torch.float32
+                                       and log_decay.is_contiguous())))
+    if good:
+        for t, _ in states:
+            if t is not None and not (t.shape == state and t.dtype is torch.float32
+                                      and t.device == dev and t.is_contiguous()):
+                good = False
+    if not good:
+        tok = tuple(qs[2:-1])
+        _check(q, "q", (B, H_qk, *tok, d_k), device=dev)
+        _check(k, "k", (B, H_qk, *tok, d_k), dt, dev)
+        _check(v, "v", (B, H, *tok, d_v), dt, dev)
+        if log_decay is not None:
+            _check(log_decay, "log_decay", (B, H, *tok), torch.float32, dev)
+        for t, n in states:
+            if t is not None:
+                _check(t, n, state, torch.float32, dev)
     return B, H, H_qk, d_k, d_v
 
 
@@ -542,21 +572,26 @@ def linear_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     head ``h // (H // H_qk)``), log_decay ``[B,H,L]`` fp32 (``-inf`` wipes the
     state exactly) or None, S0 ``[B,H,d_k,d_v]`` fp32 or None.  Returns
     ``(o, S_final)``; S_final is None when ``want_state`` is False."""
-    lib = load()
-    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S0, "S0"), (S_final, "S_final")))
+    lib = _lib or load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S0, "S0"), (S_final, "S_final")), 4)
     dev, L = q.device, q.shape[2]
-    with _on(dev):
-        if o is None:
-            o = _alloc((B, H, L, d_v), out_dtype, dev, stream)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear_chunk_fwd(q, k, v, log_decay, S0, out_dtype=out_dtype, o=o,
+                                    S_final=S_final, want_state=want_state, workspace=workspace,
+                                    stream=stream)
+    if o is None:
+        o = _alloc((B, H, L, d_v), out_dtype, dev, stream)
+    else:
         _check(o, "o", (B, H, L, d_v), out_dtype, dev)
-        if S_final is None and want_state:
-            S_final = _alloc((B, H, d_k, d_v), torch.float32, dev, stream)
-        need = linear_workspace_bytes(B, H, L, d_k, d_v, q.dtype, H_qk)
-        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
-        st = lib.deltanet_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
-                                           _ptr(o), _ptr(S_final), B, H, H_qk, L, d_k, d_v,
-                                           _code(q.dtype), _code(out_dtype), ws, ws_bytes,
-                                           _stream(dev, stream))
+    if S_final is None and want_state:
+        S_final = _alloc((B, H, d_k, d_v), torch.float32, dev, stream)
+    need = linear_workspace_bytes(B, H, L, d_k, d_v, q.dtype, H_qk)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(log_decay),
+                                       _ptr(S0), o.data_ptr(), _ptr(S_final), B, H, H_qk, L, d_k,
+                                       d_v, _code(q.dtype), _code(out_dtype), ws, ws_bytes,
+                                       _stream(dev, stream))
     if st != DN_OK:
         _raise(lib, st, "deltanet_linear_chunk_fwd")
     return o, S_final
@@ -571,21 +606,26 @@ def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     None.  Returns ``(dq, dk, dv, dlog_decay, dS0)``: dq, dk, dv in the inputs'
     dtype, dlog_decay (None without log_decay) and dS0 (None when ``want_dS0``
     is False) in fp32."""
-    lib = load()
-    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S0, "S0"), (dS_final, "dS_final")))
-    dev, L = q.device, q.shape[2]
-    _check(dO, "dO", (B, H, L, d_v), q.dtype, dev)
-    with _on(dev):
-        dq, dk = (_alloc(q.shape, q.dtype, dev, stream) for _ in range(2))
-        dv = _alloc(v.shape, q.dtype, dev, stream)
-        dg = None if log_decay is None else _alloc(log_decay.shape, torch.float32, dev, stream)
-        dS0 = _alloc((B, H, d_k, d_v), torch.float32, dev, stream) if want_dS0 else None
-        need = linear_workspace_bytes(B, H, L, d_k, d_v, q.dtype, H_qk, backward=True)
-        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
-        st = lib.deltanet_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
-                                           _ptr(dO), _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv),
-                                           _ptr(dg), _ptr(dS0), B, H, H_qk, L, d_k, d_v,
-                                           _code(q.dtype), ws, ws_bytes, _stream(dev, stream))
+    lib = _lib or load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay,
+                                         ((S0, "S0"), (dS_final, "dS_final")), 4)
+    dev, dt, L = q.device, q.dtype, q.shape[2]
+    _check(dO, "dO", (B, H, L, d_v), dt, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear_chunk_bwd(q, k, v, log_decay, S0, dO, dS_final, want_dS0=want_dS0,
+                                    workspace=workspace, stream=stream)
+    dq, dk = _alloc(q.shape, dt, dev, stream), _alloc(q.shape, dt, dev, stream)
+    dv = _alloc(v.shape, dt, dev, stream)
+    dg = None if log_decay is None else _alloc(log_decay.shape, torch.float32, dev, stream)
+    dS0 = _alloc((B, H, d_k, d_v), torch.float32, dev, stream) if want_dS0 else None
+    need = linear_workspace_bytes(B, H, L, d_k, d_v, dt, H_qk, True)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_linear_chunk_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(log_decay),
+                                       _ptr(S0), dO.data_ptr(), _ptr(dS_final), dq.data_ptr(),
+                                       dk.data_ptr(), dv.data_ptr(), _ptr(dg), _ptr(dS0), B, H,
+                                       H_qk, L, d_k, d_v, _code(dt), ws, ws_bytes,
+                                       _stream(dev, stream))
     if st != DN_OK:
         _raise(lib, st, "deltanet_linear_chunk_bwd")
     return dq, dk, dv, dg, dS0
@@ -625,16 +665,21 @@ def linear_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """One token of the gated linear recurrence (``deltanet_linear_decode_step``):
     updates S ``[B,H,d_k,d_v]`` in place and returns o ``[B,H,d_v]`` = q S_new.
     q,k ``[B,H_qk,d_k]``, v ``[B,H,d_v]``, log_decay ``[B,H]`` fp32 or None."""
-    lib = load()
-    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S, "S"),), dims=3)
+    lib = _lib or load()
+    B, H, H_qk, d_k, d_v = _check_linear(q, k, v, log_decay, ((S, "S"),), 3)
     dev = q.device
-    with _on(dev):
-        if o is None:
-            o = _alloc((B, H, d_v), out_dtype, dev, stream)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear_decode_step(q, k, v, log_decay, S, out_dtype=out_dtype, o=o,
+                                      stream=stream)
+    if o is None:
+        o = _alloc((B, H, d_v), out_dtype, dev, stream)
+    else:
         _check(o, "o", (B, H, d_v), out_dtype, dev)
-        st = lib.deltanet_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S),
-                                             _ptr(o), B, H, H_qk, d_k, d_v, _code(q.dtype),
-                                             _code(out_dtype), _stream(dev, stream))
+    st = lib.deltanet_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                         _ptr(log_decay), S.data_ptr(), o.data_ptr(), B, H, H_qk,
+                                         d_k, d_v, _code(q.dtype), _code(out_dtype),
+                                         _stream(dev, stream))
     if st != DN_OK:
         _raise(lib, st, "deltanet_linear_decode_step")
     return o
@@ -642,6 +687,9 @@ def linear_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 def _check_rows(t: torch.Tensor, name: str, shape, dtype, device):
     """A tensor of rows at any strides over its other dimensions."""
+    if (type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == device
+            and t.is_cuda and t.stride(-1) == 1):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
@@ -656,38 +704,53 @@ def _check_rows(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
+_Strides = ctypes.c_longlong * 3
+
+
 def _strides(t: torch.Tensor):
-    return (ctypes.c_longlong * 3)(*t.stride()[:3])
+    return _Strides(*t.stride()[:3])
+
+
+@functools.lru_cache(maxsize=256)
+def _int_array(*x):
+    return (ctypes.c_int * len(x))(*x)
 
 
 def _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, sections):
-    """Checks shared by both directions; (sizes, leading arguments, section counts)."""
-    if q_raw.dim() != 4 or k_raw.dim() != 4:
+    """Checks shared by both directions; (sizes, leading arguments)."""
+    qs, ks = q_raw.shape, k_raw.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("q_raw and k_raw must be [B, H, L, d]")
-    dev, (B, H_q, L, d) = q_raw.device, q_raw.shape
-    H_k = k_raw.shape[1]
-    _check_rows(q_raw, "q_raw", (B, H_q, L, d), q_raw.dtype, dev)
-    _check_rows(k_raw, "k_raw", (B, H_k, L, d), q_raw.dtype, dev)
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _check(t, n, (d,), torch.float32, dev)
-    d_rot, axes, counts = 0, 1, None
+    dev, dt, (B, H_q, L, d), H_k = q_raw.device, q_raw.dtype, qs, ks[1]
+    qst, kst = q_raw.stride(), k_raw.stride()
+    if not (q_raw.is_cuda and ks[0] == B and ks[2:] == qs[2:] and k_raw.dtype is dt
+            and k_raw.device == dev and qst[3] == 1 and kst[3] == 1):
+        _check_rows(q_raw, "q_raw", (B, H_q, L, d), dt, dev)
+        _check_rows(k_raw, "k_raw", (B, H_k, L, d), dt, dev)
+    if q_weight is not None:
+        _check(q_weight, "q_weight", (d,), torch.float32, dev)
+    if k_weight is not None:
+        _check(k_weight, "k_weight", (d,), torch.float32, dev)
+    d_rot, axes, counts, pos, inv = 0, 1, None, None, None
     if inv_freq is not None:
-        d_rot = 2 * inv_freq.numel()
-        _check(inv_freq, "inv_freq", (d_rot // 2,), torch.float32, dev)
+        n = inv_freq.numel()
+        d_rot = 2 * n
+        _check(inv_freq, "inv_freq", (n,), torch.float32, dev)
         if positions is None:
             raise ValueError("positions are required with inv_freq")
-        axes = positions.shape[0] if positions.dim() == 3 else 1
-        _check(positions, "positions", (axes, B, L) if positions.dim() == 3 else (B, L),
-               torch.int32, dev)
-        if sections is None and axes > 1:
-            raise ValueError("several position axes need sections")
+        several = positions.dim() == 3
+        axes = positions.shape[0] if several else 1
+        _check(positions, "positions", (axes, B, L) if several else (B, L), torch.int32, dev)
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError(f"{len(sections)} sections for {axes} position axes")
-            counts = (ctypes.c_int * axes)(*sections)
-    lead = (_ptr(q_raw), _strides(q_raw), _ptr(k_raw), _strides(k_raw), _ptr(q_weight),
-            _ptr(k_weight), _ptr(positions) if d_rot else None, _ptr(inv_freq), counts, axes)
+            counts = _int_array(*sections)
+        elif axes > 1:
+            raise ValueError("several position axes need sections")
+        if d_rot:
+            pos, inv = positions.data_ptr(), inv_freq.data_ptr()
+    lead = (q_raw.data_ptr(), _Strides(*qst[:3]), k_raw.data_ptr(), _Strides(*kst[:3]),
+            _ptr(q_weight), _ptr(k_weight), pos, inv, counts, axes)
     return (B, H_q, H_k, L, d, d_rot), lead
 
 
@@ -703,19 +766,27 @@ def qk_norm_rope(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[t
     ``[B,L]`` or ``[axes,B,L]`` int32; inv_freq ``[d_rot/2]`` fp32 (None: no
     rotation); ``sections``: rotated pairs per position axis.  Returns dense
     ``(q_hat, k_hat)`` in the inputs' dtype."""
-    lib = load()
+    lib = _lib or load()
     (B, H_q, H_k, L, d, d_rot), lead = _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight,
                                                  k_weight, sections)
-    dev = q_raw.device
-    with _on(dev):
-        qh = _alloc((B, H_q, L, d), q_raw.dtype, dev, stream)
-        kh = _alloc((B, H_k, L, d), q_raw.dtype, dev, stream)
-        st = lib.deltanet_qk_norm_rope(*lead, _ptr(qh), _ptr(kh), B, H_q, H_k, L, d, d_rot,
-                                       int(norm), int(interleaved), eps, _code(q_raw.dtype),
-                                       _stream(dev, stream))
+    dev, dt = q_raw.device, q_raw.dtype
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return qk_norm_rope(q_raw, k_raw, positions, inv_freq, q_weight=q_weight,
+                                k_weight=k_weight, sections=sections, eps=eps, norm=norm,
+                                interleaved=interleaved, stream=stream)
+    qh, kh = _alloc((B, H_q, L, d), dt, dev, stream), _alloc((B, H_k, L, d), dt, dev, stream)
+    st = lib.deltanet_qk_norm_rope(*lead, qh.data_ptr(), kh.data_ptr(), B, H_q, H_k, L, d, d_rot,
+                                   int(norm), int(interleaved), eps, _code(dt),
+                                   _stream(dev, stream))
     if st != DN_OK:
         _raise(lib, st, "deltanet_qk_norm_rope")
     return qh, kh
+
+
+@functools.lru_cache(maxsize=1024)
+def _qk_bwd_workspace_bytes(*sizes) -> int:
+    return int(load().deltanet_qk_norm_rope_bwd_workspace_bytes(*sizes))
 
 
 def _like_rows(t: torch.Tensor, stream) -> torch.Tensor:
@@ -739,29 +810,38 @@ def qk_norm_rope_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Option
     dq_weight, dk_weight)``; the weights' gradients (fp32) are None where the
     weight is.  ``dq_raw``, ``dk_raw`` may be given, at any strides (the parts
     of a fused projection's gradient)."""
-    lib = load()
+    lib = _lib or load()
     (B, H_q, H_k, L, d, d_rot), lead = _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight,
                                                  k_weight, sections)
     dev, t = q_raw.device, q_raw.dtype
     _check(dq_hat, "dq_hat", (B, H_q, L, d), t, dev)
     _check(dk_hat, "dk_hat", (B, H_k, L, d), t, dev)
-    with _on(dev):
-        dq_raw = _like_rows(q_raw, stream) if dq_raw is None else dq_raw
-        dk_raw = _like_rows(k_raw, stream) if dk_raw is None else dk_raw
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return qk_norm_rope_bwd(q_raw, k_raw, positions, inv_freq, dq_hat, dk_hat,
+                                    q_weight=q_weight, k_weight=k_weight, sections=sections,
+                                    eps=eps, norm=norm, interleaved=interleaved, dq_raw=dq_raw,
+                                    dk_raw=dk_raw, workspace=workspace, stream=stream)
+    if dq_raw is None:
+        dq_raw = _like_rows(q_raw, stream)
+    else:
         _check_rows(dq_raw, "dq_raw", (B, H_q, L, d), t, dev)
+    if dk_raw is None:
+        dk_raw = _like_rows(k_raw, stream)
+    else:
         _check_rows(dk_raw, "dk_raw", (B, H_k, L, d), t, dev)
-        dw = [None if w is None else _alloc((d,), torch.float32, dev, stream)
-              for w in (q_weight, k_weight)]
-        need = int(lib.deltanet_qk_norm_rope_bwd_workspace_bytes(B, H_q, H_k, L, d, _code(t)))
-        ws, ws_bytes, keep = _workspace(workspace, need, dev, stream)
-        st = lib.deltanet_qk_norm_rope_bwd(*lead, _ptr(dq_hat), _ptr(dk_hat), _ptr(dq_raw),
-                                           _strides(dq_raw), _ptr(dk_raw), _strides(dk_raw),
-                                           _ptr(dw[0]), _ptr(dw[1]), B, H_q, H_k, L, d, d_rot,
-                                           int(norm), int(interleaved), eps, _code(t), ws,
-                                           ws_bytes, _stream(dev, stream))
+    dqw = None if q_weight is None else _alloc((d,), torch.float32, dev, stream)
+    dkw = None if k_weight is None else _alloc((d,), torch.float32, dev, stream)
+    need = _qk_bwd_workspace_bytes(B, H_q, H_k, L, d, _code(t))
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_qk_norm_rope_bwd(*lead, dq_hat.data_ptr(), dk_hat.data_ptr(),
+                                       dq_raw.data_ptr(), _strides(dq_raw), dk_raw.data_ptr(),
+                                       _strides(dk_raw), _ptr(dqw), _ptr(dkw), B, H_q, H_k, L, d,
+                                       d_rot, int(norm), int(interleaved), eps, _code(t), ws,
+                                       ws_bytes, _stream(dev, stream))
     if st != DN_OK:
         _raise(lib, st, "deltanet_qk_norm_rope_bwd")
-    return dq_raw, dk_raw, dw[0], dw[1]
+    return dq_raw, dk_raw, dqw, dkw
 
 
 class _RotaryQK(torch.autograd.Function):
