@@ -38,10 +38,10 @@
 //
 // Precision.  bf16 q, k, v (and dO) enter products as they are.  An fp32
 // operand enters as a sum of bf16 pieces: 3 pieces (24 bits, all of fp32) where
-// it reaches an fp32 result through long sums: the rows added to the state, the
-// state read for an fp32 output or for what the decay's gradient is summed
-// from; 2 pieces (16 bits) for the state read for a bf16 output, whose own
-// rounding is 256 times coarser, and for P, whose sums span one chunk (a third
+// it reaches an fp32 result through long sums: the rows added to a state that is
+// a result or enters a segment, the state read for an fp32 output or for what
+// the decay's gradient is summed from; 2 pieces (16 bits) for rows and state
+// that only reach bf16 outputs, whose own rounding is 256 times coarser, and for P, whose sums span one chunk (a third
 // piece of P would cost the second workgroup of each CU its LDS; it leaves
 // 2^-17 of a term).  fp32 inputs run the same
 // kernels on the fp32 matrix instruction, with nothing split.  Log decays are
@@ -461,12 +461,15 @@ struct StateArgs {
   Split s;
 };
 
-// S = total S + K^T diag(up) V on this wave's columns.
-template <typename IT, int DK>
+// S = total S + K^T diag(up) V on this wave's columns, diag(up) V in NU pieces.
+template <int NU, typename IT, int DK>
 __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> K,
                                              const typename Tile<IT, 64>::Frag (&vf)[C / 32], const Decays* d, int l) {
   // Column fragments are read AHEAD tiles before their products, so that LDS
   // answers meanwhile.
+  // The waves that are here go first: theirs are the long runs of matrix
+  // instructions that the others' vector work hides behind (3% of a walk).
+  __builtin_amdgcn_s_setprio(1);
   constexpr int KT = DK / 16, N = KT * (C / 32), AHEAD = 4;
   const int g = l >> 4;
   typename Tile<IT, DK>::Frag a[AHEAD];
@@ -481,7 +484,7 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> 
     to_floats(vf[tb], x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] *= u0[e], x[4 + e] *= u1[e];
-    const Made<IT, 3> y(x);
+    const Made<IT, NU> y(x);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       const int i = tb * KT + kt;
@@ -490,6 +493,7 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> 
       if (i + AHEAD < N) a[i % AHEAD] = K.state_col((i + AHEAD) % KT, (i + AHEAD) / KT, l);
     }
   }
+  __builtin_amdgcn_s_setprio(0);
 }
 
 // fp32 state (row-major [DK][DV], or [DV][DK] when TRANS) <-> this wave's
@@ -588,7 +592,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& a, int flat, Lds m) 
     unsigned char* const at = smem + (i & 1) * TB;
     typename Tile<IT, DV>::Frag vf[C / 32];
     value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes}, w, lane);
-    update_state<IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], lane);
+    update_state<3, IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], lane);
     if (more && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
     wait_loads();
     __syncthreads();
@@ -809,8 +813,8 @@ __device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row
 //   2  P V, the output, the state's update (K, V);  the next Q and K arrive
 // Four tile buffers suffice: the next Q goes where V was a chunk ago, the next
 // K where Q is no longer read, the next V where K is no longer read.
-template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
-__device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
+template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA, int NU>
+__device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, Lds m) {
   unsigned char* const smem = m.p;
   using LD = OutLds<IT, OT, DK, DV, EXTRA>;
   constexpr int NW = waves(DV), NRT = C / 16, NSP = LD::NSP, NSS = LD::NSS;
@@ -821,8 +825,6 @@ __device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
   Decays* const tables = reinterpret_cast<Decays*>(smem + LD::D);
   Sums<NW>* const sums = reinterpret_cast<Sums<NW>*>(smem + LD::S);
 
-  int bh, seg;
-  if (!item_of(flat, a.BH, a.grp, a.s.nseg, bh, seg)) return;
   const int L = a.L, c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
   const IT* q = a.q.head<IT>(bh, L, DK);
   const IT* k = a.k.head<IT>(bh, L, DK);
@@ -1029,7 +1031,7 @@ __device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
     for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
       for (int kb = 0; kb <= rt / 2; ++kb) acc[rt] = mma(vf[kb], P.get(rt, kb, lane), acc[rt]);
-    update_state<IT, DK>(st, K, vf, dec, lane);
+    update_state<NU, IT, DK>(st, K, vf, dec, lane);
     if (w == kTableWave && more) fill_decays(&tables[(ci + 1) & 1], gn);
     wait_loads();
 #pragma unroll
@@ -1052,6 +1054,19 @@ __device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
     const float f = REV && g ? exp2_hw((float)log2_decay(g[0])) : 1.f;
     store_state<DK, DV, TRANS>(st, a.last + (size_t)bh * a.last_stride, f);
   }
+}
+
+template <typename IT, typename OT, int DK, int DV, bool REV, int EXTRA>
+__device__ __forceinline__ void out_walk(const OutArgs& a, int flat, Lds m) {
+  int bh, seg;
+  if (!item_of(flat, a.BH, a.grp, a.s.nseg, bh, seg)) return;
+  // A segment whose last state goes nowhere and whose outputs are stored in
+  // bf16 keeps 16 bits of what it adds to its state.
+  constexpr bool rough = sizeof(IT) == 2 && sizeof(OT) == 2 && EXTRA == kNone;
+  if (rough && !(a.last && seg == (REV ? 0 : a.s.nseg - 1)))
+    walk_segment<IT, OT, DK, DV, REV, EXTRA, rough ? 2 : 3>(a, bh, seg, m);
+  else
+    walk_segment<IT, OT, DK, DV, REV, EXTRA, 3>(a, bh, seg, m);
 }
 
 template <typename IT, typename OT, int DK, int DV>

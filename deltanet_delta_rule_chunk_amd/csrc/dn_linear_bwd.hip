@@ -56,34 +56,21 @@ constexpr int walks_lds() {
   return max_of(OutLds<IT, OT, DV, DK, kPairs>::bytes,
                 max_of(OutLds<IT, IT, DK, DV, kNone>::bytes, OutLds<IT, OT, DV, DK, kDots>::bytes));
 }
-template <typename IT, typename OT, int DK, int DV>
-__global__ __launch_bounds__(walk_threads(DK, DV), simd_waves<IT>(max_of(DK, DV))) void walks_kernel(
-    OutArgs q, OutArgs k, OutArgs v, int n) {
-  const Lds m = dynamic_lds();
-  const int walk = blockIdx.x / n, flat = blockIdx.x % n;
-  if ((int)threadIdx.x >= 64 * waves(walk < 2 ? DK : DV)) return;
-  if (walk == 0) out_walk<IT, OT, DV, DK, false, kPairs>(q, flat, m);
-  else if (walk == 1) out_walk<IT, OT, DV, DK, true, kDots>(k, flat, m);
-  else out_walk<IT, IT, DK, DV, true, kNone>(v, flat, m);
-}
-
-struct DecayGradArgs {
-  const float *g, *x, *y, *m;
-  const float* S;      // [BH][nseg + 1][N]: slot s = the state that enters segment s
-  const float* X;      // [BH][nseg][N]: the reversed walk's state behind segment s (nseg > 1)
-  const float *S0, *dS0;  // [BH][N]: the first state and its gradient; S0 null: zero; dS0 null: not known
-  const float* dS;     // [BH][N] or null: gradient of the last state
-  float* dg;
-  int L, BH, N;
+// Behind them in the grid, one workgroup per inner border of the segments: the
+// state there against its gradient, which the decay's gradient starts from.
+struct BorderArgs {
+  const float *S, *X;  // [BH][nseg + 1][N], [BH][nseg][N]
+  const float* g;
+  double* border;      // [BH][nseg]: entry s for the start of segment s >= 1
+  int L, N;
   Split s;
 };
 
-constexpr int kGradThreads = 1024;
-
-// <u, v> over a workgroup, every thread's answer.
-static __device__ double dot_states(const float* u, const float* v, int n, double* part) {
+// <u, v> over T threads, every thread's answer.
+template <int T>
+__device__ __forceinline__ double dot_states(const float* u, const float* v, int n, double* part) {
   double acc = 0.0;
-  for (int i = threadIdx.x * 4; i < n; i += kGradThreads * 4) {
+  for (int i = threadIdx.x * 4; i < n; i += T * 4) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(u + i), b = *reinterpret_cast<const f32x4*>(v + i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc += (double)a[e] * (double)b[e];
@@ -93,38 +80,72 @@ static __device__ double dot_states(const float* u, const float* v, int n, doubl
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
   __syncthreads();
   double sum = 0.0;
-  for (int i = 0; i < kGradThreads / 64; ++i) sum += part[i];
+  for (int i = 0; i < T / 64; ++i) sum += part[i];
   return sum;
 }
 
+template <int T>
+__device__ __forceinline__ void border_dot(const BorderArgs& a, int i, double* part) {
+  const int bh = i / (a.s.nseg - 1), s = i % (a.s.nseg - 1) + 1;
+  const double d = dot_states<T>(a.S + ((size_t)bh * (a.s.nseg + 1) + s) * a.N, a.X + ((size_t)bh * a.s.nseg + s - 1) * a.N,
+                                 a.N, part);
+  // The reversed walk's states are gradients of the state after the token
+  // behind them; that token's decay stands between.
+  if (threadIdx.x == 0)
+    a.border[(size_t)bh * a.s.nseg + s] =
+        d * (double)exp2_hw((float)log2_decay(a.g[(size_t)bh * a.L + (size_t)s * a.s.cps * C]));
+}
+
+template <typename IT, typename OT, int DK, int DV>
+__global__ __launch_bounds__(walk_threads(DK, DV), simd_waves<IT>(max_of(DK, DV))) void walks_kernel(
+    OutArgs q, OutArgs k, OutArgs v, int n, BorderArgs b) {
+  const Lds m = dynamic_lds();
+  const int walk = blockIdx.x / n, flat = blockIdx.x % n;
+  if ((int)blockIdx.x >= 3 * n) {
+    border_dot<walk_threads(DK, DV)>(b, blockIdx.x - 3 * n, reinterpret_cast<double*>(m.p));
+    return;
+  }
+  if ((int)threadIdx.x >= 64 * waves(walk < 2 ? DK : DV)) return;
+  if (walk == 0) out_walk<IT, OT, DV, DK, false, kPairs>(q, flat, m);
+  else if (walk == 1) out_walk<IT, OT, DV, DK, true, kDots>(k, flat, m);
+  else out_walk<IT, IT, DK, DV, true, kNone>(v, flat, m);
+}
+
+struct DecayGradArgs {
+  const float *g, *x, *y, *m;
+  const float* S;      // [BH][nseg + 1][N]: slot nseg = the last state
+  const double* border;
+  const float *S0, *dS0;  // [BH][N]: the first state and its gradient; S0 null: zero; dS0 null: not known
+  const float* dS;     // [BH][N] or null: gradient of the last state
+  float* dg;
+  int L, BH, N;
+  Split s;
+};
+
+constexpr int kGradThreads = 1024;
+
 // One workgroup per (head, segment).
-static __global__ __launch_bounds__(kGradThreads) void decay_grad_kernel(DecayGradArgs a) {
+__device__ __forceinline__ void decay_grad(const DecayGradArgs& a, int block) {
   __shared__ double part[kGradThreads / 64], tx[kMaxChunks], ty[kMaxChunks], carry[kMaxChunks];
-  const int bh = blockIdx.x / a.s.nseg, seg = blockIdx.x % a.s.nseg;
+  const int bh = block / a.s.nseg, seg = block % a.s.nseg;
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
   const bool end = seg == a.s.nseg - 1;
   const size_t row0 = ((size_t)bh * a.s.nc + c0) * C, tok0 = (size_t)bh * a.L;
-  const float* S = a.S + (size_t)bh * (a.s.nseg + 1) * a.N;
-  const float* X = a.X + (size_t)bh * a.s.nseg * a.N;
-  // The reversed walk's states are gradients of the state after the token
-  // behind them; that token's decay stands between.
-  const auto first_decay = [&](int c) { return (double)exp2_hw((float)log2_decay(a.g[tok0 + (size_t)c * C])); };
-
   // <state that leaves the segment, its gradient>, and the same at its start
   // (nothing is known there only if S0 is given and dS0 not asked for).
   double held = 0.0, enter = 0.0;
   bool known = true;
-  if (end) {
-    if (a.dS) held = dot_states(S + (size_t)a.s.nseg * a.N, a.dS + (size_t)bh * a.N, a.N, part);
-  } else {
-    held = dot_states(S + (size_t)(seg + 1) * a.N, X + (size_t)seg * a.N, a.N, part) * first_decay(c1);
+  if (!end) {
+    held = a.border[(size_t)bh * a.s.nseg + seg + 1];
+  } else if (a.dS) {
+    held = dot_states<kGradThreads>(a.S + ((size_t)bh * (a.s.nseg + 1) + a.s.nseg) * a.N, a.dS + (size_t)bh * a.N, a.N, part);
   }
   if (seg > 0) {
-    enter = dot_states(S + (size_t)seg * a.N, X + (size_t)(seg - 1) * a.N, a.N, part) * first_decay(c0);
+    enter = a.border[(size_t)bh * a.s.nseg + seg];
   } else if (a.S0) {
     known = a.dS0 != nullptr;
-    if (known) enter = dot_states(a.S0 + (size_t)bh * a.N, a.dS0 + (size_t)bh * a.N, a.N, part);
+    if (known) enter = dot_states<kGradThreads>(a.S0 + (size_t)bh * a.N, a.dS0 + (size_t)bh * a.N, a.N, part);
   }
 
   for (int i = w; i < n; i += kGradThreads / 64) {
@@ -167,19 +188,34 @@ static __global__ __launch_bounds__(kGradThreads) void decay_grad_kernel(DecayGr
 }
 
 // out[u] = sum over the group's members of in[u grp + m], rounded once.
+struct GroupSumArgs {
+  const float *dq, *dk;
+  void *out_q, *out_k;
+  size_t per_head, n;  // elements of a head, of an output
+  int grp;
+};
 template <typename OT>
-__global__ __launch_bounds__(256) void group_sum_kernel(const float* in, OT* out, size_t per_head, int grp, size_t n) {
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  const size_t u = i / per_head;
-  const float* p = in + u * grp * per_head + (i - u * per_head);
+__device__ __forceinline__ void group_sum(const GroupSumArgs& a, size_t i4) {
+  const size_t i = i4 * 4 < a.n ? i4 * 4 : i4 * 4 - a.n;
+  if (i >= a.n) return;
+  const bool first = i4 * 4 < a.n;
+  const size_t u = i / a.per_head;
+  const float* p = (first ? a.dq : a.dk) + u * a.grp * a.per_head + (i - u * a.per_head);
   f32x4 x = *reinterpret_cast<const f32x4*>(p);
-  for (int m = 1; m < grp; ++m) x += *reinterpret_cast<const f32x4*>(p + (size_t)m * per_head);
-  store4(out + i, x);
+  for (int m = 1; m < a.grp; ++m) x += *reinterpret_cast<const f32x4*>(p + (size_t)m * a.per_head);
+  store4(static_cast<OT*>(first ? a.out_q : a.out_k) + i, x);
+}
+
+// What is left after the walks: the decay's gradient (the first `ng`
+// workgroups) and the sums over shared heads.
+template <typename OT>
+__global__ __launch_bounds__(kGradThreads) void finish_kernel(DecayGradArgs g, int ng, GroupSumArgs s) {
+  if ((int)blockIdx.x < ng) decay_grad(g, blockIdx.x);
+  else group_sum<OT>(s, (size_t)(blockIdx.x - ng) * kGradThreads + threadIdx.x);
 }
 
 struct BwdWs {
-  size_t S, X, dS, dX, x, y, m, dq, dk, total;  // byte offsets
+  size_t S, X, dS, dX, border, x, y, m, dq, dk, total;  // byte offsets
 };
 static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v) {
   const size_t BH = (size_t)B * H, N = (size_t)d_k * d_v * 4;
@@ -196,6 +232,7 @@ static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v) {
   w.X = take(s.nseg > 1 ? BH * s.nseg * N : 0);
   w.dS = take(BH * s.nseg * 8);
   w.dX = take(BH * s.nseg * 8);
+  w.border = take(BH * s.nseg * 8);
   w.x = take(rows);
   w.y = take(rows);
   w.m = take(rows);
@@ -243,24 +280,19 @@ static hipError_t backward(const LinearBwdArgs& a) {
   constexpr int lds = walks_lds<IT, OT, DK, DV>();
   static_assert(lds <= (sizeof(IT) == 2 ? 80 : 160) * 1024, "two bf16 workgroups share a CU's LDS");
   const int n = (int)items(BH, grp, s.nseg);
-  e = launch(&walks_kernel<IT, OT, DK, DV>, kSlotLinearBwd, 3LL * n, walk_threads(DK, DV), lds, a.stream, q, k, v, n);
+  BorderArgs b{f(o.S), f(o.X), a.log_decay, d(o.border), a.L, N, s};
+  const long long borders = a.dlog_decay ? (long long)BH * (s.nseg - 1) : 0;
+  e = launch(&walks_kernel<IT, OT, DK, DV>, kSlotLinearBwd, 3LL * n + borders, walk_threads(DK, DV), lds, a.stream, q,
+             k, v, n, b);
   if (e != hipSuccess) return e;
-  if (shared) {
-    const size_t n = (size_t)a.B * a.H_qk * a.L * DK, per = (size_t)a.L * DK;
-    const dim3 grid((unsigned)((n / 4 + 255) / 256));
-    for (int i = 0; i < 2; ++i) {
-      hipLaunchKernelGGL((group_sum_kernel<IT>), grid, dim3(256), 0, a.stream, f(i ? o.dk : o.dq),
-                         static_cast<IT*>(i ? a.dk : a.dq), per, grp, n);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-  }
-  if (!a.dlog_decay) return hipSuccess;
-  DecayGradArgs g{a.log_decay, f(o.x), f(o.y), f(o.m), f(o.S), f(o.X), a.S0, a.dS0, a.dS_final, a.dlog_decay, a.L, BH, N, s};
-  prof_mark(kSlotLinearBwd, false, a.stream);
-  hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(BH * s.nseg)), dim3(kGradThreads), 0, a.stream, g);
-  e = hipGetLastError();
-  prof_mark(kSlotLinearBwd, true, a.stream);
-  return e;
+  if (!a.dlog_decay && !shared) return hipSuccess;
+  DecayGradArgs g{a.log_decay, f(o.x), f(o.y), f(o.m), f(o.S), d(o.border), a.S0, a.dS0, a.dS_final, a.dlog_decay,
+                  a.L, BH, N, s};
+  const size_t per = (size_t)a.L * DK, total = shared ? (size_t)a.B * a.H_qk * per : 0;
+  GroupSumArgs sum{f(o.dq), f(o.dk), a.dq, a.dk, per, total, grp};
+  const int ng = a.dlog_decay ? BH * s.nseg : 0;
+  const long long blocks = ng + (long long)((2 * total / 4 + kGradThreads - 1) / kGradThreads);
+  return launch(&finish_kernel<IT>, kSlotLinearBwd, blocks, kGradThreads, 0, a.stream, g, ng, sum);
 }
 
 template <int DK, int DV>
