@@ -78,6 +78,10 @@ __device__ __forceinline__ double log2_decay(float g) {
   return x < kWipe2 ? kWipe2 : x;
 }
 
+// x after a decay by f.  One by 0 (a wipe) drops x whatever it is: the state of a
+// call whose first token wipes it may be memory never written.
+__device__ __forceinline__ f32x4 decayed(f32x4 x, float f) { return f == 0.f ? zero4() : x * f; }
+
 // ---- operands ------------------------------------------------------------------
 //
 // A fragment holds, per lane (g = lane / 16, i = lane % 16), the 8 values of
@@ -640,7 +644,7 @@ __device__ __forceinline__ void combine(const CombineArgs& a) {
       if (i0 + j < steps) {
         const int s = REV ? a.nseg - 1 - (i0 + j) : i0 + j;
         *reinterpret_cast<f32x4*>(S + (size_t)s * a.N) = run;
-        run = run * exp2_hw((float)d[s]) + x[j];
+        run = decayed(run, exp2_hw((float)d[s])) + x[j];
       }
     }
   }
@@ -855,6 +859,8 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   f32x4 st[DK / 16];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
+  // (A wipe in front of the first row: see decayed().)
+  if (!REV && g && exp2_hw((float)log2_decay(g[c0 * C])) == 0.f) S = nullptr;
   load_state<DK, DV, TRANS>(st, S);
   wait_loads();
   __syncthreads();

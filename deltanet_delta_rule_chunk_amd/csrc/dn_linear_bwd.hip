@@ -66,14 +66,15 @@ struct BorderArgs {
   Split s;
 };
 
-// <u, v> over T threads, every thread's answer.
+// <u, v> over T threads, every thread's answer.  (Where v is 0, u may be
+// anything: the state of a call that wipes it first has no gradient.)
 template <int T>
 __device__ __forceinline__ double dot_states(const float* u, const float* v, int n, double* part) {
   double acc = 0.0;
   for (int i = threadIdx.x * 4; i < n; i += T * 4) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(u + i), b = *reinterpret_cast<const f32x4*>(v + i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc += (double)a[e] * (double)b[e];
+    for (int e = 0; e < 4; ++e) acc += b[e] == 0.f ? 0.0 : (double)a[e] * (double)b[e];
   }
   acc = lane_value(wave_scan(acc), 63);
   __syncthreads();
@@ -91,9 +92,8 @@ __device__ __forceinline__ void border_dot(const BorderArgs& a, int i, double* p
                                  a.N, part);
   // The reversed walk's states are gradients of the state after the token
   // behind them; that token's decay stands between.
-  if (threadIdx.x == 0)
-    a.border[(size_t)bh * a.s.nseg + s] =
-        d * (double)exp2_hw((float)log2_decay(a.g[(size_t)bh * a.L + (size_t)s * a.s.cps * C]));
+  const float f = exp2_hw((float)log2_decay(a.g[(size_t)bh * a.L + (size_t)s * a.s.cps * C]));
+  if (threadIdx.x == 0) a.border[(size_t)bh * a.s.nseg + s] = f == 0.f ? 0.0 : d * (double)f;
 }
 
 template <typename IT, typename OT, int DK, int DV>

@@ -40,6 +40,11 @@ __global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, c
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = to_f32(v[(size_t)bh * DV + c0 + cg * 4 + e]);
   const float a = g ? expf(g[bh]) : 1.f;
+  // A wipe drops the state whatever it holds (memory never written, say).
+  if (a == 0.f) {
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) s[i] = 0.f;
+  }
   __syncthreads();
   vf4 acc = 0.f;
 #pragma unroll

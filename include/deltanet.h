@@ -316,10 +316,11 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
  *              head its own).
  *   v        : [B, H, L, d_v] in_dtype
  *   log_decay: [B, H, L] fp32, the decay's natural logarithm, or NULL (no
- *              decay).  0 keeps the state, -inf wipes it exactly: a log decay
- *              of -inf at its first token separates a document from the one
- *              before it in the same row.  Values above 0 are not checked
- *              (the product is then no decay).
+ *              decay).  0 keeps the state, -inf wipes it: a log decay of -inf
+ *              at its first token separates a document from the one before it
+ *              in the same row.  At a call's first token it drops S0 whatever
+ *              that holds, infinities or memory never written too.  Values
+ *              above 0 are not checked (the product is then no decay).
  *   S0       : [B, H, d_k, d_v] fp32 or NULL (zero state)
  *   o        : [B, H, L, d_v] out_dtype, written
  *   S_final  : [B, H, d_k, d_v] fp32 or NULL; may be the buffer of S0.
@@ -327,8 +328,8 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
  * The result does not depend on how the sequence is cut into chunks, so
  * there is no chunk argument.  bf16 inputs run on the bf16 matrix cores, every
  * fp32 operand as a sum of bf16 pieces; fp32 inputs on the fp32 ones.  A
- * non-finite q, k or v row makes the outputs of its 64-token chunk and the
- * states after it non-finite.  workspace, workspace_bytes, stream, status
+ * non-finite q, k or v row makes outputs of its 64-token chunk (tokens 64 n to
+ * 64 n + 63) and, from k or v, the states after it non-finite.  workspace, workspace_bytes, stream, status
  * codes and every other rule: as for deltanet_chunk_fwd; the workspace holds
  * one fp32 state per segment that the sequence is cut into, and may be 0
  * bytes.

@@ -385,6 +385,26 @@ def test_non_finite_rows_stay_in_their_chunk_and_after(gpu_lib):
     assert not torch.isfinite(o[:, :, 130:]).any() and not torch.isfinite(S).any()
 
 
+@pytest.mark.parametrize("L,dt,grp", [(1, "bf16", 1), (64, "f32", 1), (200, "bf16", 2), (900, "bf16", 1), (900, "f32", 3)])
+@pytest.mark.parametrize("junk", [float("nan"), float("inf")])
+def test_a_wipe_drops_any_state(gpu_lib, L, dt, grp, junk):
+    """A wipe at a sequence's first token: what the state's buffer held, memory
+    never written among it, does not show, in any output or gradient."""
+    x = _gpu(_inputs(29, 1, 2, grp, L, 128, 64, dt, True, "usual"))
+    x["g"][..., 0] = -float("inf")
+
+    def call(S0):
+        S = S0.clone()
+        row = [x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g")]
+        return (*N.linear_chunk_fwd(x["q"], x["k"], x["v"], x["g"], S0),
+                *N.linear_chunk_bwd(x["q"], x["k"], x["v"], x["g"], S0, x["dO"], x["dS"]),
+                N.linear_decode_step(*row, S), S)
+
+    want, got = call(torch.zeros_like(x["S0"])), call(torch.full_like(x["S0"], junk))
+    for a, b in zip(want, got):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
 def test_profile_slots(gpu_lib):
     x = _gpu(_inputs(27, 1, 2, 1, 600, 64, 64, "bf16", True, "usual"))
     N.profile_start()
