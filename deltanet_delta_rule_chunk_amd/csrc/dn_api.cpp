@@ -157,8 +157,8 @@ int check_rows(const void* p, const long long* strides, int B, int H, int L, int
   for (int i = 0; i < 3; ++i) {
     if (n[i] == 1) continue;  // this stride is not used
     if (s[i] < 0) return DN_ERR_BAD_SHAPE;
-    if (s[i] * (long long)size % 16) return DN_ERR_MISALIGNED;
     if (s[i] > (1LL << 60) / n[i]) return DN_ERR_UNSUPPORTED;
+    if (s[i] * (long long)size % 16) return DN_ERR_MISALIGNED;
     last += (n[i] - 1) * s[i];
   }
   out->bytes = (size_t)(last + d) * size;
@@ -809,7 +809,8 @@ int deltanet_qk_norm_rope(const void* q_raw, const long long* q_strides, const v
 size_t deltanet_qk_norm_rope_bwd_workspace_bytes(int B, int H_q, int H_k, int L, int d_k,
                                                  dn_dtype dtype) {
   if (B < 1 || H_q < 1 || H_k < 0 || L < 0 || !dim_ok(d_k) || !dtype_ok(dtype)) return 0;
-  return dn::qk_norm_rope_bwd_workspace_bytes(B, L, d_k);
+  if ((int64_t)H_q + H_k > 65535) return 0;
+  return dn::qk_norm_rope_bwd_workspace_bytes(B, H_q + H_k, L, d_k);
 }
 
 int deltanet_qk_norm_rope_bwd(const void* q_raw, const long long* q_strides, const void* k_raw,
@@ -835,7 +836,7 @@ int deltanet_qk_norm_rope_bwd(const void* q_raw, const long long* q_strides, con
   if (L > 0 && (!dq_hat || !dq_raw || (H_k > 0 && (!dk_hat || !dk_raw)))) return DN_ERR_NULL_ARG;
   if (any_misaligned({dq_hat, dk_hat, dq_raw, dk_raw, dq_weight, dk_weight, workspace})) return DN_ERR_MISALIGNED;
   const size_t row = (size_t)B * L * d_k * size, wb = (size_t)d_k * sizeof(float);
-  const size_t need = dn::qk_norm_rope_bwd_workspace_bytes(B, L, d_k);
+  const size_t need = dn::qk_norm_rope_bwd_workspace_bytes(B, H_q + H_k, L, d_k);
   const Span in[] = {{q_raw, rows[0].bytes}, {k_raw, rows[1].bytes}, {q_weight, wb}, {k_weight, wb},
                      {positions, pos}, {inv_freq, (size_t)d_rot / 2 * sizeof(float)},
                      {dq_hat, row * H_q}, {dk_hat, row * H_k}};

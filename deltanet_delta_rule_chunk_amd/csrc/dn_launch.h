@@ -191,7 +191,7 @@ struct QkNormRopeArgs {
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a);
 long long qk_norm_rope_max_tokens(int heads, int d);
-size_t qk_norm_rope_bwd_workspace_bytes(int B, int L, int d);
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int heads, int L, int d);
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeArgs& a);
 
 // The fixed per-GPU scratch area of the allocation-free forward

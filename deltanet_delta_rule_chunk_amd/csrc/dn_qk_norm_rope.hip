@@ -19,6 +19,15 @@
 // hold elements behind d_rot.  A group of lanes keeps its token and walks
 // over heads, so a token's 4 angles per lane are formed once for all of them.
 //
+// Heads.  A workgroup takes 4 of them at most, and the workgroups that follow
+// it the next ones of the same tokens: together they read adjacent parts of a
+// fused projection's rows at one time.  32 + 32 heads of 128 bf16 elements, 65536
+// tokens out of rows of 3 x 4096: 392 us (5.5 TB/s); with 2 heads 475, with 6
+// 402, 8 429, 16 448, all 64 471 (few workgroups, each far from the others'
+// rows).  The gradient at 16384 tokens: 179 us (4.5 TB/s) against 186 with all
+// heads, at 2048 tokens of 12 + 12 heads of 64 fp32 elements 15 against 31 (few
+// tokens alone do not fill the card).
+//
 // Angles.  p inv_freq reaches millions of turns; it is taken in turns in
 // fp64, its whole turns dropped there, and only the rest (below half a turn)
 // goes to fp32 sine and cosine.
@@ -152,16 +161,18 @@ __global__ __launch_bounds__(NT) void forward_kernel(QkNormRopeArgs a, long long
   }
 }
 
-// The gradient.  Workgroups walk over blocks of tokens; each leaves one
-// partial row of dw for q and one for k.
+// The gradient.  Workgroups take a block of heads and walk over blocks of
+// tokens; each leaves one partial row of dw for q and one for k.
 template <int D, typename T>
-__global__ __launch_bounds__(NT) void backward_kernel(QkNormRopeArgs a, long long tokens, float* partial) {
+__global__ __launch_bounds__(NT) void backward_kernel(QkNormRopeArgs a, long long tokens, int hpb, int blocks_h, float* partial) {
   constexpr int LPR = D / 8, TPB = NT / LPR;
   __shared__ float red[TPB][D];
   const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR;
   const Place p = place_of(lane, a.d_rot, a.interleaved);
   f32x4 acc[2][2] = {{zero4(), zero4()}, {zero4(), zero4()}};
-  for (long long t0 = (long long)blockIdx.x * TPB; t0 < tokens; t0 += (long long)gridDim.x * TPB) {
+  const int h0 = blockIdx.x % blocks_h * hpb, h1 = min(h0 + hpb, a.H[0] + a.H[1]);
+  const long long step = gridDim.x / blocks_h;  // a whole number
+  for (long long t0 = blockIdx.x / blocks_h * TPB; t0 < tokens; t0 += step * TPB) {
     const long long tok = t0 + row;
     const bool on = tok < tokens;
     const int b = on ? (int)(tok / a.L) : 0, l = on ? (int)(tok % a.L) : 0;
@@ -169,12 +180,14 @@ __global__ __launch_bounds__(NT) void backward_kernel(QkNormRopeArgs a, long lon
     angles(a, p, b, l, c, s);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
+      const int first = part ? max(h0 - a.H[0], 0) : h0, end = part ? h1 - a.H[0] : min(h1, a.H[0]);
+      if (first >= end) continue;
       f32x4 w0{1.f, 1.f, 1.f, 1.f}, w1 = w0;
       if (a.weight[part]) w0 = load4(a.weight[part] + p.o0), w1 = load4(a.weight[part] + p.o1);
       const T* x = static_cast<const T*>(a.x[part].p) + (long long)b * a.x[part].sb + (long long)l * a.x[part].sl;
       T* dx = static_cast<T*>(const_cast<void*>(a.dx[part].p)) + (long long)b * a.dx[part].sb + (long long)l * a.dx[part].sl;
       const T* dy = static_cast<const T*>(a.y[part]) + ((size_t)b * a.H[part] * a.L + l) * D;
-      for (int h = 0; h < a.H[part]; ++h) {
+      for (int h = first; h < end; ++h) {
         const T* xr = x + (long long)h * a.x[part].sh;
         const T* dr = dy + (size_t)h * a.L * D;
         f32x4 x0 = load4(xr + p.o0), x1 = load4(xr + p.o1);
@@ -242,23 +255,33 @@ static long long token_blocks(long long tokens, int d) {
   const int tpb = NT / (d / 8);
   return (tokens + tpb - 1) / tpb;
 }
-// Workgroups of the backward: each leaves partial rows to add up.
-static int backward_blocks(long long tokens, int d) {
-  const long long n = token_blocks(tokens, d);
-  return (int)(n < 1024 ? n : 1024);
+// Heads per workgroup and blocks of heads, with `n` blocks of heads wanted at
+// the least.
+struct HeadSplit {
+  int hpb, blocks;
+};
+static HeadSplit split_heads(int H, long long n) {
+  if (n < (H + 3) / 4) n = (H + 3) / 4;
+  if (n > H) n = H;
+  const int hpb = (int)((H + n - 1) / n);
+  return HeadSplit{hpb, (H + hpb - 1) / hpb};
+}
+// Workgroups of the backward: each leaves partial rows to add up, so about
+// 1024 of them at most.
+static int backward_blocks(long long tokens, int H, int d) {
+  const int bh = split_heads(H, 1).blocks;
+  const long long tb = token_blocks(tokens, d), most = bh < 1024 ? 1024 / bh : 1;
+  return (int)(tb < most ? tb : most) * bh;
 }
 
 template <int D, typename T>
 static hipError_t forward(const QkNormRopeArgs& a) {
   const long long tokens = (long long)a.B * a.L, tb = token_blocks(tokens, D);
   const int H = a.H[0] + a.H[1];
-  // Heads per workgroup: all of them once there are blocks of tokens enough
-  // for every CU; fewer, down to one, to spread few tokens.
-  long long per = (2048 + tb - 1) / tb;
-  if (per > H) per = H;
-  const int hpb = (int)((H + per - 1) / per), bh = (H + hpb - 1) / hpb;
+  // Fewer heads per workgroup, down to one, spread few tokens.
+  const HeadSplit h = split_heads(H, (2048 + tb - 1) / tb);
   prof_mark(kSlotQkNormRope, false, a.stream);
-  hipLaunchKernelGGL((forward_kernel<D, T>), dim3((unsigned)(tb * bh)), dim3(NT), 0, a.stream, a, tokens, hpb, bh);
+  hipLaunchKernelGGL((forward_kernel<D, T>), dim3((unsigned)(tb * h.blocks)), dim3(NT), 0, a.stream, a, tokens, h.hpb, h.blocks);
   hipError_t e = hipGetLastError();
   prof_mark(kSlotQkNormRope, true, a.stream);
   return e;
@@ -267,12 +290,13 @@ static hipError_t forward(const QkNormRopeArgs& a) {
 template <int D, typename T>
 static hipError_t backward(const QkNormRopeArgs& a) {
   const long long tokens = (long long)a.B * a.L;
-  const int n = backward_blocks(tokens, D);
+  const int H = a.H[0] + a.H[1], n = backward_blocks(tokens, H, D);
+  const HeadSplit h = split_heads(H, 1);
   float* partial = static_cast<float*>(a.workspace);
   prof_mark(kSlotQkNormRopeBwd, false, a.stream);
   hipError_t e = hipSuccess;
   if (n > 0) {
-    hipLaunchKernelGGL((backward_kernel<D, T>), dim3((unsigned)n), dim3(NT), 0, a.stream, a, tokens, partial);
+    hipLaunchKernelGGL((backward_kernel<D, T>), dim3((unsigned)n), dim3(NT), 0, a.stream, a, tokens, h.hpb, h.blocks, partial);
     e = hipGetLastError();
   }
   if (e == hipSuccess && (a.dw[0] || a.dw[1])) {
@@ -295,8 +319,8 @@ hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a) {
   return a.d == 64 ? qkr::forward<64, float>(a) : qkr::forward<128, float>(a);
 }
 
-size_t qk_norm_rope_bwd_workspace_bytes(int B, int L, int d) {
-  return (size_t)qkr::backward_blocks((long long)B * L, d) * 2 * d * sizeof(float);
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int heads, int L, int d) {
+  return (size_t)qkr::backward_blocks((long long)B * L, heads, d) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeArgs& a) {

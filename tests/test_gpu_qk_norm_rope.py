@@ -34,6 +34,7 @@ CASES = [
     (1, 2, 2, 40, 128, 104, [0, 50, 1, 1], True, False, False, "f32"),
     (5, 9, 3, 129, 64, 16, None, False, True, True, "bf16"),
     (1, 32, 8, 2500, 64, 64, None, False, True, True, "bf16"),
+    (1, 41, 23, 2100, 64, 32, None, True, True, True, "bf16"),  # several token blocks per workgroup
 ]
 
 
