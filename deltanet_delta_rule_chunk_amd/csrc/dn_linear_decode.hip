@@ -5,9 +5,13 @@
 // does 4 d_k d_v flops on it.  Nothing in the step waits for a sum over the
 // state: each element is read, updated, multiplied by its q and written.
 //
-// A work item is a head, or a slice of a head's columns; thread (rg, cg) of a
-// 256-thread workgroup holds 4 adjacent columns of rows rg, rg + ROWG, ....
-// The partial sums of o meet in LDS.
+// A workgroup takes a head; thread (rg, cg) of its 256 holds 4 adjacent columns
+// of rows rg, rg + ROWG, ....  The partial sums of o meet in LDS.  All of a
+// thread's loads are under way at once, and the new state is stored past the
+// caches: 8192 heads of 128 x 128 (256 sequences of 32) take 160 us, 6.7 TB/s.
+// Cutting a head's columns over 4 workgroups, for calls of few heads, made 32
+// heads no faster (6.4 us against 6.3 between two events) and 4096 slower (102
+// against 87).
 
 #include "dn_common.h"
 #include "dn_launch.h"
@@ -17,17 +21,17 @@ namespace lin {
 
 typedef float vf4 __attribute__((ext_vector_type(4)));
 
-template <int DK, int DV, int NSL, typename IT, typename OT>
+template <int DK, int DV, typename IT, typename OT>
 __global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, const IT* __restrict__ k,
                                                      const IT* __restrict__ v, const float* __restrict__ g,
                                                      float* __restrict__ S, OT* __restrict__ o, int grp) {
-  constexpr int W = DV / NSL, COLG = W / 4, ROWG = 256 / COLG, RPT = DK / ROWG;
-  static_assert(COLG * 4 * NSL == DV && RPT * ROWG == DK, "tile shape");
+  constexpr int COLG = DV / 4, ROWG = 256 / COLG, RPT = DK / ROWG;
+  static_assert(COLG * 4 == DV && RPT * ROWG == DK, "tile shape");
   __shared__ float ks[DK], qs[DK];
   __shared__ vf4 red[ROWG][COLG];
   const int tid = threadIdx.x, cg = tid % COLG, rg = tid / COLG;
-  const int bh = blockIdx.x / NSL, c0 = blockIdx.x % NSL * W;
-  float* const Sh = S + (size_t)bh * (DK * DV) + c0 + cg * 4;
+  const int bh = blockIdx.x;
+  float* const Sh = S + (size_t)bh * (DK * DV) + cg * 4;
   vf4 s[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) s[i] = *reinterpret_cast<const vf4*>(Sh + (size_t)(rg + i * ROWG) * DV);
@@ -38,7 +42,7 @@ __global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, c
   }
   vf4 x;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = to_f32(v[(size_t)bh * DV + c0 + cg * 4 + e]);
+  for (int e = 0; e < 4; ++e) x[e] = to_f32(v[(size_t)bh * DV + cg * 4 + e]);
   const float a = g ? expf(g[bh]) : 1.f;
   // A wipe drops the state whatever it holds (memory never written, say).
   if (a == 0.f) {
@@ -56,11 +60,11 @@ __global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, c
   }
   red[rg][cg] = acc;
   __syncthreads();
-  if (tid < W) {
+  if (tid < DV) {
     float y = 0.f;
 #pragma unroll
     for (int r = 0; r < ROWG; ++r) y += red[r][tid / 4][tid % 4];
-    o[(size_t)bh * DV + c0 + tid] = from_f32<OT>(y);
+    o[(size_t)bh * DV + tid] = from_f32<OT>(y);
   }
 }
 
@@ -68,13 +72,9 @@ template <int DK, int DV, typename IT, typename OT>
 static hipError_t launch(const LinearDecodeArgs& a) {
   const int BH = a.B * a.H;
   prof_mark(kSlotLinearDecode, false, a.stream);
-#define DN_LAUNCH(NSL)                                                                            \
-  hipLaunchKernelGGL((decode_kernel<DK, DV, NSL, IT, OT>), dim3((unsigned)BH * NSL), dim3(256), 0, \
-                     a.stream, static_cast<const IT*>(a.q), static_cast<const IT*>(a.k),          \
-                     static_cast<const IT*>(a.v), a.log_decay, a.S, static_cast<OT*>(a.o), a.H / a.H_qk)
-  if (BH < 512) DN_LAUNCH(4);
-  else DN_LAUNCH(1);
-#undef DN_LAUNCH
+  hipLaunchKernelGGL((decode_kernel<DK, DV, IT, OT>), dim3((unsigned)BH), dim3(256), 0, a.stream,
+                     static_cast<const IT*>(a.q), static_cast<const IT*>(a.k), static_cast<const IT*>(a.v),
+                     a.log_decay, a.S, static_cast<OT*>(a.o), a.H / a.H_qk);
   hipError_t e = hipGetLastError();
   prof_mark(kSlotLinearDecode, true, a.stream);
   return e;
