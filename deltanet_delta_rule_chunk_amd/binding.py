@@ -16,6 +16,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdeltanet.so")
@@ -642,6 +643,7 @@ class _LinearRule(torch.autograd.Function):
         return o, S_final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dO, dS_final):
         q, k, v, log_decay, S0 = ctx.saved_tensors
         want_dS0 = S0 is not None and ctx.needs_input_grad[4]
@@ -855,6 +857,7 @@ class _RotaryQK(torch.autograd.Function):
                             k_weight=k_weight, **how)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_hat, dk_hat):
         q_raw, k_raw, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         return (*qk_norm_rope_bwd(q_raw, k_raw, positions, inv_freq, dq_hat.contiguous(),
