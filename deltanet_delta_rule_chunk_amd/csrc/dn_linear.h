@@ -41,12 +41,19 @@
 // it reaches an fp32 result through long sums: the rows added to a state that is
 // a result or enters a segment, the state read for an fp32 output or for what
 // the decay's gradient is summed from; 2 pieces (16 bits) for rows and state
-// that only reach bf16 outputs, whose own rounding is 256 times coarser, and for P, whose sums span one chunk (a third
-// piece of P would cost the second workgroup of each CU its LDS; it leaves
-// 2^-17 of a term).  fp32 inputs run the same
-// kernels on the fp32 matrix instruction, with nothing split.  Log decays are
-// summed in fp64: a difference of two sums keeps the accuracy of the short
+// that only reach bf16 outputs, whose own rounding is 256 times coarser, and for
+// P, whose sums span one chunk (a third piece of P would cost the second
+// workgroup of each CU its LDS; it leaves 2^-17 of a term).  fp32 inputs run the
+// same kernels on the fp32 matrix instruction, with nothing split.  Log decays
+// are summed in fp64: a difference of two sums keeps the accuracy of the short
 // sum between them however long the chunk's own is.
+//
+// What bounds it.  32 heads of 128 x 128, bf16, L = 65536: segment sums 233 us (reads
+// 1.0 GB, 4.4 TB/s), outputs 475 us (2.2 GB, 4.6 TB/s): near the rate of HBM (a
+// copy reaches 5.2), with the matrix instructions busy for 46% of the time (740
+// TFLOP/s as executed) and about as many cycles of vector work (pieces,
+// decays) beside them, which they hardly overlap.  At few rows, the latency of a
+// chunk: about 4 us, two barriers with P's way through LDS between them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -422,9 +429,12 @@ struct Split {
   int nc, cps, nseg;
 };
 
-// Enough segments for two workgroups on each of the 256 CUs, none of them
-// shorter than kMinChunks chunks (a segment costs a state's write and two
-// reads, 4 d_k d_v bytes each, against the rows it spares a walk).
+// Enough segments for two workgroups on each of the 256 CUs (32 heads of 128 x 128
+// at L = 65536: 711 us of kernels; with 1024 workgroups 798, 384 798, 256 818),
+// none of them shorter than kMinChunks chunks (a segment costs a state's
+// write and two reads, 4 d_k d_v bytes each, against the rows it spares a walk;
+// 24 heads of 64 x 128 at L = 1501, forward and backward: 98 us, with 2 chunks 112,
+// with 3 95, but 2 fp32 heads of 4 chunks 90 with 3, against 69 in one segment).
 // None is longer than kMaxChunks, which bounds how far the decay's gradient is
 // carried from an exact value.
 constexpr int kWorkgroups = 512, kMinChunks = 4, kMaxChunks = 256;
