@@ -706,11 +706,10 @@ def _check_rows(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
-_Strides = ctypes.c_longlong * 3
-
-
-def _strides(t: torch.Tensor):
-    return _Strides(*t.stride()[:3])
+@functools.lru_cache(maxsize=1024)
+def _strides(s):
+    """The C array of a row tensor's strides (of all but the last dimension)."""
+    return (ctypes.c_longlong * 3)(*s[:3])
 
 
 @functools.lru_cache(maxsize=256)
@@ -751,7 +750,7 @@ def _qk_setup(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, sections):
             raise ValueError("several position axes need sections")
         if d_rot:
             pos, inv = positions.data_ptr(), inv_freq.data_ptr()
-    lead = (q_raw.data_ptr(), _Strides(*qst[:3]), k_raw.data_ptr(), _Strides(*kst[:3]),
+    lead = (q_raw.data_ptr(), _strides(qst), k_raw.data_ptr(), _strides(kst),
             _ptr(q_weight), _ptr(k_weight), pos, inv, counts, axes)
     return (B, H_q, H_k, L, d, d_rot), lead
 
@@ -837,8 +836,8 @@ def qk_norm_rope_bwd(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Option
     need = _qk_bwd_workspace_bytes(B, H_q, H_k, L, d, _code(t))
     keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
     st = lib.deltanet_qk_norm_rope_bwd(*lead, dq_hat.data_ptr(), dk_hat.data_ptr(),
-                                       dq_raw.data_ptr(), _strides(dq_raw), dk_raw.data_ptr(),
-                                       _strides(dk_raw), _ptr(dqw), _ptr(dkw), B, H_q, H_k, L, d,
+                                       dq_raw.data_ptr(), _strides(dq_raw.stride()), dk_raw.data_ptr(),
+                                       _strides(dk_raw.stride()), _ptr(dqw), _ptr(dkw), B, H_q, H_k, L, d,
                                        d_rot, int(norm), int(interleaved), eps, _code(t), ws,
                                        ws_bytes, _stream(dev, stream))
     if st != DN_OK:
