@@ -329,10 +329,11 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
  * there is no chunk argument.  bf16 inputs run on the bf16 matrix cores, every
  * fp32 operand as a sum of bf16 pieces; fp32 inputs on the fp32 ones.  A
  * non-finite q, k or v row makes outputs of its 64-token chunk (tokens 64 n to
- * 64 n + 63) and, from k or v, the states after it non-finite.  workspace, workspace_bytes, stream, status
- * codes and every other rule: as for deltanet_chunk_fwd; the workspace holds
- * one fp32 state per segment that the sequence is cut into, and may be 0
- * bytes.
+ * 64 n + 63, earlier ones too) and, from k or v, the states after it
+ * non-finite: padding has to be finite.  workspace, workspace_bytes, stream,
+ * status codes and every other rule: as for deltanet_chunk_fwd; the workspace
+ * holds one fp32 state per segment that the sequence is cut into, and may be
+ * 0 bytes.
  */
 int deltanet_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* log_decay,
                               const float* S0, void* o, float* S_final,
