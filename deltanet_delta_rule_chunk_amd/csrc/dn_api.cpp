@@ -704,7 +704,7 @@ size_t deltanet_linear_chunk_fwd_workspace_bytes(int B, int H, int H_qk, int L, 
                                                  dn_dtype in_dtype) {
   LinearSizes s;
   if (check_linear_shape(B, H, H_qk, L, d_k, d_v, in_dtype, DN_F32, &s) != DN_OK) return 0;
-  return dn::linear_workspace_bytes(B, H, L, d_k, d_v);
+  return dn::linear_workspace_bytes(B, H, L, d_k, d_v, in_dtype);
 }
 
 int deltanet_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -716,7 +716,7 @@ int deltanet_linear_chunk_fwd(const void* q, const void* k, const void* v, const
   if (st != DN_OK) return st;
   if (L > 0 && (!q || !k || !v || !o)) return DN_ERR_NULL_ARG;
   if (any_misaligned({q, k, v, log_decay, S0, o, S_final, workspace})) return DN_ERR_MISALIGNED;
-  const size_t need = dn::linear_workspace_bytes(B, H, L, d_k, d_v);
+  const size_t need = dn::linear_workspace_bytes(B, H, L, d_k, d_v, in_dtype);
   const Span ws{workspace, workspace ? need : 0};
   const Span in[] = {{q, s.qk}, {k, s.qk}, {v, s.v}, {log_decay, s.g}, {S_final == S0 ? nullptr : S0, s.state}};
   const Span out[] = {{o, s.o}, {S_final, s.state}};
@@ -733,7 +733,7 @@ size_t deltanet_linear_chunk_bwd_workspace_bytes(int B, int H, int H_qk, int L, 
                                                  dn_dtype in_dtype) {
   LinearSizes s;
   if (check_linear_shape(B, H, H_qk, L, d_k, d_v, in_dtype, DN_F32, &s) != DN_OK) return 0;
-  return dn::linear_bwd_workspace_bytes(B, H, H_qk, L, d_k, d_v);
+  return dn::linear_bwd_workspace_bytes(B, H, H_qk, L, d_k, d_v, in_dtype);
 }
 
 int deltanet_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -748,7 +748,7 @@ int deltanet_linear_chunk_bwd(const void* q, const void* k, const void* v, const
     return DN_ERR_NULL_ARG;
   if (any_misaligned({q, k, v, log_decay, S0, dO, dS_final, dq, dk, dv, dlog_decay, dS0, workspace}))
     return DN_ERR_MISALIGNED;
-  const size_t need = dn::linear_bwd_workspace_bytes(B, H, H_qk, L, d_k, d_v);
+  const size_t need = dn::linear_bwd_workspace_bytes(B, H, H_qk, L, d_k, d_v, in_dtype);
   const Span in[] = {{q, s.qk}, {k, s.qk}, {v, s.v}, {log_decay, s.g}, {S0, s.state}, {dO, s.v}, {dS_final, s.state}};
   const Span out[] = {{dq, s.qk}, {dk, s.qk}, {dv, s.v}, {dlog_decay, s.g}, {dS0, s.state}};
   if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;

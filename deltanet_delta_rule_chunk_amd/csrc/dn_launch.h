@@ -139,7 +139,7 @@ struct LinearArgs {
   void* workspace;         // at least linear_workspace_bytes(...) bytes
   hipStream_t stream;
 };
-size_t linear_workspace_bytes(int B, int H, int L, int d_k, int d_v);
+size_t linear_workspace_bytes(int B, int H, int L, int d_k, int d_v, int in_dtype);
 hipError_t launch_linear_fwd(const LinearArgs& a);
 
 struct LinearBwdArgs {
@@ -155,7 +155,7 @@ struct LinearBwdArgs {
   void* workspace;         // at least linear_bwd_workspace_bytes(...) bytes
   hipStream_t stream;
 };
-size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v);
+size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v, int in_dtype);
 hipError_t launch_linear_bwd(const LinearBwdArgs& a);
 
 struct LinearDecodeArgs {

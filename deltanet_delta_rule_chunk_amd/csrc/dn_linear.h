@@ -429,23 +429,45 @@ struct Split {
   int nc, cps, nseg;
 };
 
-// Enough segments for two workgroups on each of the 256 CUs (32 heads of 128 x 128
-// at L = 65536: 711 us of kernels; with 1024 workgroups 798, 384 798, 256 818),
-// none of them shorter than kMinChunks chunks (a segment costs a state's
-// write and two reads, 4 d_k d_v bytes each, against the rows it spares a walk;
-// 24 heads of 64 x 128 at L = 1501, forward and backward: 98 us, with 2 chunks 112,
-// with 3 95, but 2 fp32 heads of 4 chunks 90 with 3, against 69 in one segment).
+// How many segments.  More of them fill the 256 CUs and shorten the walks; each
+// costs a state's write and two reads and a step of the combination, and more
+// than one costs two launches.  An estimate in us decides, from times measured at
+// few rows: a walk's start, its chunks (the segment sums' take about half),
+// two bf16 workgroups on a CU taking up to 1.6 times as long as one (fp32: one per
+// CU).  Against segments of 4 chunks at the least and 512 workgroups for every
+// call, forward + backward: 4 bf16 heads of 128 x 128, L = 2000 100 -> 80 us of
+// kernels, 32 heads, L = 600 105 -> 91; 4 fp32 heads of 64 x 64, L = 1000 108 -> 64;
+// forward of 16 fp32 heads of 128 x 128, L = 2000 95 -> 69.  Long sequences of few
+// heads come out at 512 workgroups (32 heads of 128 x 128, L = 65536: 711 us of
+// kernels; with 1024 798, 384 798, 256 818).
 // None is longer than kMaxChunks, which bounds how far the decay's gradient is
 // carried from an exact value.
-constexpr int kWorkgroups = 512, kMinChunks = 4, kMaxChunks = 256;
-inline Split split_of(int BH, int L) {
-  Split s;
-  s.nc = cdiv(L, C);
-  s.cps = cdiv(s.nc, cdiv(kWorkgroups, BH));
-  if (s.cps < kMinChunks) s.cps = kMinChunks;
-  if (s.cps > kMaxChunks) s.cps = kMaxChunks;
-  s.nseg = cdiv(s.nc, s.cps);
-  return s;
+constexpr int kMaxChunks = 256;
+struct WalkTime {
+  double pair, slots;  // of two workgroups on a CU against one; workgroups the card takes
+  // n workgroups of cps chunks each: full rounds of the card, and a last one.
+  double us(double n, int cps, double per_chunk) const {
+    const double full = (double)(long long)(n / slots), rest = n - full * slots;
+    return (2.5 + cps * per_chunk) * (full * pair + (rest > 256 ? pair : rest > 0 ? 1.0 : 0.0));
+  }
+};
+inline Split split_of(int BH, int L, int d_k, int d_v, bool f32, bool bwd) {
+  Split best{cdiv(L, C), 0, 0};
+  const int nc = best.nc, d = d_k + d_v, fill = cdiv(512, BH);
+  const double chunk = f32 ? d / 20.0 : 0.7 + d / 64.0;
+  const WalkTime t{f32 ? 1.0 : 1.0 + 0.6 * d / 256, f32 ? 256.0 : 512.0};
+  double least = 0.0;
+  for (const int k : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64, fill}) {
+    Split s{nc, cdiv(nc, k), 0};
+    if (s.cps > kMaxChunks) s.cps = kMaxChunks;
+    s.nseg = cdiv(nc, s.cps);
+    const double n = (double)BH * s.nseg;
+    double us = bwd ? t.us(3 * n, s.cps, 1.3 * chunk) : t.us(n, s.cps, chunk);
+    if (s.nseg > 1)
+      us += bwd ? t.us(2 * n, s.cps, 0.45 * chunk) + 9 + 0.5 * s.nseg : t.us(n, s.cps, 0.45 * chunk) + 6 + 0.45 * s.nseg;
+    if (best.nseg == 0 || us < least) best = s, least = us;
+  }
+  return best;
 }
 
 // Work items (unit, member): the `grp` heads that share q and k rows run on

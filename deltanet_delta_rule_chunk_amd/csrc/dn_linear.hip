@@ -20,7 +20,7 @@ hipError_t launch_copy_state(float* dst, const float* src, size_t n, hipStream_t
 template <typename IT, typename OT, int DK, int DV>
 static hipError_t forward(const LinearArgs& a) {
   const int BH = a.B * a.H, grp = a.H / a.H_qk;
-  const Split s = split_of(BH, a.L);
+  const Split s = split_of(BH, a.L, DK, DV, sizeof(IT) == 4, false);
   const size_t N = (size_t)DK * DV;
   float* states = static_cast<float*>(a.workspace);
   hipError_t e;
@@ -53,10 +53,10 @@ static hipError_t forward_d(const LinearArgs& a) {
 
 }  // namespace lin
 
-size_t linear_workspace_bytes(int B, int H, int L, int d_k, int d_v) {
+size_t linear_workspace_bytes(int B, int H, int L, int d_k, int d_v, int in_dtype) {
   if (L == 0) return 0;
   const size_t BH = (size_t)B * H;
-  const lin::Split s = lin::split_of((int)BH, L);
+  const lin::Split s = lin::split_of((int)BH, L, d_k, d_v, in_dtype == 0, false);
   return s.nseg > 1 ? BH * s.nseg * ((size_t)d_k * d_v * 4 + 8) : 0;
 }
 

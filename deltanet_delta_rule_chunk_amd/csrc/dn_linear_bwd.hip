@@ -222,9 +222,9 @@ __global__ __launch_bounds__(kGradThreads) void finish_kernel(DecayGradArgs g, i
 struct BwdWs {
   size_t S, X, dS, dX, border, x, y, m, dq, dk, total;  // byte offsets
 };
-static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v) {
+static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v, bool f32) {
   const size_t BH = (size_t)B * H, N = (size_t)d_k * d_v * 4;
-  const Split s = split_of((int)BH, L);
+  const Split s = split_of((int)BH, L, d_k, d_v, f32, true);
   const size_t rows = BH * s.nc * C * 4, vec = H == H_qk ? 0 : BH * L * d_k * 4;
   BwdWs w{};
   size_t at = 0;
@@ -250,8 +250,8 @@ static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v) {
 template <typename IT, typename OT, int DK, int DV>
 static hipError_t backward(const LinearBwdArgs& a) {
   const int BH = a.B * a.H, grp = a.H / a.H_qk;
-  const Split s = split_of(BH, a.L);
-  const BwdWs o = bwd_ws(a.B, a.H, a.H_qk, a.L, DK, DV);
+  const Split s = split_of(BH, a.L, DK, DV, sizeof(IT) == 4, true);
+  const BwdWs o = bwd_ws(a.B, a.H, a.H_qk, a.L, DK, DV, sizeof(IT) == 4);
   const int N = DK * DV;
   char* const base = static_cast<char*>(a.workspace);
   auto f = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
@@ -308,8 +308,8 @@ static hipError_t backward_d(const LinearBwdArgs& a) {
 
 }  // namespace lin
 
-size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v) {
-  return L == 0 ? 0 : lin::bwd_ws(B, H, H_qk, L, d_k, d_v).total;
+size_t linear_bwd_workspace_bytes(int B, int H, int H_qk, int L, int d_k, int d_v, int in_dtype) {
+  return L == 0 ? 0 : lin::bwd_ws(B, H, H_qk, L, d_k, d_v, in_dtype == 0).total;
 }
 
 hipError_t launch_linear_bwd(const LinearBwdArgs& a) {

@@ -85,14 +85,16 @@ CASES = [
     (1, 2, 1, 64, 128, 128, "bf16", True, "none"),
     (1, 2, 1, 65, 64, 64, "f32", True, "wiping"),
     (1, 1, 3, 130, 64, 128, "bf16", False, "strong"),
-    (1, 3, 1, 256, 128, 128, "bf16", True, "wiping"),   # one segment
-    (1, 2, 1, 257, 128, 64, "bf16", True, "usual"),     # two, the second of one row
+    (1, 3, 1, 256, 128, 128, "bf16", True, "wiping"),
+    (1, 2, 1, 257, 128, 64, "bf16", True, "usual"),     # a last chunk of one row
     (1, 1, 2, 257, 64, 128, "f32", False, "keep"),
     (2, 1, 3, 700, 64, 64, "bf16", True, "wiping"),
     (1, 1, 1, 1025, 128, 128, "bf16", True, "slow"),
     (1, 1, 2, 1090, 128, 128, "f32", True, "wiping"),
     (3, 2, 4, 333, 128, 64, "bf16", False, "none"),
     (1, 9, 1, 400, 64, 64, "bf16", True, "usual"),      # heads in no multiple of the XCDs
+    (2, 101, 1, 300, 64, 64, "bf16", True, "wiping"),   # heads enough for one segment of several chunks
+    (1, 60, 4, 193, 64, 64, "f32", True, "usual"),
 ]
 IDS = ["-".join(map(str, c)) for c in CASES]
 
