@@ -22,7 +22,7 @@
 // the row sums that the decay's gradient needs line up between the passes.
 //
 // Parallelism over the sequence.  B H heads alone do not fill 256 CUs, so a
-// head's chunks are cut into segments.  A state kernel sums each segment from
+// head's chunks are cut into segments (split_of()).  A state kernel sums each segment from
 // a zero state (it reads k and v only), a combine kernel turns the sums into
 // the state entering every segment, and the output kernel walks each segment
 // from there.  With one segment the output kernel runs alone.
