@@ -812,20 +812,21 @@ struct OutLds {
   static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums<waves(DV)>) : 0);
 };
 
-// Four adjacent elements of a row of w straight from HBM (rows past the end
-// read as zeros).
+// Four adjacent elements of a row of w straight from HBM.  Rows past the end read
+// as zeros: the whole offset goes through the vector operand, which the
+// descriptor's range check sees (a scalar offset on top of it need not be seen).
 template <typename IT>
 struct Four;
 template <>
 struct Four<float> {
   f32x4 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t at, uint32_t more) { x = __builtin_bit_cast(f32x4, bload16(r, at, more)); }
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = __builtin_bit_cast(f32x4, bload16(r, at, 0)); }
   __device__ __forceinline__ f32x4 get() const { return x; }
 };
 template <>
 struct Four<bf16> {
   uint2 x;
-  __device__ __forceinline__ void load(rsrc_t r, uint32_t at, uint32_t more) { x = bload8(r, at, more); }
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at) { x = bload8(r, at, 0); }
   __device__ __forceinline__ f32x4 get() const {
     return f32x4{__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
                  __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u)};
@@ -838,8 +839,8 @@ __device__ __forceinline__ typename Tile<IT, D>::Frag row_frag(rsrc_t r, int row
     return as_bf16x8(bload16(r, at, 0));
   } else {
     Four<float> a, b;
-    a.load(r, at, 0);
-    b.load(r, at + 16, 0);
+    a.load(r, at);
+    b.load(r, at + 16);
     return F32x8{{a.x[0], a.x[1], a.x[2], a.x[3], b.x[0], b.x[1], b.x[2], b.x[3]}};
   }
 }
@@ -927,8 +928,7 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
       wr = make_rsrc(wp + (size_t)c * C * DV, (uint32_t)(min(C, L - c * C) * DV * (int)sizeof(IT)));
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
-        wd[rt].load(wr, (uint32_t)((REV ? 15 - li : li) * DV + w * 16 + 4 * lg) * sizeof(IT),
-                    16 * (REV ? NRT - 1 - rt : rt) * DV * sizeof(IT));
+        wd[rt].load(wr, (uint32_t)(w_row(16 * rt + li) * DV + w * 16 + 4 * lg) * sizeof(IT));
     }
     sv.load(v, c, L, m.at + bv);
     float gn = 0.f;
