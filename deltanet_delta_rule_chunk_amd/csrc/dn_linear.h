@@ -297,8 +297,8 @@ __device__ __forceinline__ float load_decay(const float* g, int c, int L) {
   return g && t < L ? g[t] : 0.f;
 }
 
-// Lane moves within the vector ALUs (no LDS round trip).  CTRL: 0x110 + n
-// moves by n lanes up within each 16, 0x120 + n turns each 16 by n, 0x142 and
+// Lane moves within the vector ALUs (no LDS round trip).  CTRL: 0x100 + n moves
+// by n lanes down and 0x110 + n up within each 16, 0x120 + n turns each 16 by n, 0x142 and
 // 0x143 hand lane 15 of a 16 to the next and lane 31 to the upper 32.  Lanes
 // that receive nothing get 0.
 template <int CTRL, int ROWS = 0xf>
@@ -692,7 +692,7 @@ static __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) { co
 enum Extra {
   kNone = 0,
   kDots = 1,   // per row: (row of w) . (the part of the output that comes from the entering state)
-  kPairs = 2   // kDots, and per row the sums of the chunk's pair terms (below)
+  kPairs = 2   // kDots, and per row t the sum of the chunk's pair terms that cross t (below)
 };
 
 struct OutArgs {
@@ -771,8 +771,8 @@ struct PBuf<float, NS> {
 template <int NW>
 struct Sums {
   float dots[NW][C];  // by wave
-  float out[10][16];  // pair terms of an output tile's rows, by tile of P
-  float key[10][16];  // ... of a key tile's rows
+  float out[10][16];  // pair terms of an output tile's rows, by tile of P (none on the diagonal)
+  float key[10][16];  // ... of a key tile's rows; on the diagonal the tile's terms that cross each row
 };
 __device__ __forceinline__ int tri(int rt, int it) { return rt * (rt + 1) / 2 + it; }
 
@@ -898,15 +898,30 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   wait_loads();
   __syncthreads();
 
-  // A chunk's pair sums, once every wave has left its own.
+  // A chunk's pair sums, once every wave has left its own: for row t the terms of
+  // pairs (i, r), i < t <= r, and of no other.  By tiles, t in tile lg: both of
+  // the pair in it; r in it and i before; i in it and r behind; the two of them
+  // around it.
   auto store_pairs = [&](int c) {
     const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
-    float y = 0.f;
+    float before = 0.f, behind = 0.f, around = 0.f;
     for (int x = 0; x < NRT; ++x) {
-      if (x <= lg) y += sums->out[tri(lg, x)][li];
-      if (x >= lg) y -= sums->key[tri(x, lg)][li];
+      if (x < lg) before += sums->out[tri(lg, x)][li];
+      if (x > lg) behind += sums->key[tri(x, lg)][li];
     }
-    a.pairs[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] = y;
+    if (lg == 1 || lg == 2) around = sums->out[tri(3, 0)][li] + sums->out[lg == 1 ? tri(2, 0) : tri(3, 1)][li];
+    // (Rows r from t on; rows i up to the one before t.)
+    before += dpp<0x101>(before);
+    before += dpp<0x102>(before);
+    before += dpp<0x104>(before);
+    before += dpp<0x108>(before);
+    behind = dpp<0x111>(behind);
+    behind += dpp<0x111>(behind);
+    behind += dpp<0x112>(behind);
+    behind += dpp<0x114>(behind);
+    behind += dpp<0x118>(behind);
+    a.pairs[(size_t)bh * a.s.nc * C + token_of<REV>(c, lane)] =
+        (sums->key[tri(lg, lg)][li] + before) + (behind + sum_lanes16(around));
   };
 
   for (int ci = 0; ci < n; ++ci) {
@@ -1033,35 +1048,42 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
       // Pair terms: P_ri (w_r . v_i), i < r.
       auto pair_sums = [&](const f32x4& x, const f32x4& y, int rt, int it) {
         const int i = li, g4 = 4 * lg, t = tri(rt, it);
-        float col = 0.f;
-        f32x4 row;
+        f32x4 m, row;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = it < rt || g4 + e < i ? x[e] * y[e] : 0.f;
-          col += m;
-          row[e] = sum_lanes16(m);
+        for (int e = 0; e < 4; ++e) m[e] = it < rt || g4 + e < i ? x[e] * y[e] : 0.f;
+        const float sum = (m[0] + m[1]) + (m[2] + m[3]);
+        if (it < rt) {
+          const float col = sum_groups(sum);
+          if (g4 == 0) sums->out[t][i] = col;
+        } else {
+          // Of output row i: the sum over the key rows in front of g4 + e.
+          const float up1 = __shfl_up(sum, 16, 64), u = g4 > 0 ? up1 : 0.f;
+          const float up2 = __shfl_up(u, 16, 64), up3 = __shfl_up(u, 32, 64);
+          float run = u + (g4 > 4 ? up2 : 0.f) + (g4 > 8 ? up3 : 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float next = run + m[e];
+            m[e] = i >= g4 + e ? run : 0.f;
+            run = next;
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row[e] = sum_lanes16(m[e]);
         if (i == 0) *reinterpret_cast<f32x4*>(&sums->key[t][g4]) = row;
-        col = sum_groups(col);
-        if (g4 == 0) sums->out[t][i] = col;
       };
-      f32x4 y[NA + 1];
 #pragma unroll
-      for (int x = 0; x <= NA; ++x) y[x] = zero4();
-#pragma unroll
-      for (int kb = 0; kb < DV / 32; ++kb)
-#pragma unroll
-        for (int x = 0; x < NA; ++x) y[x] = mma(V.row(16 * (pit + x), kb, lane), wf[kb], y[x]);
-      if (more_p) {
+      for (int x = 0; x <= NA; ++x) {
+        if (x == NA && !more_p) break;
+        const bool second = NW == 4 && x == NA;
+        const int rt = x < NA ? prt : prt2, it = x < NA ? pit + x : pit2;
+        f32x4 y = zero4();
 #pragma unroll
         for (int kb = 0; kb < DV / 32; ++kb) {
-          if constexpr (NW == 4) y[NA] = mma(V.row(16 * pit2, kb, lane), wf2[kb], y[NA]);
-          else y[NA] = mma(V.row(16 * pit2, kb, lane), wf[kb], y[NA]);
+          if constexpr (NW == 4) y = mma(V.row(16 * it, kb, lane), second ? wf2[kb] : wf[kb], y);
+          else y = mma(V.row(16 * it, kb, lane), wf[kb], y);
         }
-        pair_sums(p[NA], y[NA], prt2, pit2);
+        pair_sums(p[x], y, rt, it);
       }
-#pragma unroll
-      for (int x = 0; x < NA; ++x) pair_sums(p[x], y[x], prt, pit + x);
     }
     typename TV::Frag vf[C / 32];
     value_frags<IT, DV>(vf, V, w, lane);

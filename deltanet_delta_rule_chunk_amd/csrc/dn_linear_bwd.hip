@@ -9,12 +9,11 @@
 //     d g_t = sum over pairs (write i < t, read r >= t) of the pair's term
 //           + what reads r >= t take from before the pairs' reach
 //           + what the state that leaves keeps of it,
-// which splits by 64-row chunks with no difference of unlike sizes in it:
-//     d g_t =  sum_{r >= t} (x_r + m_r)  +  sum_{i < t} y_i  +  D_c
+// which splits by 64-row chunks into sums over pairs that cross t alone:
+//     d g_t =  sum_{r >= t} x_r  +  sum_{i < t} y_i  +  m_t  +  D_c
 //   x_r = q_r . (dq_r's part from the entering state)        (walk of dq)
 //   y_i = k_i . (dk_i's part from the exit gradient)         (walk of dk)
-//   m_r = sum_{i<r} P_ri (dO_r . v_i) - sum_{s>r} P_sr (dO_s . v_r)  (walk of dq:
-//         summed over r >= t, the pairs that cross t)
+//   m_t = sum_{i < t <= r} P_ri (dO_r . v_i), the chunk's own pairs (walk of dq)
 //   D_c = e^{G_C} <S_c, dS_c'>: entering state against exit gradient.
 // D follows from chunk to chunk: <S_{c+1}, dS_c'> = D_{c+1} + sum x (chunk
 // c+1) = D_c + sum y (chunk c), anchored at both ends of each segment, where
@@ -22,9 +21,9 @@
 // reach the other as an offset; the difference found there is handed back to
 // the chunks in proportion to the squares of the sums passed on the way, which
 // is the best estimate if those are what the roundings go by.  A token's own
-// pair (r = i) never enters, so a strong decay, whose gradient is small beside
-// q . dq, keeps its accuracy.  The sums over rows and chunks are taken in fp64;
-// they are a few bytes per token.
+// pair (r = i) and the pairs on one side of t never enter x, y and m, so a strong
+// decay, whose gradient is small beside q . dq, keeps its accuracy.  The sums
+// over rows and chunks are taken in fp64; they are a few bytes per token.
 //
 // 32 heads of 128 x 128, bf16, L = 65536: sums of both directions 455 us, walks 1.79
 // ms (7.7 GB, 4.3 TB/s; matrix instructions busy for 42%, 757 TFLOP/s as
@@ -182,12 +181,14 @@ __device__ __forceinline__ void decay_grad(const DecayGradArgs& a, int block) {
   }
   __syncthreads();
   for (int i = w; i < n; i += kGradThreads / 64) {
-    const size_t at = row0 + (size_t)i * C + l;
+    const size_t at = row0 + (size_t)i * C;
     const int t = (c0 + i) * C + l;
-    const double x = (double)a.x[at] + (double)a.m[at], y = a.y[at];
-    const double sx = wave_scan(x), sy = wave_scan(y);
-    // sum_{r >= t} (x_r + m_r) - sum_{i >= t} y_i + <the state that leaves>
-    const double v = (lane_value(sx, 63) - sx + x) - (lane_value(sy, 63) - sy + y) + carry[i];
+    // Sums over the rows from t on (lane l: from row 63 - l on, then handed to
+    // its lane) and over those in front of t.
+    const double from = __shfl(wave_scan(a.x[at + C - 1 - l]), C - 1 - l, 64);
+    const double before = wave_scan(l > 0 ? a.y[at + l - 1] : 0.f);
+    // (carry - ty: what the state that leaves holds of the one that entered.)
+    const double v = from + before + (double)a.m[at + l] + (carry[i] - ty[i]);
     if (t < a.L) a.dg[tok0 + t] = log2_decay(a.g[tok0 + t]) <= kWipe2 ? 0.f : (float)v;
   }
 }
