@@ -17,10 +17,17 @@
 //   D_c = e^{G_C} <S_c, dS_c'>: entering state against exit gradient.
 // D follows from chunk to chunk: <S_{c+1}, dS_c'> = D_{c+1} + sum x (chunk
 // c+1) = D_c + sum y (chunk c), anchored at both ends of each segment, where
-// both states are at hand.  Walked from one end the roundings of the sums would
-// reach the other as an offset; the difference found there is handed back to
-// the chunks in proportion to the squares of the sums passed on the way, which
-// is the best estimate if those are what the roundings go by.  A token's own
+// both states are at hand, and at every chunk that leaves less than 2^-64 of what
+// enters it (a wipe in it, say): D is 0 there, which gives both its neighbours.
+// Nothing is carried past such a chunk, so documents in one row stay apart bit
+// for bit.  Walked from one anchor the roundings of the sums would reach the next
+// as an offset; D is taken from both, each weighted with the squares of the sums
+// passed on the way from the other, which is the best estimate if those are what
+// the roundings go by.  Between two anchors D is off by about 2^-24 of the largest
+// <state, gradient> there, and so is the gradient of each of the chunk's tokens:
+// far below its neighbours', but not small against a single token's whose decay
+// leaves less than that of the state.  (The state and its gradient at every chunk
+// would show more; they are 4 times a chunk's rows.)  A token's own
 // pair (r = i) and the pairs on one side of t never enter x, y and m, so a strong
 // decay, whose gradient is small beside q . dq, keeps its accuracy.  The sums
 // over rows and chunks are taken in fp64; they are a few bytes per token.
@@ -127,10 +134,52 @@ struct DecayGradArgs {
 };
 
 constexpr int kGradThreads = 1024;
+// log2 of what a chunk has to leave of its entering state for D to be more than
+// 0: 2^40 under the roundings of the sums that it would be a difference of.
+constexpr double kThrough2 = -64.0;
+
+// One step of a wave's inclusive sums that start anew behind every lane whose
+// `cut` is set (its own value is the first).
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ void cut_scan_step(double& v, double& q, int& cut) {
+  const double pv = dpp<CTRL, ROWS>(v), pq = dpp<CTRL, ROWS>(q);
+  const int pc = dpp<CTRL, ROWS>(cut);
+  if (!cut) v += pv, q += pq;
+  cut |= pc;
+}
+
+// <state, gradient> in front of each of n chunks in the walk's order, from `first`
+// in front of them all on: behind a chunk it is in[i] where the chunk lets nothing
+// through, else in[i] - out[i] more than in front.  v[i] receives it and q[i] the
+// squares of the sums that it is made of, of which `first` has q0.  One wave.
+__device__ __forceinline__ void carry_walk(const double* in, const double* out, const unsigned char* shut, int n,
+                                           bool reversed, double first, double q0, double* v, double* q) {
+  const int l = threadIdx.x & 63;
+  for (int base = 0; base < n; base += 64) {
+    const int j = base + l, i = reversed ? n - 1 - j : j;
+    const bool on = j < n;
+    int cut = on && shut[i];
+    const double a = on ? in[i] : 0.0, b = on && !cut ? out[i] : 0.0;
+    double x = a - b, y = a * a + b * b;
+    cut_scan_step<0x111>(x, y, cut);
+    cut_scan_step<0x112>(x, y, cut);
+    cut_scan_step<0x114>(x, y, cut);
+    cut_scan_step<0x118>(x, y, cut);
+    cut_scan_step<0x142, 0xa>(x, y, cut);
+    cut_scan_step<0x143, 0xc>(x, y, cut);
+    if (!cut) x += first, y += q0;
+    const double px = __shfl_up(x, 1, 64), py = __shfl_up(y, 1, 64);
+    if (on) v[i] = l == 0 ? first : px, q[i] = l == 0 ? q0 : py;
+    first = lane_value(x, 63);
+    q0 = lane_value(y, 63);
+  }
+}
 
 // One workgroup per (head, segment).
 __device__ __forceinline__ void decay_grad(const DecayGradArgs& a, int block) {
-  __shared__ double part[kGradThreads / 64], tx[kMaxChunks], ty[kMaxChunks], carry[kMaxChunks];
+  __shared__ double part[kGradThreads / 64], tx[kMaxChunks], ty[kMaxChunks];
+  __shared__ double left[kMaxChunks], left_q[kMaxChunks], right[kMaxChunks], right_q[kMaxChunks];
+  __shared__ unsigned char shut[kMaxChunks];
   const int bh = block / a.s.nseg, seg = block % a.s.nseg;
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
@@ -154,41 +203,33 @@ __device__ __forceinline__ void decay_grad(const DecayGradArgs& a, int block) {
 
   for (int i = w; i < n; i += kGradThreads / 64) {
     const size_t at = row0 + (size_t)i * C + l;
-    const double x = wave_scan(a.x[at]), y = wave_scan(a.y[at]);
-    if (l == 63) tx[i] = x, ty[i] = y;
+    const int t = (c0 + i) * C + l;
+    const double x = wave_scan(a.x[at]), y = wave_scan(a.y[at]), g = wave_scan(log2_decay(t < a.L ? a.g[tok0 + t] : 0.f));
+    // (Nothing enters a zero state's first chunk or leaves the last towards no gradient.)
+    if (l == 63) {
+      tx[i] = x, ty[i] = y;
+      shut[i] = g < kThrough2 || (seg == 0 && i == 0 && !a.S0) || (end && i == n - 1 && !a.dS);
+    }
   }
   __syncthreads();
-  // carry[i]: <state that leaves chunk i, its gradient>, from the segment's
-  // end: held + sum over later chunks of x - y; then the correction.
-  if (w == 0) {
-    double run = held, passed = 0.0;  // uniform over the wave
-    for (int hi = n; hi > 0; hi -= 64) {
-      const int i = hi - 1 - l;  // lane 0: the last chunk
-      const bool on = i >= 0;
-      const double x = on ? tx[i] : 0.0, y = on ? ty[i] : 0.0;
-      const double d = wave_scan(x - y), v = wave_scan(x * x + y * y);
-      if (on) {
-        carry[i] = run + d - (x - y);
-        tx[i] = passed + v - (x * x + y * y);  // squares passed from the end to here
-      }
-      run += lane_value(d, 63);
-      passed += lane_value(v, 63);
-    }
-    if (known && passed > 0.0) {
-      const double off = (enter - run) / passed;
-      for (int i = l; i < n; i += 64) carry[i] += off * tx[i];
-    }
-  }
+  // <state, its gradient> in front of each chunk from the left, behind it from the right.
+  if (w == 0) carry_walk(ty, tx, shut, n, false, enter, known ? 0.0 : HUGE_VAL, left, left_q);
+  else if (w == 1) carry_walk(tx, ty, shut, n, true, held, 0.0, right, right_q);
   __syncthreads();
   for (int i = w; i < n; i += kGradThreads / 64) {
+    // What the chunk lets through: from the left, from the right, both.
+    const double lo = left[i] - tx[i], hi = right[i] - ty[i];
+    const double lq = left_q[i] + tx[i] * tx[i], hq = right_q[i] + ty[i] * ty[i];
+    double through = hi;
+    if (lq < HUGE_VAL && lq + hq > 0.0) through += (lo - hi) * (hq / (lq + hq));
+    if (shut[i]) through = 0.0;
     const size_t at = row0 + (size_t)i * C;
     const int t = (c0 + i) * C + l;
     // Sums over the rows from t on (lane l: from row 63 - l on, then handed to
     // its lane) and over those in front of t.
     const double from = __shfl(wave_scan(a.x[at + C - 1 - l]), C - 1 - l, 64);
     const double before = wave_scan(l > 0 ? a.y[at + l - 1] : 0.f);
-    // (carry - ty: what the state that leaves holds of the one that entered.)
-    const double v = from + before + (double)a.m[at + l] + (carry[i] - ty[i]);
+    const double v = from + before + (double)a.m[at + l] + through;
     if (t < a.L) a.dg[tok0 + t] = log2_decay(a.g[tok0 + t]) <= kWipe2 ? 0.f : (float)v;
   }
 }

@@ -353,7 +353,13 @@ size_t deltanet_linear_chunk_fwd_workspace_bytes(int B, int H, int H_qk, int L, 
  *   dv        : [B, H, L, d_v] in_dtype
  *   dlog_decay: [B, H, L] fp32, the gradient of log_decay (exactly 0 where
  *               log_decay is -inf), or NULL (not written; required to be NULL
- *               when log_decay is)
+ *               when log_decay is).  Summed over the pairs (write before t, read
+ *               at t or after) alone, so documents that a wipe separates do not
+ *               reach each other's.  What a 64-token chunk passes through is a
+ *               difference of sums, off by about 2^-24 of the largest
+ *               <state, its gradient> of the document: not small against a single
+ *               token's gradient whose decay leaves less than that of the state
+ *               (where a chunk leaves below 2^-64 there is no such term).
  *   dS0       : [B, H, d_k, d_v] fp32 or NULL (not written)
  * Nothing from a forward call is needed.  Outputs may not overlap inputs or
  * one another.
