@@ -37,13 +37,16 @@
 // through LDS as operand fragments.
 //
 // Precision.  bf16 q, k, v (and dO) enter products as they are.  An fp32
-// operand enters as a sum of bf16 pieces: 3 pieces (24 bits, all of fp32) where
-// it reaches an fp32 result through long sums: the rows added to a state that is
-// a result or enters a segment, the state read for an fp32 output or for what
-// the decay's gradient is summed from; 2 pieces (16 bits) for rows and state
-// that only reach bf16 outputs, whose own rounding is 256 times coarser, and for
-// P, whose sums span one chunk (a third piece of P would cost the second
-// workgroup of each CU its LDS; it leaves 2^-17 of a term).  fp32 inputs run the
+// operand enters as a sum of bf16 pieces: 3 pieces (24 bits, all of fp32) wherever
+// it reaches an fp32 result: the rows added to a state that is a result or enters
+// a segment, the state and P read for an fp32 output, the state read for what
+// the decay's gradient is summed from.  2 pieces (they leave 2^-17 of a term) only
+// on the way to bf16 outputs, whose own rounding is 2^-8: the state that a walk
+// reads and what it adds to it (with 3 pieces there the long forward's outputs
+// take 553 us for 482), and P in the walks of dq and dk beyond 64 x 64, whose sums
+// leave no LDS for a third piece beside a second workgroup.  P's third piece
+// elsewhere costs 3% of the outputs' time (486 -> 501 us); without it an fp32 o is
+// off by 2.3e-6 of its norm, with it by 0.8e-7.  fp32 inputs run the
 // same kernels on the fp32 matrix instruction, with nothing split.  Log decays
 // are summed in fp64: a difference of two sums keeps the accuracy of the short
 // sum between them however long the chunk's own is.
@@ -281,10 +284,12 @@ __device__ __forceinline__ void to_floats(const F32x8& f, float (&x)[8]) {
 
 // ---- what a chunk's rows are multiplied by ---------------------------------------
 
+// The tables of a chunk and the next: `up` is read until the state's update, while
+// the next chunk's is filled; G is not read as late as that.  A row's factor to
+// the chunk's end is 1 for the last row, whose place holds the whole chunk's.
 struct alignas(16) Decays {
-  double G[C];    // log2 decay from the chunk's start through a row
-  float up[C];    // 2^(G_last - G): from a row to the chunk's end
-  float total;    // 2^G_last
+  double G[C];      // log2 decay from the chunk's start through a row
+  float up[2][C];   // by chunk's parity: 2^(G_last - G); [C - 1]: 2^G_last
 };
 
 // Row u of chunk c: token, and the log decay in front of it.
@@ -330,12 +335,11 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
 }
 
 // One wave fills a chunk's table from its rows' log decays; returns the sum.
-__device__ __forceinline__ double fill_decays(Decays* d, float g) {
+__device__ __forceinline__ double fill_decays(Decays* d, int chunk, float g) {
   const int l = threadIdx.x & 63;
   const double G = wave_scan(log2_decay(g)), last = lane_value(G, 63);
   d->G[l] = G;
-  d->up[l] = exp2_hw((float)(last - G));
-  if (l == 63) d->total = exp2_hw((float)G);
+  d->up[chunk & 1][l] = exp2_hw((float)(l == 63 ? G : last - G));
   return last;
 }
 
@@ -500,7 +504,7 @@ struct StateArgs {
 // S = total S + K^T diag(up) V on this wave's columns, diag(up) V in NU pieces.
 template <int NU, typename IT, int DK>
 __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> K,
-                                             const typename Tile<IT, 64>::Frag (&vf)[C / 32], const Decays* d, int l) {
+                                             const typename Tile<IT, 64>::Frag (&vf)[C / 32], const float* up, int l) {
   // Column fragments are read AHEAD tiles before their products, so that LDS
   // answers meanwhile.
   // The waves that are here go first: theirs are the long runs of matrix
@@ -511,11 +515,12 @@ __device__ __forceinline__ void update_state(f32x4 (&st)[DK / 16], Tile<IT, DK> 
   typename Tile<IT, DK>::Frag a[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) a[i] = K.state_col(i % KT, i / KT, l);
-  const float total = d->total;
+  const float total = up[C - 1];
 #pragma unroll
   for (int tb = 0; tb < C / 32; ++tb) {
-    const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d->up[32 * tb + 4 * g]);
-    const f32x4 u1 = *reinterpret_cast<const f32x4*>(&d->up[32 * tb + 16 + 4 * g]);
+    const f32x4 u0 = *reinterpret_cast<const f32x4*>(&up[32 * tb + 4 * g]);
+    f32x4 u1 = *reinterpret_cast<const f32x4*>(&up[32 * tb + 16 + 4 * g]);
+    if (tb == C / 32 - 1 && g == 3) u1[3] = 1.f;  // (row C - 1: see Decays)
     float x[8];
     to_floats(vf[tb], x);
 #pragma unroll
@@ -580,14 +585,14 @@ __host__ __device__ constexpr int simd_waves(int DV) { return waves(DV) / 4 * (s
 
 // Two sets of tiles: a chunk's rows arrive while the one before is used.
 template <typename IT, int DK, int DV>
-constexpr int state_lds() { return 2 * (Tile<IT, DK>::bytes + Tile<IT, DV>::bytes + (int)sizeof(Decays)); }
+constexpr int state_lds() { return 2 * (Tile<IT, DK>::bytes + Tile<IT, DV>::bytes) + (int)sizeof(Decays); }
 
 template <typename IT, int DK, int DV, bool REV>
 __device__ __forceinline__ void state_walk(const StateArgs& a, int flat, Lds m) {
   unsigned char* const smem = m.p;
   constexpr int NW = waves(DV);
   constexpr int TB = Tile<IT, DK>::bytes + Tile<IT, DV>::bytes;
-  Decays* const tables = reinterpret_cast<Decays*>(smem + 2 * TB);
+  Decays* const table = reinterpret_cast<Decays*>(smem + 2 * TB);
 
   int bh, seg;
   if (!item_of(flat, a.BH, a.grp, a.count, bh, seg)) return;
@@ -612,7 +617,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& a, int flat, Lds m) 
   };
   double sum = 0.0;
   load(0);
-  if (tables_wave) sum += fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
+  if (tables_wave) sum += fill_decays(table, 0, load_decay<REV>(g, chunk(0), L));
   wait_loads();
   __syncthreads();
   for (int i = 0; i < n; ++i) {
@@ -628,8 +633,8 @@ __device__ __forceinline__ void state_walk(const StateArgs& a, int flat, Lds m) 
     unsigned char* const at = smem + (i & 1) * TB;
     typename Tile<IT, DV>::Frag vf[C / 32];
     value_frags<IT, DV>(vf, Tile<IT, DV>{at + Tile<IT, DK>::bytes}, w, lane);
-    update_state<3, IT, DK>(st, Tile<IT, DK>{at}, vf, &tables[i & 1], lane);
-    if (more && tables_wave) sum += fill_decays(&tables[(i + 1) & 1], gn);
+    update_state<3, IT, DK>(st, Tile<IT, DK>{at}, vf, table->up[i & 1], lane);
+    if (more && tables_wave) sum += fill_decays(table, i + 1, gn);
     wait_loads();
     __syncthreads();
   }
@@ -798,17 +803,16 @@ __device__ __forceinline__ void store4<bf16>(bf16* p, f32x4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-// Bytes of LDS: four tile buffers, P, the decay tables of this chunk and the
-// next, and the sums.
+// Bytes of LDS: four tile buffers, P, the decay tables, and the sums.
 template <typename IT, typename OT, int DK, int DV, int EXTRA>
 struct OutLds {
   // Pieces of an fp32 operand (see "Precision" above): of P, of the state.
-  static constexpr int NSP = 2;
+  static constexpr int NSP = EXTRA == kNone || (DK == 64 && DV == 64) ? 3 : 2;
   static constexpr int NSS = sizeof(OT) == 2 && EXTRA == kNone ? 2 : 3;
   static constexpr int tile = Tile<IT, (DK > DV ? DK : DV)>::bytes;
   static constexpr int P = 4 * tile;
   static constexpr int D = P + PBuf<IT, NSP>::bytes;
-  static constexpr int S = D + 2 * (int)sizeof(Decays);
+  static constexpr int S = D + (int)sizeof(Decays);
   static constexpr int bytes = S + (EXTRA != kNone ? (int)sizeof(Sums<waves(DV)>) : 0);
 };
 
@@ -859,7 +863,6 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   typedef Tile<IT, DK> TK;
   typedef Tile<IT, DV> TV;
   const PBuf<IT, NSP> P{smem + LD::P};
-  Decays* const tables = reinterpret_cast<Decays*>(smem + LD::D);
   Sums<NW>* const sums = reinterpret_cast<Sums<NW>*>(smem + LD::S);
 
   const int L = a.L, c0 = seg * a.s.cps, c1 = min(c0 + a.s.cps, a.s.nc), n = c1 - c0;
@@ -888,7 +891,7 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   int bq = 0, bk = LD::tile, bv = 2 * LD::tile, bf = 3 * LD::tile;
   sk.load(q, chunk(0), L, m.at + bq);
   sk.load(k, chunk(0), L, m.at + bk);
-  if (w == kTableWave) fill_decays(&tables[0], load_decay<REV>(g, chunk(0), L));
+  if (w == kTableWave) fill_decays(reinterpret_cast<Decays*>(smem + LD::D), 0, load_decay<REV>(g, chunk(0), L));
   f32x4 st[DK / 16];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
@@ -933,7 +936,11 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
     int lane = threadIdx.x & 63;
     if (EXTRA == kPairs) asm volatile("" : "+v"(lane));
     const int lg = lane >> 4, li = lane & 15;
-    const Decays* dec = &tables[ci & 1];
+    // (Where the table lies is formed anew in each chunk as well: known for the whole
+    // loop, every address into it would stay in a register.)
+    int table = LD::D;
+    asm volatile("" : "+s"(table));
+    Decays* const dec = reinterpret_cast<Decays*>(smem + table);
     const TK Q{smem + bq}, K{smem + bk};
     const TV V{smem + bv};
     rsrc_t wr;
@@ -1091,8 +1098,8 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
     for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
       for (int kb = 0; kb <= rt / 2; ++kb) acc[rt] = mma(vf[kb], P.get(rt, kb, lane), acc[rt]);
-    update_state<NU, IT, DK>(st, K, vf, dec, lane);
-    if (w == kTableWave && more) fill_decays(&tables[(ci + 1) & 1], gn);
+    update_state<NU, IT, DK>(st, K, vf, dec->up[ci & 1], lane);
+    if (w == kTableWave && more) fill_decays(dec, ci + 1, gn);
     wait_loads();
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {

@@ -327,7 +327,9 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
  *   L >= 0 (L = 0 copies S0, or zeros, to S_final).  d_k, d_v in {64, 128}.
  * The result does not depend on how the sequence is cut into chunks, so
  * there is no chunk argument.  bf16 inputs run on the bf16 matrix cores, every
- * fp32 operand as a sum of bf16 pieces; fp32 inputs on the fp32 ones.  A
+ * fp32 operand as a sum of bf16 pieces: three, which are all of its 24 bits, on
+ * the way to fp32 results (S_final always is one), two, which leave 2^-17 of a
+ * term, for what only reaches a bf16 o.  fp32 inputs run on the fp32 ones.  A
  * non-finite q, k or v row makes outputs of its 64-token chunk (tokens 64 n to
  * 64 n + 63, earlier ones too) and, from k or v, the states after it
  * non-finite: padding has to be finite.  workspace, workspace_bytes, stream,
