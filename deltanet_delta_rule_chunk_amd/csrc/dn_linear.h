@@ -88,9 +88,10 @@ __device__ __forceinline__ double log2_decay(float g) {
   return x < kWipe2 ? kWipe2 : x;
 }
 
-// x after a decay by f.  One by 0 (a wipe) drops x whatever it is: the state of a
-// call whose first token wipes it may be memory never written.
-__device__ __forceinline__ f32x4 decayed(f32x4 x, float f) { return f == 0.f ? zero4() : x * f; }
+// Whether a head's first token wipes the state it starts from, which may then be
+// memory never written and is not read.  (Only there: a wipe behind it multiplies
+// by 0, which leaves what is not finite so, however the sequence is cut.)
+__device__ __forceinline__ bool starts_with_wipe(const float* g) { return g && exp2_hw((float)log2_decay(g[0])) == 0.f; }
 
 // ---- operands ------------------------------------------------------------------
 //
@@ -658,7 +659,8 @@ struct CombineArgs {
   float* states;
   const double* decays;
   const float* S0;  // [BH][N] or null: the first state of the walk
-  int slots, nseg, N;
+  const float* g;   // [BH][L] or null: log decays (forward)
+  int slots, nseg, N, L;
 };
 
 template <bool REV>
@@ -667,7 +669,8 @@ __device__ __forceinline__ void combine(const CombineArgs& a) {
   if (e >= a.N) return;
   float* S = a.states + (size_t)bh * a.slots * a.N + e;
   const double* d = a.decays + (size_t)bh * a.nseg;
-  f32x4 run = a.S0 ? *reinterpret_cast<const f32x4*>(a.S0 + (size_t)bh * a.N + e) : zero4();
+  const bool none = !a.S0 || (!REV && starts_with_wipe(a.g ? a.g + (size_t)bh * a.L : nullptr));
+  f32x4 run = none ? zero4() : *reinterpret_cast<const f32x4*>(a.S0 + (size_t)bh * a.N + e);
   const int steps = a.nseg - 1;
   for (int i0 = 0; i0 < steps; i0 += 8) {
     f32x4 x[8];
@@ -681,7 +684,7 @@ __device__ __forceinline__ void combine(const CombineArgs& a) {
       if (i0 + j < steps) {
         const int s = REV ? a.nseg - 1 - (i0 + j) : i0 + j;
         *reinterpret_cast<f32x4*>(S + (size_t)s * a.N) = run;
-        run = decayed(run, exp2_hw((float)d[s])) + x[j];
+        run = run * exp2_hw((float)d[s]) + x[j];
       }
     }
   }
@@ -895,8 +898,7 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   f32x4 st[DK / 16];
   const float* S = a.s.nseg > 1 ? a.states + ((size_t)bh * a.slots + seg) * (DK * DV)
                                 : (a.S0 ? a.S0 + (size_t)bh * (DK * DV) : nullptr);
-  // (A wipe in front of the first row: see decayed().)
-  if (!REV && g && exp2_hw((float)log2_decay(g[c0 * C])) == 0.f) S = nullptr;
+  if (!REV && c0 == 0 && starts_with_wipe(g)) S = nullptr;
   load_state<DK, DV, TRANS>(st, S);
   wait_loads();
   __syncthreads();

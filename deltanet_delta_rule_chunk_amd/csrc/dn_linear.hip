@@ -30,7 +30,7 @@ static hipError_t forward(const LinearArgs& a) {
     e = launch(&state_kernel<IT, DK, DV>, kSlotLinearState, items(BH, grp, st.count), 64 * waves(DV),
                state_lds<IT, DK, DV>(), a.stream, st);
     if (e != hipSuccess) return e;
-    CombineArgs cb{states, decays, a.S0, s.nseg, s.nseg, (int)N};
+    CombineArgs cb{states, decays, a.S0, a.log_decay, s.nseg, s.nseg, (int)N, a.L};
     prof_mark(kSlotLinearState, false, a.stream);
     hipLaunchKernelGGL(combine_kernel, dim3(cdiv((int)N, 1024), (unsigned)BH), dim3(256), 0, a.stream, cb);
     e = hipGetLastError();

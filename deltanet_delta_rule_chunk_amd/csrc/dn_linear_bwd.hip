@@ -306,8 +306,8 @@ static hipError_t backward(const LinearBwdArgs& a) {
     e = launch(&bwd_state_kernel<IT, DK, DV>, kSlotLinearState, 2LL * ns, 64 * waves(DV), state_lds<IT, DK, DV>(),
                a.stream, st, sx, ns);
     if (e != hipSuccess) return e;
-    CombineArgs cs{f(o.S), d(o.dS), a.S0, s.nseg + 1, s.nseg, N};
-    CombineArgs cx{f(o.X), d(o.dX), a.dS_final, s.nseg, s.nseg, N};
+    CombineArgs cs{f(o.S), d(o.dS), a.S0, a.log_decay, s.nseg + 1, s.nseg, N, a.L};
+    CombineArgs cx{f(o.X), d(o.dX), a.dS_final, nullptr, s.nseg, s.nseg, N, a.L};
     prof_mark(kSlotLinearState, false, a.stream);
     hipLaunchKernelGGL(bwd_combine_kernel, dim3(cdiv(N, 1024), (unsigned)BH, 2), dim3(256), 0, a.stream, cs, cx);
     e = hipGetLastError();

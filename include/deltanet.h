@@ -332,7 +332,8 @@ int deltanet_decode_step_features(const void* q_raw, const void* k_raw, const vo
  * term, for what only reaches a bf16 o.  fp32 inputs run on the fp32 ones.  A
  * non-finite q, k or v row makes outputs of its 64-token chunk (tokens 64 n to
  * 64 n + 63, earlier ones too) and, from k or v, the states after it
- * non-finite: padding has to be finite.  workspace, workspace_bytes, stream,
+ * non-finite (a wipe behind it in the same call does not clear them): padding
+ * has to be finite.  workspace, workspace_bytes, stream,
  * status codes and every other rule: as for deltanet_chunk_fwd; the workspace
  * holds one fp32 state per segment that the sequence is cut into, and may be
  * 0 bytes.
