@@ -767,7 +767,7 @@ int deltanet_linear_decode_step(const void* q, const void* k, const void* v, con
   if (B < 1 || H < 1 || H_qk < 1 || d_k < 1 || d_v < 1 || H % H_qk) return DN_ERR_BAD_SHAPE;
   if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return DN_ERR_UNSUPPORTED;
   if (!dim_ok(d_k) || !dim_ok(d_v)) return DN_ERR_UNSUPPORTED;
-  if ((int64_t)B * H > 0x7fffffff / 8) return DN_ERR_UNSUPPORTED;
+  if ((int64_t)B * H > dn::linear_decode_max_heads()) return DN_ERR_UNSUPPORTED;
   if (!q || !k || !v || !S || !o) return DN_ERR_NULL_ARG;
   if (any_misaligned({q, k, v, log_decay, S, o})) return DN_ERR_MISALIGNED;
   const size_t bh = (size_t)B * H, qk = (size_t)B * H_qk * d_k * dtype_size(in_dtype);

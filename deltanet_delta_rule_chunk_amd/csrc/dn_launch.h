@@ -127,6 +127,10 @@ hipError_t launch_kda_chunk_fwd(const ChunkArgs& a);
 // the workspace, after the kernels' other scratch.
 size_t gated_log_decay_bytes(int B, int H, int L, int C);
 
+// Workgroups of `threads` that one launch takes: a dispatch counts its work-items
+// per dimension in 32 bits.
+constexpr long long max_blocks(int threads) { return 0xffffffffLL / threads; }
+
 // The gated linear recurrence (dn_linear.hip, dn_linear_bwd.hip,
 // dn_linear_decode.hip).  Head h reads q and k of head h / (H / H_qk).
 struct LinearArgs {
@@ -166,6 +170,7 @@ struct LinearDecodeArgs {
   int B, H, H_qk, d_k, d_v, in_dtype, out_dtype;
   hipStream_t stream;
 };
+long long linear_decode_max_heads();
 hipError_t launch_linear_decode(const LinearDecodeArgs& a);
 
 // Per-head norm of q and k and rotation by position (dn_qk_norm_rope.hip).

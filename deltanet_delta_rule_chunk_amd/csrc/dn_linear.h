@@ -1151,9 +1151,11 @@ hipError_t allow_lds(K* kernel, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// One launch of `kernel`, bracketed for the profiling hook.
+// One launch of `kernel`, bracketed for the profiling hook.  (The sizes that the
+// entry points accept stay below a launch's limit wherever their tensors fit the card.)
 template <typename K, typename... A>
 hipError_t launch(K* kernel, int slot, long long blocks, int threads, int lds, hipStream_t stream, const A&... args) {
+  if (blocks > max_blocks(threads)) return hipErrorInvalidConfiguration;
   hipError_t e = lds > 65536 ? allow_lds(kernel, lds) : hipSuccess;
   if (e != hipSuccess) return e;
   prof_mark(slot, false, stream);

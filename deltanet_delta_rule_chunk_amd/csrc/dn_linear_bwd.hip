@@ -243,9 +243,8 @@ struct GroupSumArgs {
 };
 template <typename OT>
 __device__ __forceinline__ void group_sum(const GroupSumArgs& a, size_t i4) {
-  const size_t i = i4 * 4 < a.n ? i4 * 4 : i4 * 4 - a.n;
-  if (i >= a.n) return;
   const bool first = i4 * 4 < a.n;
+  const size_t i = first ? i4 * 4 : i4 * 4 - a.n;
   const size_t u = i / a.per_head;
   const float* p = (first ? a.dq : a.dk) + u * a.grp * a.per_head + (i - u * a.per_head);
   f32x4 x = *reinterpret_cast<const f32x4*>(p);
@@ -258,7 +257,9 @@ __device__ __forceinline__ void group_sum(const GroupSumArgs& a, size_t i4) {
 template <typename OT>
 __global__ __launch_bounds__(kGradThreads) void finish_kernel(DecayGradArgs g, int ng, GroupSumArgs s) {
   if ((int)blockIdx.x < ng) decay_grad(g, blockIdx.x);
-  else group_sum<OT>(s, (size_t)(blockIdx.x - ng) * kGradThreads + threadIdx.x);
+  else
+    for (size_t i = (size_t)(blockIdx.x - ng) * kGradThreads + threadIdx.x; i < s.n / 2; i += (size_t)(gridDim.x - ng) * kGradThreads)
+      group_sum<OT>(s, i);
 }
 
 struct BwdWs {
@@ -288,6 +289,9 @@ static BwdWs bwd_ws(int B, int H, int H_qk, int L, int d_k, int d_v, bool f32) {
   w.total = at;
   return w;
 }
+
+// Workgroups of the sums over shared heads at most: 32 rounds of the card.
+constexpr size_t kSumBlocks = 16384;
 
 template <typename IT, typename OT, int DK, int DV>
 static hipError_t backward(const LinearBwdArgs& a) {
@@ -338,7 +342,8 @@ static hipError_t backward(const LinearBwdArgs& a) {
   const size_t per = (size_t)a.L * DK, total = shared ? (size_t)a.B * a.H_qk * per : 0;
   GroupSumArgs sum{f(o.dq), f(o.dk), a.dq, a.dk, per, total, grp};
   const int ng = a.dlog_decay ? BH * s.nseg : 0;
-  const long long blocks = ng + (long long)((2 * total / 4 + kGradThreads - 1) / kGradThreads);
+  const size_t sums = (2 * total / 4 + kGradThreads - 1) / kGradThreads;
+  const long long blocks = ng + (long long)(sums < kSumBlocks ? sums : kSumBlocks);
   return launch(&finish_kernel<IT>, kSlotLinearBwd, blocks, kGradThreads, 0, a.stream, g, ng, sum);
 }
 

@@ -19,13 +19,15 @@
 namespace dn {
 namespace lin {
 
+constexpr int kThreads = 256;
+
 typedef float vf4 __attribute__((ext_vector_type(4)));
 
 template <int DK, int DV, typename IT, typename OT>
-__global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, const IT* __restrict__ k,
+__global__ __launch_bounds__(kThreads) void decode_kernel(const IT* __restrict__ q, const IT* __restrict__ k,
                                                      const IT* __restrict__ v, const float* __restrict__ g,
                                                      float* __restrict__ S, OT* __restrict__ o, int grp) {
-  constexpr int COLG = DV / 4, ROWG = 256 / COLG, RPT = DK / ROWG;
+  constexpr int COLG = DV / 4, ROWG = kThreads / COLG, RPT = DK / ROWG;
   static_assert(COLG * 4 == DV && RPT * ROWG == DK, "tile shape");
   __shared__ float ks[DK], qs[DK];
   __shared__ vf4 red[ROWG][COLG];
@@ -36,7 +38,7 @@ __global__ __launch_bounds__(256) void decode_kernel(const IT* __restrict__ q, c
 #pragma unroll
   for (int i = 0; i < RPT; ++i) s[i] = *reinterpret_cast<const vf4*>(Sh + (size_t)(rg + i * ROWG) * DV);
   const size_t row = (size_t)(bh / grp) * DK;
-  for (int i = tid; i < DK; i += 256) {
+  for (int i = tid; i < DK; i += kThreads) {
     ks[i] = to_f32(k[row + i]);
     qs[i] = to_f32(q[row + i]);
   }
@@ -72,7 +74,7 @@ template <int DK, int DV, typename IT, typename OT>
 static hipError_t launch(const LinearDecodeArgs& a) {
   const int BH = a.B * a.H;
   prof_mark(kSlotLinearDecode, false, a.stream);
-  hipLaunchKernelGGL((decode_kernel<DK, DV, IT, OT>), dim3((unsigned)BH), dim3(256), 0, a.stream,
+  hipLaunchKernelGGL((decode_kernel<DK, DV, IT, OT>), dim3((unsigned)BH), dim3(kThreads), 0, a.stream,
                      static_cast<const IT*>(a.q), static_cast<const IT*>(a.k), static_cast<const IT*>(a.v),
                      a.log_decay, a.S, static_cast<OT*>(a.o), a.H / a.H_qk);
   hipError_t e = hipGetLastError();
@@ -88,6 +90,8 @@ static hipError_t launch_d(const LinearDecodeArgs& a) {
 }
 
 }  // namespace lin
+
+long long linear_decode_max_heads() { return max_blocks(lin::kThreads); }
 
 hipError_t launch_linear_decode(const LinearDecodeArgs& a) {
   if (a.d_k == 64 && a.d_v == 64) return lin::launch_d<64, 64>(a);

@@ -309,9 +309,10 @@ static hipError_t backward(const QkNormRopeArgs& a) {
 
 }  // namespace qkr
 
-// Most tokens one launch takes (the grid's x extent, a head per workgroup).
+// Most tokens one launch takes.  (Few tokens, over which more blocks of heads are
+// spread, stay far below the launch's limit.)
 long long qk_norm_rope_max_tokens(int heads, int d) {
-  return 0x7fffffffLL / heads * (qkr::NT / (d / 8));
+  return max_blocks(qkr::NT) / qkr::split_heads(heads, 1).blocks * (qkr::NT / (d / 8));
 }
 
 hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a) {

@@ -379,7 +379,8 @@ size_t deltanet_linear_chunk_bwd_workspace_bytes(int B, int H, int H_qk, int L, 
                                                  dn_dtype in_dtype);
 
 /* One token of the gated linear recurrence, S updated in place; o = q S_new.
- * q, k: [B, H_qk, d_k], v, o: [B, H, d_v], log_decay: [B, H] fp32 or NULL. */
+ * q, k: [B, H_qk, d_k], v, o: [B, H, d_v], log_decay: [B, H] fp32 or NULL;
+ * B H up to 2^24 - 1. */
 int deltanet_linear_decode_step(const void* q, const void* k, const void* v, const float* log_decay,
                                 float* S, void* o, int B, int H, int H_qk, int d_k, int d_v,
                                 dn_dtype in_dtype, dn_dtype out_dtype, hipStream_t stream);
@@ -407,7 +408,9 @@ int deltanet_linear_decode_step(const void* q, const void* k, const void* v, con
  *   q_hat, k_hat  : [B, H_q, L, d_k], [B, H_k, L, d_k] dtype, dense, written
  *   d_k in {64, 128}; d_rot a multiple of 8, 0 .. d_k; n_axes 1 .. 4; eps >= 0.
  * Evaluated in fp32, angles in fp64 (any int32 position).  Rows beyond ~1e19
- * overflow their fp32 sum of squares (the row then maps to zeros).
+ * overflow their fp32 sum of squares (the row then maps to zeros).  Sizes beyond
+ * one launch are DN_ERR_UNSUPPORTED: with H_q + H_k <= 4, 2^24 - 1 times 32 tokens
+ * of 64 elements or 16 of 128, with more heads that many fewer.
  */
 int deltanet_qk_norm_rope(const void* q_raw, const long long* q_strides,
                           const void* k_raw, const long long* k_strides,

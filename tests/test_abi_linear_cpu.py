@@ -199,3 +199,20 @@ def test_binding_refuses_wrong_tensors():
         binding.qk_norm_rope(x, x, None, None)
     with pytest.raises(ValueError, match=r"\[B, H, L, d\]"):
         binding.qk_norm_rope(x[0], x[0], None, None)
+
+
+def test_sizes_beyond_one_launch_are_refused(lib):
+    """A launch holds fewer than 2^32 work-items: sizes up to that pass the checks
+    of size (and are refused for the overlap here), the next one does not."""
+    most = 2 ** 24 - 1                             # workgroups of 256
+    assert _dec(lib, B=most, H=1, Hqk=1, S=AT(3)) == ALIAS
+    assert _dec(lib, B=most + 1, H=1, Hqk=1, S=AT(3)) == UNSUP
+    for call, same in ((_qk, dict(qh=AT(0))), (_qk_bwd, dict(dq=AT(0)))):
+        # 32 tokens of 64 elements per workgroup, 16 of 128; up to 4 heads
+        for d, rows in ((64, 32), (128, 16)):
+            one = dict(B=1, Hq=1, Hk=0, d=d, drot=d, **same)
+            assert call(lib, L=most * rows, **one) == ALIAS
+            assert call(lib, L=most * rows + 1, **one) == UNSUP
+            assert call(lib, L=most // 2 * rows, **dict(one, Hq=5)) == ALIAS
+            assert call(lib, L=most // 2 * rows + 1, **dict(one, Hq=5)) == UNSUP
+    assert lib.deltanet_last_hip_error() == 0

@@ -200,3 +200,19 @@ def test_repeated_rows_are_read_in_place(gpu_lib):
     want = N.qk_norm_rope_bwd(q.contiguous(), k.contiguous(), pos, inv, *want)
     for a, b in zip(got[:2], want[:2]):
         assert torch.equal(a, b)
+
+
+def test_sums_over_shared_heads_in_more_than_one_round(gpu_lib):
+    """More elements than the workgroups of the sums hold at once (fp32: what two
+    heads leave is added exactly)."""
+    L, d = 2 ** 18 + 70, 128
+    assert 2 * L * d // 4 > 16384 * 1024
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    r = lambda h, d=d: torch.randn((1, h, L, d), generator=gen, device=DEV)  # noqa: E731
+    q, k, v, dO = r(1), r(1).mul_(d ** -0.5), r(2, 64), r(2, 64)
+    g = torch.nn.functional.logsigmoid(torch.randn((1, 2, L), generator=gen, device=DEV) + 3)
+    got = N.linear_chunk_bwd(q, k, v, g, None, dO)
+    two = lambda t: t.expand(1, 2, L, d).contiguous()  # noqa: E731
+    want = N.linear_chunk_bwd(two(q), two(k), v, g, None, dO)
+    for a, b in zip(got[:2], want[:2]):
+        assert torch.equal(a[:, 0], b[:, 0] + b[:, 1])
