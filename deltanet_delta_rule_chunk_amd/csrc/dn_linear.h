@@ -352,10 +352,15 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // range check of the descriptor `r` makes rows past the end zeros.  Written in
 // assembly so that the compiler does not order LDS reads of other buffers
 // behind it: the caller waits with wait_loads() and a barrier before reading.
+// (m0 is named as changed, so that a value that the compiler keeps there is set
+// again; it warns that it will not be preserved, which is what is meant.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(r) : "memory");
+               :: "s"(lds), "v"(voff), "s"(r) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // Waits for all of this wave's vector memory operations.  (They end in order,
 // and the compiler does not count those issued above, so any wait of its own for
 // a load into registers waits for them too: such loads are made to arrive here,
