@@ -2,10 +2,10 @@
 
 Every step of the computation runs in the library's HIP kernels; this module
 checks tensors (device, dtype, contiguity, shape), allocates outputs and the
-workspace through PyTorch's caching allocator (recorded on the launch stream
-when that is not the current one), and passes raw device pointers and the HIP
-stream (the current one unless ``stream=`` names another) to the C ABI.  If
-the library is missing it raises: there is no fallback.
+workspace through PyTorch's caching allocator (on the launch stream, and
+recorded on the current one when that is another), and passes raw device
+pointers and the HIP stream (the current one unless ``stream=`` names another)
+to the C ABI.  If the library is missing it raises: there is no fallback.
 """
 
 from __future__ import annotations
@@ -186,13 +186,17 @@ def _stream(device: torch.device, stream) -> int:
 
 
 def _alloc(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
-    """A new tensor from PyTorch's caching allocator.  The allocator ties a
-    block to the stream current at allocation; when the kernels run on another
-    stream, the block is also recorded on that stream, so that it is not
-    handed out again while those kernels may still use it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        t.record_stream(stream)
+    """A new tensor from PyTorch's caching allocator, of the stream that the
+    kernels run on: a block of the current stream may still be in use there by
+    work that the other one does not wait for.  It is recorded on the current
+    stream as well, where the caller may read it last, so that it is not handed
+    out again before that."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
     return t
 
 
