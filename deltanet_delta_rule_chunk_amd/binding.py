@@ -874,6 +874,8 @@ def rotary_qk(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torc
               norm: bool = True, interleaved: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable ``qk_norm_rope`` for training, with gradients for q_raw,
     k_raw and the weights from ``deltanet_qk_norm_rope_bwd``."""
+    # (A copy: the backward uses the sections of this call whatever becomes of the list.)
+    sections = None if sections is None else tuple(sections)
     return _RotaryQK.apply(q_raw, k_raw, q_weight, k_weight, positions, inv_freq,
                            dict(sections=sections, eps=eps, norm=norm, interleaved=interleaved))
 
