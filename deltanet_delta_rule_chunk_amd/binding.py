@@ -873,7 +873,10 @@ def rotary_qk(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torc
               k_weight: Optional[torch.Tensor] = None, sections=None, eps: float = 1e-6,
               norm: bool = True, interleaved: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable ``qk_norm_rope`` for training, with gradients for q_raw,
-    k_raw and the weights from ``deltanet_qk_norm_rope_bwd``."""
+    k_raw and the weights from ``deltanet_qk_norm_rope_bwd``.  There is none for
+    inv_freq, which may not ask for it."""
+    if inv_freq is not None and inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq has no gradient here (pass it detached)")
     # (A copy: the backward uses the sections of this call whatever becomes of the list.)
     sections = None if sections is None else tuple(sections)
     return _RotaryQK.apply(q_raw, k_raw, q_weight, k_weight, positions, inv_freq,

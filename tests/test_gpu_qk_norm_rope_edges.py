@@ -27,3 +27,13 @@ def test_sections_changed_after_the_call(gpu_lib):
     y, _ = N.rotary_qk(q, k, pos, inv, sections=[8, 24])
     want, = torch.autograd.grad(y.sum(), q)
     assert torch.equal(got, want)
+
+
+def test_a_frequency_that_asks_for_a_gradient_is_refused(gpu_lib):
+    q, k, pos, inv = _inputs()
+    inv.requires_grad_()
+    with pytest.raises(ValueError, match="inv_freq"):
+        N.rotary_qk(q, k, pos, inv, sections=[8, 24])
+    with torch.no_grad():
+        N.rotary_qk(q, k, pos, inv, sections=[8, 24])
+    N.rotary_qk(q, k, pos, inv.detach(), sections=[8, 24])
