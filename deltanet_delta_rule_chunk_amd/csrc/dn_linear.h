@@ -937,11 +937,12 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
   for (int ci = 0; ci < n; ++ci) {
     const int c = chunk(ci);
     const bool more = ci + 1 < n;
-    // (kPairs: addresses are formed anew in each chunk.  Kept over the loop they
+    // (dq and dk: addresses are formed anew in each chunk.  Kept over the loop they
     // do not fit beside the state, and a reload from scratch memory waits for
-    // every row on its way.)
+    // every row on its way.  Of the bf16 walks the 64 x 128 ones keep one value there,
+    // 8 bytes per lane; the others none.)
     int lane = threadIdx.x & 63;
-    if (EXTRA == kPairs) asm volatile("" : "+v"(lane));
+    if (EXTRA != kNone) asm volatile("" : "+v"(lane));
     const int lg = lane >> 4, li = lane & 15;
     // (Where the table lies is formed anew in each chunk as well: known for the whole
     // loop, every address into it would stay in a register.)
@@ -1035,9 +1036,13 @@ __device__ __forceinline__ void walk_segment(const OutArgs& a, int bh, int seg, 
 #pragma unroll
     for (int kb = 0; kb < WF; ++kb) {
       wf[kb] = row_frag<IT, DV>(wr, w_row(16 * prt + li), kb, lane);
-      if constexpr (NW == 4) wf2[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb, lane);
     }
     if (EXTRA == kPairs) make_p();
+    // (Behind P, whose fragments leave no registers for it.)
+#pragma unroll
+    for (int kb = 0; kb < WF; ++kb) {
+      if constexpr (NW == 4) wf2[kb] = row_frag<IT, DV>(wr, w_row(16 * prt2 + li), kb, lane);
+    }
     keep(gn);
 #pragma unroll
     for (int kb = 0; kb < WF; ++kb) {
