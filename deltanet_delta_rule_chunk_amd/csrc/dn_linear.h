@@ -51,9 +51,9 @@
 // are summed in fp64: a difference of two sums keeps the accuracy of the short
 // sum between them however long the chunk's own is.
 //
-// What bounds it.  32 heads of 128 x 128, bf16, L = 65536: segment sums 233 us (reads
-// 1.0 GB, 4.4 TB/s), outputs 475 us (2.2 GB, 4.6 TB/s): near the rate of HBM (a
-// copy reaches 5.2), with the matrix instructions busy for 46% of the time (740
+// What bounds it.  32 heads of 128 x 128, bf16, L = 65536: segment sums 231 us (reads
+// 1.0 GB, 4.4 TB/s), outputs 490 us (2.2 GB, 4.5 TB/s): near the rate of HBM (a
+// copy reaches 5.2), with the matrix instructions busy for 45% of the time (770
 // TFLOP/s as executed) and about as many cycles of vector work (pieces,
 // decays) beside them, which they hardly overlap.  At few rows, the latency of a
 // chunk: about 4 us, two barriers with P's way through LDS between them.
@@ -448,8 +448,8 @@ struct Split {
 // call, forward + backward: 4 bf16 heads of 128 x 128, L = 2000 100 -> 80 us of
 // kernels, 32 heads, L = 600 105 -> 91; 4 fp32 heads of 64 x 64, L = 1000 108 -> 64;
 // forward of 16 fp32 heads of 128 x 128, L = 2000 95 -> 69.  Long sequences of few
-// heads come out at 512 workgroups (32 heads of 128 x 128, L = 65536: 711 us of
-// kernels; with 1024 798, 384 798, 256 818).
+// heads come out at 512 workgroups (32 heads of 128 x 128, L = 65536, P in 2 pieces:
+// 711 us of kernels; with 1024 798, 384 798, 256 818).
 // None is longer than kMaxChunks, which bounds how far the decay's gradient is
 // carried from an exact value.
 constexpr int kMaxChunks = 256;

@@ -32,9 +32,9 @@
 // decay, whose gradient is small beside q . dq, keeps its accuracy.  The sums
 // over rows and chunks are taken in fp64; they are a few bytes per token.
 //
-// 32 heads of 128 x 128, bf16, L = 65536: sums of both directions 455 us, walks 1.79
-// ms (7.7 GB, 4.3 TB/s; matrix instructions busy for 42%, 757 TFLOP/s as
-// executed), the decay's gradient 23 us.  dk's and dv's walks of a segment side by
+// 32 heads of 128 x 128, bf16, L = 65536: sums of both directions 455 us, walks 1.84
+// ms (7.7 GB, 4.2 TB/s; matrix instructions busy for 42%, 745 TFLOP/s as
+// executed), the decay's gradient 28 us.  dk's and dv's walks of a segment side by
 // side on one XCD, for the rows that both read, took 1.84 ms for 1.75.
 //
 // Heads that share q and k: each state head's dq and dk go to the workspace

@@ -408,7 +408,9 @@ int deltanet_linear_decode_step(const void* q, const void* k, const void* v, con
  *   q_hat, k_hat  : [B, H_q, L, d_k], [B, H_k, L, d_k] dtype, dense, written
  *   d_k in {64, 128}; d_rot a multiple of 8, 0 .. d_k; n_axes 1 .. 4; eps >= 0.
  * Evaluated in fp32, angles in fp64 (any int32 position).  Rows beyond ~1e19
- * overflow their fp32 sum of squares (the row then maps to zeros).  Sizes beyond
+ * overflow their fp32 sum of squares (the row then maps to zeros); with eps = 0,
+ * rows below ~1e-18 lose bits of it, and rows of zeros or below ~1e-23 are not
+ * finite.  Sizes beyond
  * one launch are DN_ERR_UNSUPPORTED: with H_q + H_k <= 4, 2^24 - 1 times 32 tokens
  * of 64 elements or 16 of 128, with more heads that many fewer.
  */
