@@ -39,10 +39,18 @@ EXPORTS = ("deltanet_chunk_fwd", "deltanet_chunk_fwd_workspace_bytes", "deltanet
            "deltanet_linear_chunk_fwd", "deltanet_linear_chunk_fwd_workspace_bytes",
            "deltanet_linear_chunk_bwd", "deltanet_linear_chunk_bwd_workspace_bytes",
            "deltanet_linear_decode_step", "deltanet_qk_norm_rope", "deltanet_qk_norm_rope_bwd",
-           "deltanet_qk_norm_rope_bwd_workspace_bytes")
+           "deltanet_qk_norm_rope_bwd_workspace_bytes", "deltanet_short_conv_fwd",
+           "deltanet_short_conv_bwd", "deltanet_short_conv_bwd_workspace_bytes",
+           "deltanet_short_conv_step", "deltanet_selective_scan_fwd",
+           "deltanet_selective_scan_fwd_workspace_bytes", "deltanet_selective_scan_bwd",
+           "deltanet_selective_scan_bwd_workspace_bytes", "deltanet_selective_scan_step",
+           "deltanet_add_rms_norm", "deltanet_add_rms_norm_bwd",
+           "deltanet_add_rms_norm_bwd_workspace_bytes")
 PROFILE_SLOTS = ("chunk_prep", "chunk_scan", "decode", "features", "bwd_prep", "bwd_fwd_scan",
                  "bwd_scan", "bwd_cc", "bwd_qk", "linear_state", "linear_out", "linear_bwd",
-                 "linear_decode", "qk_norm_rope", "qk_norm_rope_bwd")
+                 "linear_decode", "qk_norm_rope", "qk_norm_rope_bwd", "short_conv",
+                 "short_conv_bwd", "selective_scan", "selective_scan_bwd", "selective_step",
+                 "add_norm", "add_norm_bwd")
 
 _lib = None
 
@@ -117,6 +125,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes, fn.restype = [i] * 7, sz
     lib.deltanet_qk_norm_rope_bwd_workspace_bytes.argtypes = [i] * 6
     lib.deltanet_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    for name, args in (("short_conv_fwd", [vp] * 8 + [i] * 7 + [vp]),
+                       ("short_conv_bwd", [vp] * 12 + [i] * 7 + [vp, sz, vp]),
+                       ("short_conv_step", [vp] * 6 + [i] * 5 + [vp]),
+                       ("selective_scan_fwd", [vp] * 13 + [i] * 7 + [vp, sz, vp]),
+                       ("selective_scan_bwd", [vp] * 22 + [i] * 7 + [vp, sz, vp]),
+                       ("selective_scan_step", [vp] * 11 + [i] * 5 + [vp]),
+                       ("add_rms_norm", [vp] * 6 + [i] * 2 + [f] + [i] * 2 + [vp]),
+                       ("add_rms_norm_bwd", [vp] * 7 + [i] * 2 + [f] + [i] * 2 + [vp, sz, vp])):
+        fn = getattr(lib, f"deltanet_{name}")
+        fn.argtypes, fn.restype = args, i
+    for name, args in (("short_conv_bwd", 4), ("selective_scan_fwd", 6),
+                       ("selective_scan_bwd", 6), ("add_rms_norm_bwd", 2)):
+        fn = getattr(lib, f"deltanet_{name}_workspace_bytes")
+        fn.argtypes, fn.restype = [i] * args, sz
     lib.deltanet_status_string.argtypes = [i]
     lib.deltanet_status_string.restype = ctypes.c_char_p
     lib.deltanet_last_hip_error.argtypes = []
@@ -881,6 +903,464 @@ def rotary_qk(q_raw: torch.Tensor, k_raw: torch.Tensor, positions: Optional[torc
     sections = None if sections is None else tuple(sections)
     return _RotaryQK.apply(q_raw, k_raw, q_weight, k_weight, positions, inv_freq,
                            dict(sections=sections, eps=eps, norm=norm, interleaved=interleaved))
+
+
+@functools.lru_cache(maxsize=1024)
+def _ll_array(*x):
+    return (ctypes.c_longlong * len(x))(*x)
+
+
+def _check_cu(cu_seqlens, B: int, device) -> int:
+    """Number of sequences: B of equal length, or what ``cu_seqlens`` packs in one row."""
+    if cu_seqlens is None:
+        return B
+    if B != 1:
+        raise ValueError(f"cu_seqlens packs sequences in one row: the batch must be 1 (got {B})")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [sequences + 1]")
+    _check(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
+    return cu_seqlens.shape[0] - 1
+
+
+def _check_optional(t, name, shape, dtype, device):
+    if t is not None:
+        _check(t, name, shape, dtype, device)
+
+
+def _conv_setup(x, weight, bias, state0, cu_seqlens, dims):
+    """Checks shared by the short convolution's calls; (sequences, K)."""
+    if x.dim() != dims or weight.dim() != 2:
+        raise ValueError(f"x must have {dims} dimensions and weight 2 "
+                         f"(got {tuple(x.shape)}, {tuple(weight.shape)})")
+    dev, dt, D, K = x.device, x.dtype, x.shape[-1], weight.shape[1]
+    _check_rows(x, "x", x.shape, dt, dev)
+    _check(weight, "weight", (D, K), torch.float32, dev)
+    _check_optional(bias, "bias", (D,), torch.float32, dev)
+    n = _check_cu(cu_seqlens, x.shape[0], dev)
+    _check_optional(state0, "state0", (n, K - 1, D), dt, dev)
+    return n, K
+
+
+def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   state0: Optional[torch.Tensor] = None, *, silu: bool = True,
+                   cu_seqlens: Optional[torch.Tensor] = None, want_state: bool = True,
+                   y: Optional[torch.Tensor] = None, stream=None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal convolution of every channel's last K tokens
+    (``deltanet_short_conv_fwd``): x ``[B,L,D]`` (fp32 or bf16) at any strides
+    with contiguous rows, weight ``[D,K]`` and bias ``[D]`` fp32, state0
+    ``[n,K-1,D]`` the rows kept from before (x's dtype) or None.  n is B, or with
+    ``cu_seqlens`` ([n+1] int32, B = 1) the sequences packed in the row; rows that
+    none of them holds become zeros.  Returns ``(y, state)``: y dense, state the
+    rows kept behind each sequence (None when ``want_state`` is False)."""
+    lib = _lib or load()
+    n, K = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
+    dev, dt, (B, L, D) = x.device, x.dtype, x.shape
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return short_conv_fwd(x, weight, bias, state0, silu=silu, cu_seqlens=cu_seqlens,
+                                  want_state=want_state, y=y, stream=stream)
+    if y is None:
+        y = _alloc((B, L, D), dt, dev, stream)
+    else:
+        _check(y, "y", (B, L, D), dt, dev)
+    state = _alloc((n, K - 1, D), dt, dev, stream) if want_state else None
+    st = lib.deltanet_short_conv_fwd(x.data_ptr(), _ll_array(*x.stride()[:2]), weight.data_ptr(),
+                                     _ptr(bias), _ptr(state0), _ptr(cu_seqlens), y.data_ptr(),
+                                     _ptr(state), B, L, D, K, n, int(silu), _code(dt),
+                                     _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_short_conv_fwd")
+    return y, state
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_bwd_workspace_bytes(*sizes) -> int:
+    return int(load().deltanet_short_conv_bwd_workspace_bytes(*sizes))
+
+
+def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                   state0: Optional[torch.Tensor], dy: torch.Tensor,
+                   dstate: Optional[torch.Tensor] = None, *, silu: bool = True,
+                   cu_seqlens: Optional[torch.Tensor] = None, want_dstate0: bool = True,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of ``short_conv_fwd`` (``deltanet_short_conv_bwd``) from dy
+    ``[B,L,D]`` and dstate ``[n,K-1,D]`` (or None), both in x's dtype.  Returns
+    ``(dx, dweight, dbias, dstate0)``: dx and dstate0 (None when
+    ``want_dstate0`` is False) in x's dtype, dweight and dbias (None without a
+    bias) fp32."""
+    lib = _lib or load()
+    n, K = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
+    dev, dt, (B, L, D) = x.device, x.dtype, x.shape
+    _check(dy, "dy", (B, L, D), dt, dev)
+    _check_optional(dstate, "dstate", (n, K - 1, D), dt, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return short_conv_bwd(x, weight, bias, state0, dy, dstate, silu=silu,
+                                  cu_seqlens=cu_seqlens, want_dstate0=want_dstate0,
+                                  workspace=workspace, stream=stream)
+    dx, dw = _alloc((B, L, D), dt, dev, stream), _alloc((D, K), torch.float32, dev, stream)
+    db = None if bias is None else _alloc((D,), torch.float32, dev, stream)
+    ds = _alloc((n, K - 1, D), dt, dev, stream) if want_dstate0 else None
+    keep, ws, ws_bytes = _workspace(workspace, _conv_bwd_workspace_bytes(B, L, D, K), dev, stream)
+    st = lib.deltanet_short_conv_bwd(x.data_ptr(), _ll_array(*x.stride()[:2]), weight.data_ptr(),
+                                     _ptr(bias), _ptr(state0), _ptr(cu_seqlens), dy.data_ptr(),
+                                     _ptr(dstate), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds),
+                                     B, L, D, K, n, int(silu), _code(dt), ws, ws_bytes,
+                                     _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_short_conv_bwd")
+    return dx, dw, db, ds
+
+
+class _ShortConv(torch.autograd.Function):
+    """``short_conv_fwd`` with its gradient from ``short_conv_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state0, cu_seqlens, silu):
+        ctx.save_for_backward(x, weight, bias, state0, cu_seqlens)
+        ctx.silu = silu
+        return short_conv_fwd(x, weight, bias, state0, silu=silu, cu_seqlens=cu_seqlens)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dstate):
+        x, weight, bias, state0, cu_seqlens = ctx.saved_tensors
+        want = state0 is not None and ctx.needs_input_grad[3]
+        return (*short_conv_bwd(x, weight, bias, state0, dy.contiguous(), dstate.contiguous(),
+                                silu=ctx.silu, cu_seqlens=cu_seqlens, want_dstate0=want), None, None)
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               state0: Optional[torch.Tensor] = None, *, silu: bool = True,
+               cu_seqlens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable ``short_conv_fwd`` for training: ``(y, state)``, with gradients
+    for x, weight, bias and state0 from ``deltanet_short_conv_bwd``."""
+    return _ShortConv.apply(x, weight, bias, state0, cu_seqlens, bool(silu))
+
+
+def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                    state: torch.Tensor, *, silu: bool = True, y: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """One token of the short convolution (``deltanet_short_conv_step``): x ``[B,D]``
+    (rows at any stride), state ``[B,K-1,D]`` moved on in place; returns y ``[B,D]``."""
+    lib = _lib or load()
+    _, K = _conv_setup(x, weight, bias, state, None, 2)
+    dev, dt, (B, D) = x.device, x.dtype, x.shape
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return short_conv_step(x, weight, bias, state, silu=silu, y=y, stream=stream)
+    if y is None:
+        y = _alloc((B, D), dt, dev, stream)
+    else:
+        _check(y, "y", (B, D), dt, dev)
+    st = lib.deltanet_short_conv_step(x.data_ptr(), _ll_array(x.stride(0)), weight.data_ptr(),
+                                      _ptr(bias), state.data_ptr(), y.data_ptr(), B, D, K,
+                                      int(silu), _code(dt), _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_short_conv_step")
+    return y
+
+
+def _scan_setup(u, dt, A, B, C, D, z, dt_bias, state, cu_seqlens, dims):
+    """Checks shared by the selective scan's calls; (sequences, N, leading arguments)."""
+    if u.dim() != dims or A.dim() != 2:
+        raise ValueError(f"u must have {dims} dimensions and A 2 "
+                         f"(got {tuple(u.shape)}, {tuple(A.shape)})")
+    dev, ty, width, N = u.device, u.dtype, u.shape[-1], A.shape[1]
+    few = (*u.shape[:-1], N)
+    _check_rows(u, "u", u.shape, ty, dev)
+    _check_rows(dt, "dt", u.shape, ty, dev)
+    _check_rows(B, "B", few, ty, dev)
+    _check_rows(C, "C", few, ty, dev)
+    if z is not None:
+        _check_rows(z, "z", u.shape, ty, dev)
+    _check(A, "A", (width, N), torch.float32, dev)
+    _check_optional(D, "D", (width,), torch.float32, dev)
+    _check_optional(dt_bias, "dt_bias", (width,), torch.float32, dev)
+    n = _check_cu(cu_seqlens, u.shape[0], dev)
+    _check_optional(state, "the state", (n, width, N), torch.float32, dev)
+    gate = u if z is None else z
+    strides = _ll_array(*u.stride()[:-1], *dt.stride()[:-1], *B.stride()[:-1], *C.stride()[:-1],
+                        *gate.stride()[:-1])
+    return n, N, (u.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(z), strides,
+                  A.data_ptr(), _ptr(D), _ptr(dt_bias))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace_bytes(backward, *sizes) -> int:
+    lib = load()
+    fn = (lib.deltanet_selective_scan_bwd_workspace_bytes if backward
+          else lib.deltanet_selective_scan_fwd_workspace_bytes)
+    return int(fn(*sizes))
+
+
+def selective_scan_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                       C: torch.Tensor, *, D: Optional[torch.Tensor] = None,
+                       z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                       h0: Optional[torch.Tensor] = None, softplus: bool = True,
+                       cu_seqlens: Optional[torch.Tensor] = None, want_state: bool = True,
+                       y: Optional[torch.Tensor] = None, hT: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Selective state space scan (``deltanet_selective_scan_fwd``): with
+    ``s = softplus(dt + dt_bias)`` (``softplus=False``: the sum itself),
+    ``h = e^{s A} h + s u B``, ``y = (C h + D u) silu(z)``.  u, dt, z ``[B,L,D]``
+    and B, C ``[B,L,N]`` (fp32 or bf16, same dtype) at any strides with contiguous
+    rows; A ``[D,N]``, D and dt_bias ``[D]`` fp32 or None; h0 ``[n,D,N]`` fp32 or
+    None; ``cu_seqlens`` as in ``short_conv_fwd``.  Returns ``(y, hT)``; hT is
+    None when ``want_state`` is False, and may be given (h0 itself: in place)."""
+    lib = _lib or load()
+    n, N, lead = _scan_setup(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 3)
+    dev, ty, (nb, L, width) = u.device, u.dtype, u.shape
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return selective_scan_fwd(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0,
+                                      softplus=softplus, cu_seqlens=cu_seqlens,
+                                      want_state=want_state, y=y, hT=hT, workspace=workspace,
+                                      stream=stream)
+    if y is None:
+        y = _alloc((nb, L, width), ty, dev, stream)
+    else:
+        _check(y, "y", (nb, L, width), ty, dev)
+    if hT is not None:
+        _check(hT, "hT", (n, width, N), torch.float32, dev)
+    elif want_state:
+        hT = _alloc((n, width, N), torch.float32, dev, stream)
+    need = _scan_workspace_bytes(False, nb, L, width, N, int(cu_seqlens is not None), n)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_selective_scan_fwd(*lead, _ptr(h0), _ptr(cu_seqlens), y.data_ptr(), _ptr(hT),
+                                         nb, L, width, N, n, int(softplus), _code(ty), ws, ws_bytes,
+                                         _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_selective_scan_fwd")
+    return y, hT
+
+
+def selective_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                       C: torch.Tensor, dy: torch.Tensor, dhT: Optional[torch.Tensor] = None, *,
+                       D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                       softplus: bool = True, cu_seqlens: Optional[torch.Tensor] = None,
+                       want_dh0: bool = True, workspace: Optional[torch.Tensor] = None,
+                       stream=None):
+    """Gradient of ``selective_scan_fwd`` (``deltanet_selective_scan_bwd``) from dy
+    ``[B,L,D]`` (u's dtype) and dhT ``[n,D,N]`` fp32 or None.  Returns ``(du, ddt,
+    dA, dB, dC, dD, dz, ddt_bias, dh0)``: du, ddt, dz, dB, dC in u's dtype, the
+    others fp32; dD, dz, ddt_bias are None where their input is, dh0 when
+    ``want_dh0`` is False."""
+    lib = _lib or load()
+    n, N, lead = _scan_setup(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 3)
+    dev, ty, (nb, L, width) = u.device, u.dtype, u.shape
+    _check(dy, "dy", (nb, L, width), ty, dev)
+    _check_optional(dhT, "dhT", (n, width, N), torch.float32, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return selective_scan_bwd(u, dt, A, B, C, dy, dhT, D=D, z=z, dt_bias=dt_bias, h0=h0,
+                                      softplus=softplus, cu_seqlens=cu_seqlens, want_dh0=want_dh0,
+                                      workspace=workspace, stream=stream)
+    rows = lambda w: _alloc((nb, L, w), ty, dev, stream)  # noqa: E731
+    f32 = lambda *s: _alloc(s, torch.float32, dev, stream)  # noqa: E731
+    du, ddt, dB, dC = rows(width), rows(width), rows(N), rows(N)
+    dz = None if z is None else rows(width)
+    dA = f32(width, N)
+    dD = None if D is None else f32(width)
+    dbias = None if dt_bias is None else f32(width)
+    dh0 = f32(n, width, N) if want_dh0 else None
+    need = _scan_workspace_bytes(True, nb, L, width, N, int(cu_seqlens is not None), n)
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_selective_scan_bwd(*lead, _ptr(h0), _ptr(cu_seqlens), dy.data_ptr(),
+                                         _ptr(dhT), du.data_ptr(), ddt.data_ptr(), dB.data_ptr(),
+                                         dC.data_ptr(), _ptr(dz), dA.data_ptr(), _ptr(dD),
+                                         _ptr(dbias), _ptr(dh0), nb, L, width, N, n, int(softplus),
+                                         _code(ty), ws, ws_bytes, _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_selective_scan_bwd")
+    return du, ddt, dA, dB, dC, dD, dz, dbias, dh0
+
+
+class _SelectiveScan(torch.autograd.Function):
+    """``selective_scan_fwd`` with its gradient from ``selective_scan_bwd``, which
+    needs only the inputs."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, softplus):
+        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+        ctx.softplus = softplus
+        return selective_scan_fwd(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0,
+                                  softplus=softplus, cu_seqlens=cu_seqlens)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dhT):
+        u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens = ctx.saved_tensors
+        want = h0 is not None and ctx.needs_input_grad[8]
+        return (*selective_scan_bwd(u, dt, A, B, C, dy.contiguous(), dhT.contiguous(), D=D, z=z,
+                                    dt_bias=dt_bias, h0=h0, softplus=ctx.softplus,
+                                    cu_seqlens=cu_seqlens, want_dh0=want), None, None)
+
+
+def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                   C: torch.Tensor, *, D: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                   h0: Optional[torch.Tensor] = None, softplus: bool = True,
+                   cu_seqlens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable ``selective_scan_fwd`` for training: ``(y, hT)``, with
+    gradients for every input but ``cu_seqlens`` from ``deltanet_selective_scan_bwd``."""
+    return _SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, bool(softplus))
+
+
+def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        C: torch.Tensor, h: torch.Tensor, *, D: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                        softplus: bool = True, y: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """One token of the selective scan (``deltanet_selective_scan_step``): u, dt, z
+    ``[B,D]``, B, C ``[B,N]`` (rows at any stride), h ``[B,D,N]`` fp32 updated in
+    place; returns y ``[B,D]``."""
+    lib = _lib or load()
+    _, N, lead = _scan_setup(u, dt, A, B, C, D, z, dt_bias, h, None, 2)
+    dev, ty, (nb, width) = u.device, u.dtype, u.shape
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return selective_scan_step(u, dt, A, B, C, h, D=D, z=z, dt_bias=dt_bias,
+                                       softplus=softplus, y=y, stream=stream)
+    if y is None:
+        y = _alloc((nb, width), ty, dev, stream)
+    else:
+        _check(y, "y", (nb, width), ty, dev)
+    st = lib.deltanet_selective_scan_step(*lead, h.data_ptr(), y.data_ptr(), nb, width, N,
+                                          int(softplus), _code(ty), _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_selective_scan_step")
+    return y
+
+
+def _add_norm(x, residual, weight, eps, total, y, out8, stream):
+    lib = _lib or load()
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if not shape:
+        raise ValueError("x must have rows")
+    D = shape[-1]
+    _check(x, "x", shape, dt, dev)
+    rdt = dt
+    if residual is not None:
+        rdt = residual.dtype
+        _check(residual, "residual", shape, rdt, dev)
+    elif total is not None:
+        raise ValueError("total is only written with a residual")
+    _check_optional(weight, "weight", (D,), torch.float32, dev)
+    _check_optional(total, "total", shape, rdt, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _add_norm(x, residual, weight, eps, total, y, out8, stream)
+    if residual is not None and total is None:
+        total = _alloc(shape, rdt, dev, stream)
+    ydt = torch.float8_e4m3fn if out8 else dt
+    if y is None:
+        y = _alloc(shape, ydt, dev, stream)
+    else:
+        _check(y, "y", shape, ydt, dev)
+    scale = _alloc(shape[:-1], torch.float32, dev, stream) if out8 else None
+    rows = x.numel() // D if D else 0
+    st = lib.deltanet_add_rms_norm(x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(total),
+                                   y.data_ptr(), _ptr(scale), rows, D, eps, _code(dt), _code(rdt),
+                                   _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_add_rms_norm")
+    return y, scale, x if residual is None else total
+
+
+def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                 *, eps: float = 1e-6, total: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Root-mean-square norm with the residual's addition (``deltanet_add_rms_norm``):
+    ``total = x + residual`` and ``y = total / rms(total) * weight`` over the last
+    dimension.  x fp32 or bf16, residual the same or fp32 (total takes its dtype) or
+    None (total is x), weight ``[D]`` fp32 or None.  Returns ``(y, total)``;
+    ``total`` may be given, the residual itself among them (in place)."""
+    y, _, total = _add_norm(x, residual, weight, eps, total, y, False, stream)
+    return y, total
+
+
+def add_rms_norm_fp8(x: torch.Tensor, residual: Optional[torch.Tensor],
+                     weight: Optional[torch.Tensor], *, eps: float = 1e-6,
+                     total: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """``add_rms_norm`` with y in 8 bits for projections in 8 bits: returns ``(y8,
+    scale, total)``, y8 ``float8_e4m3fn`` and scale fp32, one per row, with
+    ``y = y8 * scale``."""
+    return _add_norm(x, residual, weight, eps, total, y, True, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_workspace_bytes(rows, D) -> int:
+    return int(load().deltanet_add_rms_norm_bwd_workspace_bytes(rows, D))
+
+
+def add_rms_norm_bwd(total: torch.Tensor, weight: Optional[torch.Tensor], dy: torch.Tensor,
+                     dtotal: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of ``add_rms_norm`` (``deltanet_add_rms_norm_bwd``) from dy (x's dtype)
+    and dtotal (total's dtype, or None).  Returns ``(dx, dresidual, dweight)``: dx in
+    dy's dtype, dresidual in total's (the same tensor where they agree), dweight fp32
+    (None without a weight)."""
+    lib = _lib or load()
+    dev, dt, rdt, shape = total.device, dy.dtype, total.dtype, total.shape
+    if not shape:
+        raise ValueError("total must have rows")
+    D = shape[-1]
+    _check(total, "total", shape, rdt, dev)
+    _check(dy, "dy", shape, dt, dev)
+    _check_optional(dtotal, "dtotal", shape, rdt, dev)
+    _check_optional(weight, "weight", (D,), torch.float32, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return add_rms_norm_bwd(total, weight, dy, dtotal, eps=eps, workspace=workspace,
+                                    stream=stream)
+    dx = _alloc(shape, dt, dev, stream)
+    dres = None if rdt == dt else _alloc(shape, rdt, dev, stream)
+    dw = None if weight is None else _alloc((D,), torch.float32, dev, stream)
+    rows = total.numel() // D if D else 0
+    need = _norm_bwd_workspace_bytes(rows, D) if dw is not None else 0
+    keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
+    st = lib.deltanet_add_rms_norm_bwd(total.data_ptr(), _ptr(weight), dy.data_ptr(), _ptr(dtotal),
+                                       dx.data_ptr(), _ptr(dres), _ptr(dw), rows, D, eps, _code(dt),
+                                       _code(rdt), ws, ws_bytes, _stream(dev, stream))
+    if st != DN_OK:
+        _raise(lib, st, "deltanet_add_rms_norm_bwd")
+    return dx, dx if dres is None else dres, dw
+
+
+class _ResidualNorm(torch.autograd.Function):
+    """``add_rms_norm`` with its gradient from ``add_rms_norm_bwd``."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        y, total = add_rms_norm(x, residual, weight, eps=eps)
+        ctx.save_for_backward(total, weight)
+        ctx.eps = eps
+        return (y, total) if residual is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dtotal=None):
+        total, weight = ctx.saved_tensors
+        dx, dres, dw = add_rms_norm_bwd(total, weight, dy.contiguous(),
+                                        None if dtotal is None else dtotal.contiguous(),
+                                        eps=ctx.eps)
+        return dx, dres if ctx.needs_input_grad[1] else None, dw, None
+
+
+def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor],
+                  weight: Optional[torch.Tensor], *, eps: float = 1e-6
+                  ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable ``add_rms_norm`` for training: ``(y, total)``, with gradients for
+    x, residual and weight from ``deltanet_add_rms_norm_bwd``."""
+    if residual is None:
+        return _ResidualNorm.apply(x, None, weight, eps), x
+    return _ResidualNorm.apply(x, residual, weight, eps)
 
 
 def profile_start() -> None:

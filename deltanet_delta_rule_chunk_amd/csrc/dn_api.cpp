@@ -12,7 +12,10 @@
 
 #include <vector>
 
+#include "dn_api_util.h"
 #include "dn_launch.h"
+
+using namespace dn::api;
 
 namespace {
 
@@ -20,28 +23,8 @@ thread_local int g_last_hip_error = 0;
 
 constexpr int kVersion = 500;  // 0.5.0
 
-int hip_fail(hipError_t e) {
-  g_last_hip_error = static_cast<int>(e);
-  return DN_ERR_HIP;
-}
-
-bool dtype_ok(int t) { return t == DN_F32 || t == DN_BF16; }
-size_t dtype_size(int t) { return t == DN_F32 ? 4 : 2; }
 bool dim_ok(int d) { return d == 64 || d == 128; }
 bool chunk_ok(int c) { return c == 64 || c == 128; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span {
-  const void* p;
-  size_t n;  // bytes
-};
-
-bool overlap(Span a, Span b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
 struct ChunkSizes {
   size_t qk, v, beta, o, state;
 };
@@ -82,62 +65,6 @@ int check_linear_shape(int B, int H, int H_qk, int L, int d_k, int d_v, int in_d
   s->state = (size_t)B * H * d_k * d_v * sizeof(float);
   return DN_OK;
 }
-
-template <int N>
-bool any_misaligned(const void* const (&ptrs)[N]) {
-  for (const void* p : ptrs)
-    if (p && !aligned16(p)) return true;
-  return false;
-}
-
-// Whether any output overlaps an input, another output or the workspace, or
-// the workspace an input.
-template <int NI, int NO>
-bool any_overlap(const Span (&in)[NI], const Span (&out)[NO], Span ws) {
-  for (int i = 0; i < NO; ++i) {
-    for (const Span& x : in)
-      if (overlap(out[i], x)) return true;
-    for (int j = i + 1; j < NO; ++j)
-      if (overlap(out[i], out[j])) return true;
-    if (overlap(ws, out[i])) return true;
-  }
-  for (const Span& x : in)
-    if (overlap(ws, x)) return true;
-  return false;
-}
-
-// The caller's workspace, or one allocated and freed on the stream.
-class Workspace {
- public:
-  Workspace(void* given, size_t need, hipStream_t stream) : p_(given), stream_(stream) {
-    if (!given && need > 0) {
-      error_ = hipMallocAsync(&p_, need, stream);
-      own_ = error_ == hipSuccess;
-    }
-  }
-  Workspace(const Workspace&) = delete;
-  Workspace& operator=(const Workspace&) = delete;
-  ~Workspace() {
-    if (own_) (void)hipFreeAsync(p_, stream_);
-  }
-  hipError_t error() const { return error_; }
-  void* get() const { return p_; }
-  // Frees it; the first error of the call.
-  hipError_t done(hipError_t e) {
-    if (own_) {
-      own_ = false;
-      const hipError_t f = hipFreeAsync(p_, stream_);
-      if (e == hipSuccess) e = f;
-    }
-    return e;
-  }
-
- private:
-  void* p_;
-  hipStream_t stream_;
-  hipError_t error_ = hipSuccess;
-  bool own_ = false;
-};
 
 // Rows of d elements of [B, H, L, d] at given strides (null: dense).
 struct StridedRows {
@@ -430,6 +357,11 @@ int decode_impl(const void* q, const void* k, const void* v, const float* alpha,
 
 namespace dn {
 
+int api::hip_fail(hipError_t e) {
+  g_last_hip_error = static_cast<int>(e);
+  return DN_ERR_HIP;
+}
+
 void prof_mark(int slot, bool end, hipStream_t s) {
   if (!g_prof.on) return;
   hipEvent_t e = prof_event();
@@ -503,9 +435,9 @@ const char* deltanet_status_string(int status) {
     case DN_OK: return "ok";
     case DN_ERR_NULL_ARG: return "a required pointer is NULL";
     case DN_ERR_BAD_SHAPE:
-      return "invalid size (B, H, d_k, d_v, C must be >= 1; L >= 0; H a multiple of H_qk; sections adding up to d_rot / 2; strides >= 0)";
+      return "invalid size (B, H, d_k, d_v, C must be >= 1; L >= 0; H a multiple of H_qk; sections adding up to d_rot / 2; strides >= 0; packed sequences in one row, B = 1)";
     case DN_ERR_UNSUPPORTED:
-      return "unsupported configuration (d_k, d_v in {64,128}; C in {64,128}; dtype f32/bf16; B*H <= 65535; d_rot a multiple of 8 up to d_k; up to 4 position axes; eps >= 0)";
+      return "unsupported configuration (d_k, d_v in {64,128}; C in {64,128}; dtype f32/bf16; B*H <= 65535; d_rot a multiple of 8 up to d_k; up to 4 position axes; eps >= 0; channels a multiple of 8, K in {2,3,4}, N in {8,16,32})";
     case DN_ERR_MISALIGNED: return "a tensor pointer is not 16-byte aligned";
     case DN_ERR_ALIASING: return "an output overlaps an input";
     case DN_ERR_WORKSPACE: return "workspace smaller than the matching *_workspace_bytes() query";

@@ -92,7 +92,14 @@ enum ProfSlot {
   kSlotLinearDecode = 12,
   kSlotQkNormRope = 13,
   kSlotQkNormRopeBwd = 14,
-  kNumSlots = 15
+  kSlotShortConv = 15,
+  kSlotShortConvBwd = 16,
+  kSlotSelectiveScan = 17,
+  kSlotSelectiveScanBwd = 18,
+  kSlotSelectiveStep = 19,
+  kSlotAddNorm = 20,
+  kSlotAddNormBwd = 21,
+  kNumSlots = 22
 };
 
 // Records a HIP event on `s` before (end = false) or after (end = true) the
@@ -198,6 +205,79 @@ hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a);
 long long qk_norm_rope_max_tokens(int heads, int d);
 size_t qk_norm_rope_bwd_workspace_bytes(int B, int heads, int L, int d);
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeArgs& a);
+
+// Rows of [B, L, D] at strides in elements.
+struct TokenRows {
+  const void* p;
+  long long sb, sl;
+};
+
+// Short causal convolution of every channel (dn_short_conv.hip).
+struct ShortConvArgs {
+  TokenRows x;
+  const float* weight;  // [D][K]
+  const float* bias;    // [D] or null
+  const void* state0;   // [n_seq][K-1][D] or null (zeros)
+  const int* cu;        // [n_seq + 1] or null: B sequences of L
+  int B, L, D, K, n_seq, silu, dtype;
+  void* y;              // forward
+  void* state;          // forward: or null; step: updated in place
+  const void *dy, *dstate;  // backward; dstate or null
+  void *dx, *dstate0;       // backward; dstate0 or null
+  float *dweight, *dbias;   // backward; dbias or null
+  void* workspace;          // backward: at least short_conv_bwd_workspace_bytes(...) bytes
+  hipStream_t stream;
+};
+bool short_conv_fits(int B, int L, int D, int n_seq, int dtype);
+hipError_t launch_short_conv(const ShortConvArgs& a);
+size_t short_conv_bwd_workspace_bytes(int B, int L, int D, int K);
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a);
+hipError_t launch_short_conv_step(const ShortConvArgs& a);
+
+// Selective state space scan (dn_selective_scan.hip, dn_selective_scan_bwd.hip).
+struct ScanArgs {
+  TokenRows u, dt, Bm, Cm, z;  // z.p null: no gate
+  const float* A;              // [D][N]
+  const float *skip, *dt_bias; // [D] or null
+  const float* h0;             // [n_seq][D][N] or null (zeros)
+  const int* cu;               // [n_seq + 1] or null: B sequences of L
+  int B, L, D, N, n_seq, softplus, dtype;
+  void* y;                     // forward, step
+  float* hT;                   // forward: or null; step: updated in place
+  const void* dy;              // backward
+  const float* dhT;            // or null (zeros)
+  void *du, *ddt, *dB, *dC, *dz;
+  float *dA, *dskip, *dbias, *dh0;  // dskip, dbias, dh0 or null
+  void* workspace;
+  hipStream_t stream;
+};
+bool selective_scan_fits(int B, int L, int D, int N, bool packed, int n_seq, bool backward);
+size_t selective_scan_workspace_bytes(int B, int L, int D, int N, bool packed, int n_seq);
+hipError_t launch_selective_scan(const ScanArgs& a);
+size_t selective_scan_bwd_workspace_bytes(int B, int L, int D, int N, bool packed, int n_seq);
+hipError_t launch_selective_scan_bwd(const ScanArgs& a);
+hipError_t launch_selective_scan_step(const ScanArgs& a);
+
+// Root-mean-square norm with the residual's addition (dn_add_norm.hip).
+struct AddNormArgs {
+  const void* x;
+  const void* residual;  // or null
+  const float* weight;   // or null (ones)
+  void* total;           // x + residual; null without a residual
+  void* y;
+  float* scale;          // [rows]: y is e4m3; or null
+  int rows, D, dtype, residual_dtype;
+  float eps;
+  const void *dy, *dtotal;  // backward (total is read); dtotal or null
+  void *dx, *dresidual;     // backward; dresidual null where it is dx
+  float* dweight;           // backward; or null
+  void* workspace;
+  hipStream_t stream;
+};
+bool add_norm_fits(int rows, int D);
+hipError_t launch_add_norm(const AddNormArgs& a);
+size_t add_norm_bwd_workspace_bytes(int rows, int D);
+hipError_t launch_add_norm_bwd(const AddNormArgs& a);
 
 // The fixed per-GPU scratch area of the allocation-free forward
 // (dn_noalloc.hip): its size, and its address on the device `stream` belongs

@@ -1,0 +1,155 @@
+// dn_selective_scan.h -- what the selective scan's forward and backward share:
+// the segments that sequences are cut into, and a workgroup's tile of tokens.
+//
+// Per channel d and state n, token t in order:
+//     h = e^{dt_t A} h + dt_t u_t B_t,   y_t = sum_n C_t h + D u_t
+// with dt_t = softplus(raw_t + bias).  Each (d, n) is a recurrence of its own
+// with a decay of its own, so there is no matrix product in it: the work is a
+// multiplication, an exponential and three more operations on every
+// (token, channel, state) and the vector units bound it.
+//
+// A workgroup takes 64 channels, one per lane, and a wave 4 of their states, so
+// that B_t and C_t are the same for all lanes of a wave (scalar loads) and a
+// token's sum over states is 4 steps in registers and one sum over the waves.
+// Tokens go in tiles of 16: the threads first form dt and dt u of the tile
+// (4 channels of one token each) and leave them in LDS, then every wave walks
+// the 16 tokens, then the threads add up the waves' parts and finish y.
+#pragma once
+
+#include "dn_launch.h"
+#include "dn_vec.h"
+
+namespace dn {
+namespace ssm {
+
+constexpr int kTile = 16;  // tokens
+constexpr int kCh = 64;    // channels per workgroup
+
+// A piece of one sequence.  Rows that no sequence holds form segments too (seq
+// < 0), whose outputs are zeros.
+struct Segment {
+  int row, n;     // first token within the batch row, tokens
+  int seq, batch;
+  bool first, last;  // of its sequence
+};
+
+// Where the segments lie: counted out for a batch of equal sequences, from a
+// table in the workspace (segment_table_kernel) for packed ones.
+struct Plan {
+  const int* used;      // packed: segments in the table, or null
+  const int* first_of;  // packed: first segment of each sequence [n_seq + 1]
+  const int4* table;    // packed: {row, n, seq, first | last << 1}
+  int len;              // tokens per segment, a multiple of kTile
+  int per_row;          // equal sequences: segments of each
+  int L;
+  int count;            // segments launched (packed: the most there can be)
+};
+
+__device__ __forceinline__ bool segment_of(const Plan& p, int id, Segment& s) {
+  if (!p.table) {
+    s.batch = s.seq = id / p.per_row;
+    const int i = id - s.seq * p.per_row;
+    s.row = i * p.len;
+    s.n = min(p.len, p.L - s.row);
+    s.first = i == 0;
+    s.last = i == p.per_row - 1;
+    return true;
+  }
+  if (id >= *p.used) return false;
+  const int4 e = p.table[id];
+  s.row = e.x;
+  s.n = e.y;
+  s.seq = e.z;
+  s.batch = 0;
+  s.first = e.w & 1;
+  s.last = e.w & 2;
+  return true;
+}
+// First and last segment of a sequence.
+__device__ __forceinline__ void segments_of(const Plan& p, int seq, int& first, int& last) {
+  first = p.table ? p.first_of[seq] : seq * p.per_row;
+  last = p.table ? p.first_of[seq + 1] - 1 : first + p.per_row - 1;
+}
+// Number of a segment's first tile, when tiles are kept: segments follow each other
+// by rows, so each may take one tile more than its rows fill.
+__device__ __forceinline__ long long first_tile(const Plan& p, const Segment& s, int id) {
+  return ((long long)s.batch * p.L + s.row) / kTile + id;
+}
+
+// Host side.
+struct Sizes {
+  int len, per_row;
+  long long segments;  // the most there can be
+  bool split;          // whether a sequence may have more than one
+};
+inline long long channel_blocks(int D) { return (D + kCh - 1) / kCh; }
+// A length of segment for `streams` sequences of at most L tokens, `most`
+// workgroups or more being enough without a cut, `want` being aimed at with one.
+inline Sizes sizes_of(bool packed, int B, int L, int n_seq, int D, long long enough, long long want, int least) {
+  const long long groups = B * channel_blocks(D);
+  Sizes s;
+  const long long whole = ((long long)L + kTile - 1) / kTile * kTile;
+  s.len = (int)(whole < kTile ? kTile : whole > 0x7fffffe0LL ? 0x7fffffe0LL : whole);
+  if (groups < enough && L > least) {
+    const long long pieces = (want + groups - 1) / groups;
+    long long len = ((long long)L + pieces - 1) / pieces;
+    len = (len + kTile - 1) / kTile * kTile;
+    s.len = (int)(len < least ? least : len);
+  }
+  s.per_row = L > 0 ? (int)(((long long)L + s.len - 1) / s.len) : 1;
+  s.segments = packed ? (long long)L / s.len + n_seq + 2 : (long long)B * s.per_row;
+  s.split = s.per_row > 1;
+  return s;
+}
+inline size_t table_bytes(bool packed, int n_seq, const Sizes& s) {
+  if (!packed) return 0;
+  return (size_t)((n_seq + 2 + 3) / 4 * 4) * sizeof(int) + (size_t)s.segments * sizeof(int4);
+}
+Sizes backward_sizes(int B, int L, int D, bool packed, int n_seq);  // (dn_selective_scan_bwd.hip)
+// Places the table in `ws` and launches the kernel that fills it.
+hipError_t make_plan(const int* cu, int n_seq, int L, const Sizes& s, void* ws, hipStream_t stream, Plan* p);
+
+// Four values that are the same for a whole wave, through the scalar cache.
+typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
+__device__ __forceinline__ f32x4 uniform4(const bf16* p) {
+  const scalar_ptr q = (scalar_ptr)(uintptr_t)p;
+  const uint32_t a = q[0], b = q[1];
+  return f32x4{__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+               __uint_as_float(b & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 uniform4(const float* p) {
+  const scalar_ptr q = (scalar_ptr)(uintptr_t)p;
+  return f32x4{__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]), __uint_as_float(q[3])};
+}
+
+// A thread's place in the phases before and after the walk: a token of the tile and
+// 4 channels.
+template <int NW>
+struct Spot {
+  static constexpr int kRows = 4 * NW;                            // tokens per pass
+  static constexpr int kPasses = kRows >= kTile ? 1 : kTile / kRows;
+  int r, c;  // first token, first channel
+  __device__ __forceinline__ Spot() : r((int)threadIdx.x >> 4), c(((int)threadIdx.x & 15) * 4) {}
+  __device__ __forceinline__ int row(int pass) const { return r + pass * kRows; }
+  __device__ __forceinline__ bool in_tile(int pass) const { return kRows <= kTile || r < kTile; }
+};
+
+__device__ __forceinline__ f32x4 softplus4(f32x4 x, bool on) {
+  if (!on) return x;
+  return f32x4{softplus(x[0]), softplus(x[1]), softplus(x[2]), softplus(x[3])};
+}
+__device__ __forceinline__ f32x4 sigmoid4(f32x4 x) {
+  return f32x4{sigmoid(x[0]), sigmoid(x[1]), sigmoid(x[2]), sigmoid(x[3])};
+}
+__device__ __forceinline__ f32x4 get4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
+// States of a sequence in front of each of its segments, in place of what each
+// segment makes from zero (the first: from h0) -- and, where `back` is given, gradients
+// of the states behind each segment in place of what each passes to its front (the
+// last: from the last state's).  Both [seg][D][N]; logs [seg][D]: sums of dt.
+// (dn_selective_scan.hip)
+hipError_t combine(const Plan& p, int n_seq, int D, int N, const float* A, const float* logs, const float* h0,
+                   float* ahead, float* back, hipStream_t stream);
+
+}  // namespace ssm
+}  // namespace dn

@@ -1,0 +1,355 @@
+// dn_selective_scan.hip -- the selective state space scan's forward on gfx950,
+// over sequences and for single tokens (the recurrence and a workgroup's tile: see
+// dn_selective_scan.h).
+//
+// Few sequences of few channels do not fill the card: their sequences are cut
+// into segments.  A first walk makes every segment's last state from zero and
+// the sum of its dt (the decay over a segment is e^{A sum dt}), combine() turns
+// them into the states in front of the segments, and the second walk makes the
+// outputs.  Enough of them take one walk.
+
+#include "dn_selective_scan.h"
+
+namespace dn {
+namespace ssm {
+
+// ---- segments of packed sequences -----------------------------------------------------
+
+// One workgroup.  Sequence i holds the rows from cu[i] to cu[i + 1]; whatever
+// cu holds, begins and ends are brought into 0 .. L and never fall, so the rows
+// of all segments lie in the tensors and their number is at most L / len + n_seq + 2.
+static __global__ __launch_bounds__(256) void segment_table_kernel(const int* cu, int n_seq, int L, int len, int* used,
+                                                                   int* first_of, int4* table) {
+  __shared__ int ends[256], counts[256];
+  const int tid = threadIdx.x;
+  int end = min(max(cu[0], 0), L);  // of the sequence before
+  int at = (end + len - 1) / len;   // segments so far: the rows in front of the first sequence
+  for (int i = tid; i < at; i += 256) table[i] = make_int4(i * len, min(len, end - i * len), -1, 3);
+  for (int base = 0; base < n_seq; base += 256) {
+    const int i = base + tid;
+    ends[tid] = i < n_seq ? min(max(cu[i + 1], 0), L) : 0;
+    __syncthreads();
+    for (int off = 1; off < 256; off <<= 1) {
+      const int o = tid >= off ? ends[tid - off] : 0;
+      __syncthreads();
+      ends[tid] = max(ends[tid], o);
+      __syncthreads();
+    }
+    const int my_end = max(ends[tid], end), begin = tid ? max(ends[tid - 1], end) : end;
+    const int next_end = max(ends[255], end);
+    const int n = my_end - begin, pieces = i < n_seq ? max(1, (n + len - 1) / len) : 0;
+    counts[tid] = pieces;
+    __syncthreads();
+    for (int off = 1; off < 256; off <<= 1) {
+      const int o = tid >= off ? counts[tid - off] : 0;
+      __syncthreads();
+      counts[tid] += o;
+      __syncthreads();
+    }
+    const int first = at + counts[tid] - pieces;
+    if (i < n_seq) first_of[i] = first;
+    for (int p = 0; p < pieces; ++p)
+      table[first + p] = make_int4(begin + p * len, min(len, n - p * len), i, (p == 0 ? 1 : 0) | (p == pieces - 1 ? 2 : 0));
+    at += counts[255];
+    end = next_end;
+    __syncthreads();
+  }
+  const int behind = (L - end + len - 1) / len;
+  for (int i = tid; i < behind; i += 256) table[at + i] = make_int4(end + i * len, min(len, L - end - i * len), -1, 3);
+  if (tid == 0) {
+    first_of[n_seq] = at;
+    *used = at + behind;
+  }
+}
+
+hipError_t make_plan(const int* cu, int n_seq, int L, const Sizes& s, void* ws, hipStream_t stream, Plan* p) {
+  *p = Plan{nullptr, nullptr, nullptr, s.len, s.per_row, L, (int)s.segments};
+  if (!cu) return hipSuccess;
+  int* ints = static_cast<int*>(ws);
+  int4* table = reinterpret_cast<int4*>(ints + (n_seq + 2 + 3) / 4 * 4);
+  hipLaunchKernelGGL(segment_table_kernel, dim3(1), dim3(256), 0, stream, cu, n_seq, L, s.len, ints, ints + 1, table);
+  p->used = ints;
+  p->first_of = ints + 1;
+  p->table = table;
+  return hipGetLastError();
+}
+
+// ---- states between segments -----------------------------------------------------------
+
+// A thread takes one (sequence, channel, state) in one direction; loads of 8 segments
+// are under way at a time.
+static __global__ __launch_bounds__(256) void combine_kernel(Plan pl, long long items, int DN, int N, const float* A,
+                                                             const float* logs, const float* h0, float* ahead, float* back) {
+  const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (item >= items) return;
+  const int seq = (int)(item / DN), e = (int)(item - (long long)seq * DN), d = e / N;
+  const int D = DN / N;
+  float* const x = blockIdx.y ? back : ahead;
+  int s0, s1;
+  segments_of(pl, seq, s0, s1);
+  const int step = blockIdx.y ? -1 : 1;
+  const int from = blockIdx.y ? s1 : s0, n = s1 - s0;
+  const float a2 = A[e] * kLog2e;
+  float carry = x[(size_t)from * DN + e];
+  if (!blockIdx.y) x[(size_t)from * DN + e] = h0 ? h0[item] : 0.f;
+  for (int i = 1; i <= n; i += 8) {
+    float v[8], g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = from + step * min(i + j, n);
+      const bool need = i + j < n;  // the last one's own part goes nowhere
+      v[j] = need ? x[(size_t)s * DN + e] : 0.f;
+      g[j] = need ? logs[(size_t)s * D + d] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i + j > n) break;
+      x[(size_t)(from + step * (i + j)) * DN + e] = carry;
+      carry = fmaf(exp2_fast(a2 * g[j]), carry, v[j]);
+    }
+  }
+}
+
+hipError_t combine(const Plan& p, int n_seq, int D, int N, const float* A, const float* logs, const float* h0, float* ahead,
+                   float* back, hipStream_t stream) {
+  const long long items = (long long)n_seq * D * N;
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((items + 255) / 256), back ? 2 : 1), dim3(256), 0, stream, p, items,
+                     D * N, N, A, logs, h0, ahead, back);
+  return hipGetLastError();
+}
+
+// ---- the walk ----------------------------------------------------------------------------
+
+// OUT: outputs from the states in front of the segments (`states`, or h0 where no
+// sequence is cut).  Otherwise: each segment's last state and sum of dt.
+template <int NW, typename T, bool GATE, bool OUT>
+__global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int blocks_d, float* states, float* logs) {
+  constexpr int N = 4 * NW;
+  using At = Spot<NW>;
+  __shared__ float2 sx[OUT ? 1 : 2][kTile][kCh];  // dt, dt u
+  __shared__ float sy[OUT ? NW : 1][OUT ? kTile : 1][kCh];
+  const int id = blockIdx.x / blocks_d, ch0 = (blockIdx.x - id * blocks_d) * kCh;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ch = ch0 + lane;
+  Segment g;
+  if (!segment_of(pl, id, g)) return;
+  const At at;
+  const int c = ch0 + at.c;
+  const bool has = c < a.D, on = ch < a.D;
+  T* const y = static_cast<T*>(a.y) + ((size_t)g.batch * a.L + g.row) * a.D + c;
+  if (g.seq < 0) {
+    if (OUT && has)
+      for (int r = at.r; r < g.n; r += At::kRows) put4(y + (size_t)r * a.D, zero4());
+    return;
+  }
+  if (!OUT && g.last) return;  // nothing asks for its last state
+  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
+  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
+  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
+  const T* const Bm = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + g.row * a.Bm.sl + 4 * w;
+  const T* const Cm = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + g.row * a.Cm.sl + 4 * w;
+  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  const f32x4 skip = OUT && has && a.skip ? get4(a.skip + c) : zero4();
+  f32x4 A2 = zero4(), h = zero4();
+  if (on) {
+    A2 = get4(a.A + (size_t)ch * N + 4 * w) * kLog2e;
+    // (With cut sequences h0 is not read here: it may be where hT goes.)
+    const float* from = OUT && logs ? states + (size_t)id * a.D * N : g.first && a.h0 ? a.h0 + (size_t)g.seq * a.D * N : nullptr;
+    if (from) h = get4(from + (size_t)ch * N + 4 * w);
+  }
+  float sum = 0.f;
+
+  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses];
+  const auto fetch = [&](int t0) {
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      const int r = t0 + at.row(p);
+      ru[p] = rd[p] = rz[p] = narrow<T>(zero4());
+      if (has && at.in_tile(p) && r < g.n) {
+        ru[p] = raw4(u + r * a.u.sl);
+        rd[p] = raw4(dt + r * a.dt.sl);
+        if (OUT && GATE) rz[p] = raw4(z + r * a.z.sl);
+      }
+    }
+  };
+  fetch(0);
+  int buf = 0;
+  for (int t0 = 0; t0 < g.n; t0 += kTile) {
+    f32x4 uu[At::kPasses], zz[At::kPasses];
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      if (!at.in_tile(p)) continue;
+      uu[p] = wide(ru[p]);
+      zz[p] = wide(rz[p]);
+      const f32x4 d = softplus4(wide(rd[p]) + bias, a.softplus), x = d * uu[p];
+      f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
+      out[0] = f32x4{d[0], x[0], d[1], x[1]};
+      out[1] = f32x4{d[2], x[2], d[3], x[3]};
+    }
+    fetch(t0 + kTile);
+    __syncthreads();
+    const int n = min(kTile, g.n - t0);
+    float part = 0.f;
+    const auto step = [&](int t) {
+      const f32x4 b = uniform4(Bm + (t0 + t) * a.Bm.sl);
+      const float2 x = sx[buf][t][lane];
+      if (OUT) {
+        const f32x4 cc = uniform4(Cm + (t0 + t) * a.Cm.sl);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[i] = fmaf(exp2_fast(x.x * A2[i]), h[i], x.y * b[i]);
+          s = fmaf(h[i], cc[i], s);
+        }
+        sy[w][t][lane] = s;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_fast(x.x * A2[i]), h[i], x.y * b[i]);
+        part += x.x;
+      }
+    };
+    if (n == kTile) {
+#pragma unroll
+      for (int t = 0; t < kTile; ++t) step(t);
+    } else {
+      for (int t = 0; t < n; ++t) step(t);
+    }
+    sum += part;
+    if (OUT) {
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < At::kPasses; ++p) {
+        if (!at.in_tile(p)) continue;
+        const int r = at.row(p);
+        f32x4 s = skip * uu[p];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) s += get4(&sy[i][r][at.c]);
+        if (GATE) s *= zz[p] * sigmoid4(zz[p]);
+        if (has && r < n) put4(y + (size_t)(t0 + r) * a.D, s);
+      }
+    } else {
+      buf ^= 1;
+    }
+  }
+  if (!on) return;
+  float* to = nullptr;
+  if (OUT) {
+    if (g.last && a.hT) to = a.hT + (size_t)g.seq * a.D * N;
+  } else {
+    to = states + (size_t)id * a.D * N;
+    if (w == 0) logs[(size_t)id * a.D + ch] = sum;
+  }
+  if (to) *reinterpret_cast<f32x4*>(to + (size_t)ch * N + 4 * w) = h;
+}
+
+static Sizes forward_sizes(int B, int L, int D, bool packed, int n_seq) {
+  return sizes_of(packed, B, L, n_seq, D, 512, 1024, 64);
+}
+
+template <int NW, typename T, bool GATE>
+static hipError_t forward(const ScanArgs& a) {
+  const Sizes s = forward_sizes(a.B, a.L, a.D, a.cu, a.n_seq);
+  const int blocks_d = (int)channel_blocks(a.D);
+  char* ws = static_cast<char*>(a.workspace);
+  Plan p;
+  prof_mark(kSlotSelectiveScan, false, a.stream);
+  hipError_t e = make_plan(a.cu, a.n_seq, a.L, s, ws, a.stream, &p);
+  ws += table_bytes(a.cu, a.n_seq, s);
+  float* states = reinterpret_cast<float*>(ws);
+  float* logs = s.split ? states + (size_t)s.segments * a.D * a.N : nullptr;
+  const dim3 grid((unsigned)(s.segments * blocks_d));
+  if (e == hipSuccess && s.split) {
+    hipLaunchKernelGGL((walk_kernel<NW, T, GATE, false>), grid, dim3(64 * NW), 0, a.stream, a, p, blocks_d, states, logs);
+    e = hipGetLastError();
+    if (e == hipSuccess) e = combine(p, a.n_seq, a.D, a.N, a.A, logs, a.h0, states, nullptr, a.stream);
+  }
+  if (e == hipSuccess) {
+    hipLaunchKernelGGL((walk_kernel<NW, T, GATE, true>), grid, dim3(64 * NW), 0, a.stream, a, p, blocks_d, states, logs);
+    e = hipGetLastError();
+  }
+  prof_mark(kSlotSelectiveScan, true, a.stream);
+  return e;
+}
+
+template <int NW>
+static hipError_t forward_t(const ScanArgs& a) {
+  if (a.dtype == 1) return a.z.p ? forward<NW, bf16, true>(a) : forward<NW, bf16, false>(a);
+  return a.z.p ? forward<NW, float, true>(a) : forward<NW, float, false>(a);
+}
+
+// ---- one token ---------------------------------------------------------------------------
+
+// Bound by HBM: the state is read and written once.  A lane takes 4 states of a
+// channel; N / 4 adjacent lanes add up their channel's y.
+template <int N, typename T>
+__global__ __launch_bounds__(256) void step_kernel(ScanArgs a, long long items) {
+  constexpr int Q = N / 4;
+  const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (item >= items) return;  // (whole channels: D is a multiple of 8)
+  const int q = (int)(item % Q);
+  const long long bd = item / Q;
+  const int b = (int)(bd / a.D), d = (int)(bd - (long long)b * a.D);
+  float* const hp = a.hT + item * 4;
+  f32x4 h = get4(hp);
+  const f32x4 A2 = get4(a.A + (size_t)d * N + 4 * q) * kLog2e;
+  const f32x4 Bq = wide(raw4(static_cast<const T*>(a.Bm.p) + b * a.Bm.sb + 4 * q));
+  const f32x4 Cq = wide(raw4(static_cast<const T*>(a.Cm.p) + b * a.Cm.sb + 4 * q));
+  const float u = to_f32(static_cast<const T*>(a.u.p)[b * a.u.sb + d]);
+  float dt = to_f32(static_cast<const T*>(a.dt.p)[b * a.dt.sb + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
+  if (a.softplus) dt = softplus(dt);
+  const float x = dt * u;
+  float y = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], x * Bq[i]);
+    y = fmaf(h[i], Cq[i], y);
+  }
+  __builtin_nontemporal_store(h, reinterpret_cast<f32x4*>(hp));
+#pragma unroll
+  for (int off = Q / 2; off > 0; off >>= 1) y += __shfl_xor(y, off, 64);
+  if (q == 0) {
+    if (a.skip) y = fmaf(a.skip[d], u, y);
+    if (a.z.p) {
+      const float z = to_f32(static_cast<const T*>(a.z.p)[b * a.z.sb + d]);
+      y *= z * sigmoid(z);
+    }
+    static_cast<T*>(a.y)[bd] = from_f32<T>(y);
+  }
+}
+
+template <int N, typename T>
+static hipError_t step(const ScanArgs& a) {
+  const long long items = (long long)a.B * a.D * (N / 4);
+  prof_mark(kSlotSelectiveStep, false, a.stream);
+  hipLaunchKernelGGL((step_kernel<N, T>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0, a.stream, a, items);
+  const hipError_t e = hipGetLastError();
+  prof_mark(kSlotSelectiveStep, true, a.stream);
+  return e;
+}
+
+}  // namespace ssm
+
+// Whether the launches hold these sizes.
+bool selective_scan_fits(int B, int L, int D, int N, bool packed, int n_seq, bool backward) {
+  const long long D64 = ssm::channel_blocks(D), states = (long long)D * N;
+  if (L > 0x7fffffff - 64 || states > 0x7fffffff || (packed && n_seq > (1 << 24))) return false;
+  const ssm::Sizes s = backward ? ssm::backward_sizes(B, L, D, packed, n_seq) : ssm::forward_sizes(B, L, D, packed, n_seq);
+  if (s.segments > max_blocks(16 * N) / D64 || (long long)n_seq > max_blocks(256) * 256 / states) return false;
+  return !backward || (long long)B * L <= max_blocks(256) * 1024 / N;
+}
+
+size_t selective_scan_workspace_bytes(int B, int L, int D, int N, bool packed, int n_seq) {
+  const ssm::Sizes s = ssm::forward_sizes(B, L, D, packed, n_seq);
+  const size_t table = ssm::table_bytes(packed, n_seq, s);
+  return s.split ? table + (size_t)s.segments * D * (N + 1) * sizeof(float) : table;
+}
+
+hipError_t launch_selective_scan(const ScanArgs& a) {
+  return a.N == 8 ? ssm::forward_t<2>(a) : a.N == 16 ? ssm::forward_t<4>(a) : ssm::forward_t<8>(a);
+}
+
+hipError_t launch_selective_scan_step(const ScanArgs& a) {
+  if (a.dtype == 1) return a.N == 8 ? ssm::step<8, bf16>(a) : a.N == 16 ? ssm::step<16, bf16>(a) : ssm::step<32, bf16>(a);
+  return a.N == 8 ? ssm::step<8, float>(a) : a.N == 16 ? ssm::step<16, float>(a) : ssm::step<32, float>(a);
+}
+
+}  // namespace dn

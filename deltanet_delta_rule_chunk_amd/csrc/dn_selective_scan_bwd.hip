@@ -1,0 +1,511 @@
+// dn_selective_scan_bwd.hip -- gradient of the selective state space scan on
+// gfx950 (the recurrence, segments and a workgroup's tile: dn_selective_scan.h).
+//
+// With g_t = dy_t silu(z_t) and G_t the gradient of h_t,
+//     G_t = C_t g_t + e^{dt_{t+1} A} G_{t+1}
+//     dC_t = sum_d h_t g_t           dB_t = sum_d G_t dt_t u_t
+//     d(dt u)_t = sum_n G_t B_t      thr_t = G_t e^{dt_t A} h_{t-1}
+//     ddt_t = u_t d(dt u)_t + sum_n thr_t A,   dA = sum_t thr_t dt_t
+//     du_t = dt_t d(dt u)_t + D g_t,           dz_t = dy_t (C_t h_t + D u_t) silu'(z_t).
+//
+// A walk forward leaves the state in front of every tile of 16 tokens; the walk
+// back takes the tiles from the last to the first: 16 steps forward from the
+// tile's state, decays and decayed states kept in registers, then 16 back.
+// Where sequences are cut into segments, the first launch walks every segment
+// from zero in both directions, combine() joins them, and a tile's state is what
+// the segment makes of it plus the segment's entering state times e^{A sum dt}.
+//
+// Sums over channels (dB, dC) are sums over lanes: 4 values of a token become one
+// register per lane by two exchanges of half a wave, 16 tokens' registers become
+// one by four more within rows of 16 lanes, so that each of the 64 lanes ends with
+// the sum of one (token, state) of the tile: 2.2 vector operations per value.
+// Every block of 64 channels leaves its part, added up in fixed order at the end,
+// as are the segments' parts of dA, dD and the bias's gradient.
+
+#include "dn_selective_scan.h"
+
+namespace dn {
+namespace ssm {
+
+struct BwdSpace {
+  float* tiles;   // [tile][D][N] state in front of a tile (cut sequences: from the segment's zero)
+  float* before;  // cut sequences: [tile][D] sum of dt from the segment's first token to the tile
+  float* ahead;   // cut sequences: [seg][D][N] states in front of segments
+  float* back;    // cut sequences: [seg][D][N] gradients of the states behind segments
+  float* logs;    // cut sequences: [seg][D] sum of dt
+  float* dBC;     // [2][block of channels][B L][N]
+  float* dA;      // [seg][D][N]
+  float* dvec;    // [seg][2][D]: D's and the bias's gradients
+};
+
+// ---- states in front of tiles; what segments make from zero in both directions ----------------
+
+// blockIdx.y = 0: forward.  1 (cut sequences only): backward.
+template <int NW, typename T, bool GATE, bool SPLIT>
+__global__ __launch_bounds__(64 * NW) void sums_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
+  constexpr int N = 4 * NW;
+  using At = Spot<NW>;
+  __shared__ float2 sx[2][kTile][kCh];  // dt, and dt u or g
+  const int id = blockIdx.x / blocks_d, ch0 = (blockIdx.x - id * blocks_d) * kCh;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ch = ch0 + lane;
+  Segment g;
+  if (!segment_of(pl, id, g) || g.seq < 0) return;
+  const bool back = SPLIT && blockIdx.y;
+  if (back && g.first) return;  // nothing asks for what arrives at its front
+  const At at;
+  const int c = ch0 + at.c;
+  const bool has = c < a.D, on = ch < a.D;
+  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
+  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
+  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
+  const T* const dy = static_cast<const T*>(a.dy) + ((size_t)g.batch * a.L + g.row) * a.D + c;
+  const TokenRows& m = back ? a.Cm : a.Bm;
+  const T* const M = static_cast<const T*>(m.p) + g.batch * m.sb + g.row * m.sl + 4 * w;
+  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  f32x4 A2 = zero4(), h = zero4();
+  const size_t place = (size_t)ch * N + 4 * w, state = (size_t)a.D * N;
+  if (on) {
+    A2 = get4(a.A + place) * kLog2e;
+    if (back ? g.last && a.dhT : g.first && a.h0) h = get4((back ? a.dhT : a.h0) + (size_t)g.seq * state + place);
+  }
+  const long long tile0 = first_tile(pl, g, id);
+  const int tiles = (g.n + kTile - 1) / kTile;
+  float sum = 0.f;
+
+  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses];
+  const auto fetch = [&](int tile) {
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      const int r = tile * kTile + at.row(p);
+      ru[p] = rd[p] = rz[p] = narrow<T>(zero4());
+      if (has && at.in_tile(p) && tile >= 0 && r < g.n) {
+        rd[p] = raw4(dt + r * a.dt.sl);
+        ru[p] = back ? raw4(dy + (size_t)r * a.D) : raw4(u + r * a.u.sl);
+        if (GATE && back) rz[p] = raw4(z + r * a.z.sl);
+      }
+    }
+  };
+  const int step = back ? -1 : 1;
+  int tile = back ? tiles - 1 : 0, buf = 0;
+  fetch(tile);
+  for (int i = 0; i < tiles; ++i, tile += step, buf ^= 1) {
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      if (!at.in_tile(p)) continue;
+      const f32x4 d = softplus4(wide(rd[p]) + bias, a.softplus);
+      f32x4 x = wide(ru[p]);
+      if (!back) x *= d;
+      if (GATE && back) {
+        const f32x4 zz = wide(rz[p]);
+        x *= zz * sigmoid4(zz);
+      }
+      f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
+      out[0] = f32x4{d[0], x[0], d[1], x[1]};
+      out[1] = f32x4{d[2], x[2], d[3], x[3]};
+    }
+    fetch(i + 1 < tiles ? tile + step : -1);
+    __syncthreads();
+    const int n = min(kTile, g.n - tile * kTile);
+    if (!back) {
+      if (on) {
+        *reinterpret_cast<f32x4*>(ws.tiles + (size_t)(tile0 + tile) * state + place) = h;
+        if (SPLIT && w == 0) ws.before[(size_t)(tile0 + tile) * a.D + ch] = sum;
+      }
+      float part = 0.f;
+      const auto one = [&](int t) {
+        const f32x4 b = uniform4(M + (tile * kTile + t) * m.sl);
+        const float2 x = sx[buf][t][lane];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[s] = fmaf(exp2_fast(x.x * A2[s]), h[s], x.y * b[s]);
+        part += x.x;
+      };
+      if (n == kTile) {
+#pragma unroll
+        for (int t = 0; t < kTile; ++t) one(t);
+      } else {
+        for (int t = 0; t < n; ++t) one(t);
+      }
+      sum += part;
+    } else {
+      const auto one = [&](int t) {
+        const f32x4 cc = uniform4(M + (tile * kTile + t) * m.sl);
+        const float2 x = sx[buf][t][lane];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[s] = exp2_fast(x.x * A2[s]) * fmaf(cc[s], x.y, h[s]);
+      };
+      if (n == kTile) {
+#pragma unroll
+        for (int t = kTile - 1; t >= 0; --t) one(t);
+      } else {
+        for (int t = n - 1; t >= 0; --t) one(t);
+      }
+    }
+  }
+  if (SPLIT && on) {
+    *reinterpret_cast<f32x4*>((back ? ws.back : ws.ahead) + (size_t)id * state + place) = h;
+    if (!back && w == 0) ws.logs[(size_t)id * a.D + ch] = sum;
+  }
+}
+
+// ---- sums over lanes ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float swap32_add(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap16_add(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Four values per lane: row r of 16 lanes gets sums over the four rows of v[r].
+__device__ __forceinline__ float rows_sum(f32x4 v) { return swap16_add(swap32_add(v[0], v[2]), swap32_add(v[1], v[3])); }
+// Lanes whose `bit` is set get a sum of b over themselves and a partner, the others of a.
+template <int CTRL>
+__device__ __forceinline__ float fold(float a, float b, bool bit) {
+  const float keep = bit ? b : a, send = bit ? a : b;
+  return keep + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(send), CTRL, 0xf, 0xf, true));
+}
+// 16 values per lane: lane i of 16 gets the sum of v[i] over the 16.
+__device__ __forceinline__ float lanes_sum(float (&v)[16], int lane) {
+  constexpr int kMirror16 = 0x140, kMirror8 = 0x141, kMirror4 = 0x1b, kMirror2 = 0xb1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fold<kMirror16>(v[i], v[i + 8], lane & 8);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = fold<kMirror8>(v[i], v[i + 4], lane & 4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) v[i] = fold<kMirror4>(v[i], v[i + 2], lane & 2);
+  return fold<kMirror2>(v[0], v[1], lane & 1);
+}
+
+// ---- the walk back -------------------------------------------------------------------------------
+
+template <int NW, typename T, bool GATE, bool SPLIT>
+__global__ __launch_bounds__(64 * NW) void back_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
+  constexpr int N = 4 * NW;
+  using At = Spot<NW>;
+  __shared__ float2 sx[kTile][kCh];                    // dt, dt u
+  __shared__ float sg[kTile][kCh];                     // g
+  __shared__ float sdx[NW][kTile][kCh];                // the waves' parts of d(dt u),
+  __shared__ float sda[NW][kTile][kCh];                // of sum_n thr A (times log2 e),
+  __shared__ float sy[GATE ? NW : 1][GATE ? kTile : 1][kCh];  // of C h
+  const int id = blockIdx.x / blocks_d, block = blockIdx.x - id * blocks_d, ch0 = block * kCh;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ch = ch0 + lane;
+  Segment g;
+  if (!segment_of(pl, id, g)) return;
+  const At at;
+  const int c = ch0 + at.c;
+  const bool has = c < a.D, on = ch < a.D;
+  const size_t token = (size_t)g.batch * a.L + g.row;  // of the segment's first row
+  T* const du = static_cast<T*>(a.du) + token * a.D + c;
+  T* const ddt = static_cast<T*>(a.ddt) + token * a.D + c;
+  T* const dz = GATE ? static_cast<T*>(a.dz) + token * a.D + c : nullptr;
+  const size_t tokens = (size_t)a.B * a.L;
+  float* const dB = ws.dBC + ((size_t)block * tokens + token) * N;
+  float* const dC = dB + (size_t)blocks_d * tokens * N;
+  const size_t place = (size_t)ch * N + 4 * w, state = (size_t)a.D * N;
+  float* const dA_to = ws.dA + (size_t)id * state + place;
+  float* const dvec = ws.dvec + (size_t)id * 2 * a.D;
+  if (g.seq < 0) {
+    for (int r = at.r; r < g.n; r += At::kRows) {
+      if (!has) break;
+      put4(du + (size_t)r * a.D, zero4());
+      put4(ddt + (size_t)r * a.D, zero4());
+      if (GATE) put4(dz + (size_t)r * a.D, zero4());
+    }
+    for (int i = threadIdx.x; i < g.n * N; i += 64 * NW) dB[i] = dC[i] = 0.f;
+    if (on) *reinterpret_cast<f32x4*>(dA_to) = zero4();
+    if (on && w == 0) dvec[ch] = dvec[a.D + ch] = 0.f;
+    return;
+  }
+  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
+  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
+  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
+  const T* const dy = static_cast<const T*>(a.dy) + token * a.D + c;
+  const T* const Bm = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + g.row * a.Bm.sl + 4 * w;
+  const T* const Cm = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + g.row * a.Cm.sl + 4 * w;
+  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  const f32x4 skip = has && a.skip ? get4(a.skip + c) : zero4();
+  f32x4 A2 = zero4(), G = zero4(), enter = zero4();
+  if (on) {
+    A2 = get4(a.A + place) * kLog2e;
+    if (SPLIT && !g.first) enter = get4(ws.ahead + (size_t)id * state + place);
+    if (SPLIT && !g.last) G = get4(ws.back + (size_t)id * state + place);
+    if (g.last && a.dhT) G = get4(a.dhT + (size_t)g.seq * state + place);
+  }
+  const long long tile0 = first_tile(pl, g, id);
+  const int tiles = (g.n + kTile - 1) / kTile;
+  f32x4 dA = zero4(), dskip = zero4(), dbias = zero4();
+
+  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses], ry[At::kPasses];
+  f32x4 held = zero4();
+  float since = 0.f;
+  const auto fetch = [&](int tile) {
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      const int r = tile * kTile + at.row(p);
+      ru[p] = rd[p] = rz[p] = ry[p] = narrow<T>(zero4());
+      if (has && at.in_tile(p) && tile >= 0 && r < g.n) {
+        ru[p] = raw4(u + r * a.u.sl);
+        rd[p] = raw4(dt + r * a.dt.sl);
+        ry[p] = raw4(dy + (size_t)r * a.D);
+        if (GATE) rz[p] = raw4(z + r * a.z.sl);
+      }
+    }
+    if (on && tile >= 0) {
+      held = get4(ws.tiles + (size_t)(tile0 + tile) * state + place);
+      if (SPLIT && !g.first) since = ws.before[(size_t)(tile0 + tile) * a.D + ch];
+    }
+  };
+  fetch(tiles - 1);
+  for (int tile = tiles - 1; tile >= 0; --tile) {
+    const int n = min(kTile, g.n - tile * kTile);
+    f32x4 uu[At::kPasses], dd[At::kPasses], slope[At::kPasses], zz[At::kPasses], yy[At::kPasses], gg[At::kPasses];
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      if (!at.in_tile(p)) continue;
+      const int r = at.row(p);
+      uu[p] = wide(ru[p]);
+      zz[p] = wide(rz[p]);
+      yy[p] = wide(ry[p]);
+      const f32x4 raw = wide(rd[p]) + bias;
+      dd[p] = r < n ? softplus4(raw, a.softplus) : zero4();  // rows behind the segment change nothing
+      slope[p] = a.softplus ? sigmoid4(raw) : f32x4{1.f, 1.f, 1.f, 1.f};
+      const f32x4 x = dd[p] * uu[p];
+      gg[p] = yy[p];
+      if (GATE) gg[p] *= zz[p] * sigmoid4(zz[p]);
+      f32x4* const out = reinterpret_cast<f32x4*>(&sx[r][at.c]);
+      out[0] = f32x4{dd[p][0], x[0], dd[p][1], x[1]};
+      out[1] = f32x4{dd[p][2], x[2], dd[p][3], x[3]};
+      *reinterpret_cast<f32x4*>(&sg[r][at.c]) = gg[p];
+    }
+    f32x4 h = held;
+    if (SPLIT && !g.first) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) h[s] = fmaf(exp2_fast(since * A2[s]), enter[s], h[s]);
+    }
+    fetch(tile - 1);
+    __syncthreads();
+    // Rows behind the segment: their B and C are taken as 0.
+    const auto rows4 = [&](const T* m, long long stride, int t) {
+      const f32x4 v = uniform4(m + (tile * kTile + min(t, n - 1)) * stride);
+      return t < n ? v : zero4();
+    };
+    float decay[kTile][4], kept[kTile][4];
+#pragma unroll
+    for (int t = 0; t < kTile; ++t) {
+      const f32x4 b = rows4(Bm, a.Bm.sl, t);
+      const float2 x = sx[t][lane];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        decay[t][s] = exp2_fast(x.x * A2[s]);
+        kept[t][s] = decay[t][s] * h[s];
+        h[s] = fmaf(x.y, b[s], kept[t][s]);
+      }
+    }
+    float lB[kTile], lC[kTile];
+    f32x4 dAt = zero4();
+#pragma unroll
+    for (int t = kTile - 1; t >= 0; --t) {
+      const f32x4 b = rows4(Bm, a.Bm.sl, t), cc = rows4(Cm, a.Cm.sl, t);
+      const float2 x = sx[t][lane];
+      const float gy = sg[t][lane];
+      f32x4 vB, vC;
+      float px = 0.f, pa = 0.f, py = 0.f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float ht = fmaf(x.y, b[s], kept[t][s]);
+        G[s] = fmaf(cc[s], gy, G[s]);
+        vC[s] = ht * gy;
+        vB[s] = G[s] * x.y;
+        px = fmaf(G[s], b[s], px);
+        if (GATE) py = fmaf(ht, cc[s], py);
+        const float thr = G[s] * kept[t][s];
+        pa = fmaf(thr, A2[s], pa);
+        dAt[s] = fmaf(thr, x.x, dAt[s]);
+        G[s] *= decay[t][s];
+      }
+      lB[t] = rows_sum(vB);
+      lC[t] = rows_sum(vC);
+      sdx[w][t][lane] = px;
+      sda[w][t][lane] = pa;
+      if (GATE) sy[w][t][lane] = py;
+    }
+    dA += dAt;
+    const float tB = lanes_sum(lB, lane), tC = lanes_sum(lC, lane);
+    if ((lane & 15) < n) {
+      const size_t o = (size_t)(tile * kTile + (lane & 15)) * N + 4 * w + (lane >> 4);
+      dB[o] = tB;
+      dC[o] = tC;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < At::kPasses; ++p) {
+      if (!at.in_tile(p)) continue;
+      const int r = at.row(p);
+      f32x4 dx = zero4(), da = zero4(), yv = skip * uu[p];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        dx += get4(&sdx[i][r][at.c]);
+        da += get4(&sda[i][r][at.c]);
+        if (GATE) yv += get4(&sy[i][r][at.c]);
+      }
+      if (!has || r >= n) continue;
+      const size_t o = (size_t)(tile * kTile + r) * a.D;
+      const f32x4 draw = (da * kLn2 + dx * uu[p]) * slope[p];
+      put4(du + o, dx * dd[p] + skip * gg[p]);
+      put4(ddt + o, draw);
+      dskip += gg[p] * uu[p];
+      dbias += draw;
+      if (GATE) {
+        const f32x4 sig = sigmoid4(zz[p]);
+        put4(dz + o, yy[p] * yv * (sig + zz[p] * sig * (1.f - sig)));
+      }
+    }
+  }
+  if (on) {
+    *reinterpret_cast<f32x4*>(dA_to) = dA;
+    if (g.first && a.dh0) *reinterpret_cast<f32x4*>(a.dh0 + (size_t)g.seq * state + place) = G;
+  }
+  // The rows' parts of D's and the bias's gradients, through the waves' parts' place.
+  constexpr int kSum = At::kRows < kTile ? At::kRows : kTile;
+  __syncthreads();
+  if (at.r < kSum) {
+    *reinterpret_cast<f32x4*>(&sg[at.r][at.c]) = dskip;
+    *reinterpret_cast<f32x4*>(&sdx[0][at.r][at.c]) = dbias;
+  }
+  __syncthreads();
+  if (on && w == 0) {
+    float s0 = 0.f, s1 = 0.f;
+    for (int r = 0; r < kSum; ++r) s0 += sg[r][lane], s1 += sdx[0][r][lane];
+    dvec[ch] = s0;
+    dvec[a.D + ch] = s1;
+  }
+}
+
+// ---- adding up parts -------------------------------------------------------------------------------
+
+// blockIdx.y = 0, 1: dB, dC over the blocks of channels, 4 values per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void channels_kernel(const float* parts, long long values, int blocks_d, T* dB, T* dC) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= values) return;
+  const float* p = parts + (blockIdx.y ? values * blocks_d : 0) + i;
+  f32x4 s = zero4();
+#pragma unroll 8
+  for (int k = 0; k < blocks_d; ++k) s += get4(p + (size_t)k * values);
+  put4((blockIdx.y ? dC : dB) + i, s);
+}
+
+// dA, then D's and the bias's gradients, over the segments: 16 columns of
+// `dA` [seg][state] and `dvec` [seg][2 D] per workgroup.
+static __global__ __launch_bounds__(256) void segments_kernel(const int* used, int segments, int state, int D, const float* dA,
+                                                              const float* dvec, float* out_A, float* out_skip, float* out_bias) {
+  __shared__ double red[16][17];
+  const int n = used ? *used : segments;
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  int e = blockIdx.x * 16 + c;
+  const bool vec = e >= state;  // (both are multiples of 16)
+  const float* p = vec ? dvec : dA;
+  const size_t stride = vec ? 2 * (size_t)D : state;
+  if (vec) e -= state;
+  double s = 0.0;
+#pragma unroll 8
+  for (int i = r; i < n; i += 16) s += (double)p[(size_t)i * stride + e];
+  red[r][c] = s;
+  __syncthreads();
+  if (r) return;
+  for (int i = 1; i < 16; ++i) s += red[i][c];
+  float* const to = !vec ? out_A + e : e < D ? (out_skip ? out_skip + e : nullptr) : (out_bias ? out_bias + e - D : nullptr);
+  if (to) *to = (float)s;
+}
+
+// ---- launches --------------------------------------------------------------------------------------
+
+Sizes backward_sizes(int B, int L, int D, bool packed, int n_seq) {
+  return sizes_of(packed, B, L, n_seq, D, 512, 1024, 64);
+}
+static size_t up(size_t n) { return (n + 3) / 4 * 4; }  // floats, to 16 bytes
+
+// Places the parts in a workspace; returns its size in bytes (ws may be null).
+static size_t place(int B, int L, int D, int N, bool packed, int n_seq, const Sizes& s, void* ws, BwdSpace* out) {
+  const size_t table = table_bytes(packed, n_seq, s), state = (size_t)D * N, tokens = (size_t)B * L;
+  const size_t tiles = tokens / kTile + s.segments + 1, seg = s.segments;
+  float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + table);
+  size_t at = 0;
+  const auto take = [&](size_t n) {
+    float* r = p + at;
+    at += up(n);
+    return r;
+  };
+  out->tiles = take(tiles * state);
+  out->before = take(s.split ? tiles * D : 0);
+  out->ahead = take(s.split ? seg * state : 0);
+  out->back = take(s.split ? seg * state : 0);
+  out->logs = take(s.split ? seg * D : 0);
+  out->dBC = take(2 * (size_t)channel_blocks(D) * tokens * N);
+  out->dA = take(seg * state);
+  out->dvec = take(seg * 2 * D);
+  return table + at * sizeof(float);
+}
+
+template <int NW, typename T, bool GATE>
+static hipError_t backward(const ScanArgs& a) {
+  const Sizes s = backward_sizes(a.B, a.L, a.D, a.cu, a.n_seq);
+  const int blocks_d = (int)channel_blocks(a.D);
+  BwdSpace ws;
+  place(a.B, a.L, a.D, a.N, a.cu, a.n_seq, s, a.workspace, &ws);
+  Plan p;
+  prof_mark(kSlotSelectiveScanBwd, false, a.stream);
+  hipError_t e = make_plan(a.cu, a.n_seq, a.L, s, a.workspace, a.stream, &p);
+  const dim3 grid((unsigned)(s.segments * blocks_d)), block(64 * NW);
+  if (e == hipSuccess) {
+    if (s.split) {
+      hipLaunchKernelGGL((sums_kernel<NW, T, GATE, true>), dim3(grid.x, 2), block, 0, a.stream, a, p, blocks_d, ws);
+      e = hipGetLastError();
+      if (e == hipSuccess) e = combine(p, a.n_seq, a.D, a.N, a.A, ws.logs, a.h0, ws.ahead, ws.back, a.stream);
+      if (e == hipSuccess) {
+        hipLaunchKernelGGL((back_kernel<NW, T, GATE, true>), grid, block, 0, a.stream, a, p, blocks_d, ws);
+        e = hipGetLastError();
+      }
+    } else {
+      hipLaunchKernelGGL((sums_kernel<NW, T, GATE, false>), grid, block, 0, a.stream, a, p, blocks_d, ws);
+      e = hipGetLastError();
+      if (e == hipSuccess) {
+        hipLaunchKernelGGL((back_kernel<NW, T, GATE, false>), grid, block, 0, a.stream, a, p, blocks_d, ws);
+        e = hipGetLastError();
+      }
+    }
+  }
+  const long long values = (long long)a.B * a.L * a.N;
+  if (e == hipSuccess && values > 0) {
+    hipLaunchKernelGGL(channels_kernel<T>, dim3((unsigned)((values / 4 + 255) / 256), 2), dim3(256), 0, a.stream, ws.dBC,
+                       values, blocks_d, static_cast<T*>(a.dB), static_cast<T*>(a.dC));
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess) {
+    hipLaunchKernelGGL(segments_kernel, dim3((unsigned)((a.D * a.N + 2 * a.D) / 16)), dim3(256), 0, a.stream, p.used,
+                       (int)s.segments, a.D * a.N, a.D, ws.dA, ws.dvec, a.dA, a.dskip, a.dbias);
+    e = hipGetLastError();
+  }
+  prof_mark(kSlotSelectiveScanBwd, true, a.stream);
+  return e;
+}
+
+template <int NW>
+static hipError_t backward_t(const ScanArgs& a) {
+  if (a.dtype == 1) return a.z.p ? backward<NW, bf16, true>(a) : backward<NW, bf16, false>(a);
+  return a.z.p ? backward<NW, float, true>(a) : backward<NW, float, false>(a);
+}
+
+}  // namespace ssm
+
+size_t selective_scan_bwd_workspace_bytes(int B, int L, int D, int N, bool packed, int n_seq) {
+  ssm::BwdSpace ws;
+  return ssm::place(B, L, D, N, packed, n_seq, ssm::backward_sizes(B, L, D, packed, n_seq), nullptr, &ws);
+}
+
+hipError_t launch_selective_scan_bwd(const ScanArgs& a) {
+  return a.N == 8 ? ssm::backward_t<2>(a) : a.N == 16 ? ssm::backward_t<4>(a) : ssm::backward_t<8>(a);
+}
+
+}  // namespace dn

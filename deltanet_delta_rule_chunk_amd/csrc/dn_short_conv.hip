@@ -1,0 +1,483 @@
+// dn_short_conv.hip -- short causal convolution of every channel on gfx950, its
+// gradient, and one token with the kept rows updated in place.
+//
+// With x_e the K - 1 rows kept from before a sequence followed by its rows,
+//     p_t = b + sum_j w[j] x_e[t + j],  y_t = silu(p_t) (or p_t),  j = 0 .. K - 1,
+// and the rows kept behind it are x_e's last K - 1.  With q_t = dy_t silu'(p_t),
+//     dx_e[i] = sum_j w[j] q_{i - j} (+ the kept rows' gradient),
+//     dw[j] = sum_t q_t x_e[t + j],   db = sum_t q_t.
+//
+// Bound by HBM: x is read and y written once.  A thread walks down a run of
+// rows of its channels with the last K - 1 of them in registers; neighbouring
+// threads hold neighbouring channels, so every load is a whole piece of a row.
+// Where packed sequences meet inside a run, the registers take the new sequence's
+// kept rows.  Rows that no sequence holds give zeros.
+
+#include "dn_launch.h"
+#include "dn_vec.h"
+
+namespace dn {
+namespace conv {
+
+constexpr int NT = 256;
+
+// The sequence that holds a row, followed from row to row.
+struct Cursor {
+  const int* cu;  // null: every batch row is a sequence
+  int n, L, batch;
+  int seq, begin, end;  // seq < 0 or >= n: rows between begin and end are in none
+
+  __device__ __forceinline__ Cursor(const int* cu, int n, int L, int batch, int row) : cu(cu), n(n), L(L), batch(batch) {
+    seq = batch;
+    begin = 0;
+    end = L;
+    if (cu) find(row);
+  }
+  __device__ __forceinline__ void find(int row) {
+    int lo = -1, hi = n;  // cu[lo] <= row < cu[hi], with cu[-1] = 0 and nothing at n + 1
+    if (row >= cu[n]) {
+      lo = n;
+    } else {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= row) lo = mid; else hi = mid;
+      }
+    }
+    seq = lo;
+    begin = lo < 0 ? 0 : cu[lo];
+    end = lo < n ? cu[lo + 1] : L;
+    // Whatever cu holds, the row is between the two.
+    begin = min(max(begin, 0), row);
+    end = min(max(end, row + 1), L);
+  }
+  __device__ __forceinline__ bool inside() const { return !cu || (seq >= 0 && seq < n); }
+};
+
+template <int V> struct Vals { f32x4 v[V / 4]; };
+template <int V>
+__device__ __forceinline__ Vals<V> zeros() {
+  Vals<V> r;
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) r.v[i] = zero4();
+  return r;
+}
+template <int V, typename T>
+struct Raws { Raw4<T> v[V / 4]; };
+template <int V, typename T>
+__device__ __forceinline__ Raws<V, T> load(const T* p) {
+  Raws<V, T> r;
+  __builtin_memcpy(&r, __builtin_assume_aligned(p, V * sizeof(T)), sizeof(r));
+  return r;
+}
+template <int V, typename T>
+__device__ __forceinline__ Raws<V, T> none() {
+  Raws<V, T> r;
+  __builtin_memset(&r, 0, sizeof(r));
+  return r;
+}
+template <int V, typename T>
+__device__ __forceinline__ void store(T* p, const Raws<V, T>& r) {
+  __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &r, sizeof(r));
+}
+template <int V, typename T>
+__device__ __forceinline__ Vals<V> widen(const Raws<V, T>& r) {
+  Vals<V> x;
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) x.v[i] = wide(r.v[i]);
+  return x;
+}
+template <int V, typename T>
+__device__ __forceinline__ Raws<V, T> narrowed(const Vals<V>& x) {
+  Raws<V, T> r;
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) r.v[i] = narrow<T>(x.v[i]);
+  return r;
+}
+
+// Weights of V channels, tap by tap.
+template <int V, int K>
+struct Taps {
+  Vals<V> w[K], b;
+  __device__ __forceinline__ Taps(const float* weight, const float* bias, int c) {
+    float t[V * K];
+    __builtin_memcpy(t, __builtin_assume_aligned(weight + (size_t)c * K, 16), sizeof(t));
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[j].v[i / 4][i % 4] = t[i * K + j];
+    b = zeros<V>();
+    if (bias)
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) b.v[i] = *reinterpret_cast<const f32x4*>(bias + c + 4 * i);
+  }
+};
+template <int V>
+__device__ __forceinline__ void add_product(Vals<V>& a, const Vals<V>& x, const Vals<V>& y) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) a.v[i] += x.v[i] * y.v[i];
+}
+// The tap sums in front of the activation; past[K - 2] is the row before.
+template <int V, int K>
+__device__ __forceinline__ Vals<V> pre(const Taps<V, K>& t, const Vals<V> (&past)[K - 1], const Vals<V>& x) {
+  Vals<V> p = t.b;
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) add_product(p, t.w[j], past[j]);
+  add_product(p, t.w[K - 1], x);
+  return p;
+}
+template <int V, int K>
+__device__ __forceinline__ void push(Vals<V> (&past)[K], const Vals<V>& x) {
+#pragma unroll
+  for (int j = 0; j + 1 < K; ++j) past[j] = past[j + 1];
+  past[K - 1] = x;
+}
+
+// Row `t` of the sequence's extended rows (t may lie up to K - 1 before its begin).
+template <int V, typename T>
+__device__ __forceinline__ Raws<V, T> row_of(const ShortConvArgs& a, const Cursor& s, int t, int c) {
+  if (!s.inside()) return none<V, T>();
+  if (t >= s.begin) return load<V>(static_cast<const T*>(a.x.p) + s.batch * a.x.sb + t * a.x.sl + c);
+  const int kept = a.K - 1 + t - s.begin;
+  if (!a.state0 || kept < 0) return none<V, T>();
+  return load<V>(static_cast<const T*>(a.state0) + ((size_t)s.seq * (a.K - 1) + kept) * a.D + c);
+}
+template <int V, int K, typename T>
+__device__ __forceinline__ void enter(const ShortConvArgs& a, const Cursor& s, int t, int c, Vals<V> (&past)[K - 1]) {
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) past[j] = widen<V>(row_of<V, T>(a, s, t - (K - 1) + j, c));
+}
+
+// A run of R rows of V channels per thread.  The workgroups behind `runs` copy the
+// kept rows.
+template <int K, int V, int R, typename T>
+__global__ __launch_bounds__(NT) void forward_kernel(ShortConvArgs a, int per_row, long long run_items, unsigned run_blocks) {
+  const int groups = a.D / V;
+  if (blockIdx.x >= run_blocks) {
+    // One (sequence, kept row, channels) per thread.
+    const long long item = (long long)(blockIdx.x - run_blocks) * NT + threadIdx.x;
+    if (item >= (long long)a.n_seq * (K - 1) * groups) return;
+    const long long row = item / groups;
+    const int c = (int)(item - row * groups) * V, seq = (int)(row / (K - 1)), j = (int)(row - (long long)seq * (K - 1));
+    Cursor s(nullptr, a.n_seq, a.L, a.cu ? 0 : seq, 0);
+    s.seq = seq;
+    if (a.cu) {
+      s.begin = min(max(a.cu[seq], 0), a.L);
+      s.end = min(max(a.cu[seq + 1], s.begin), a.L);
+    }
+    store<V>(static_cast<T*>(a.state) + row * a.D + c, row_of<V, T>(a, s, s.end - (K - 1) + j, c));
+    return;
+  }
+  const long long item = (long long)blockIdx.x * NT + threadIdx.x;
+  if (item >= run_items) return;
+  const long long run = item / groups;
+  const int c = (int)(item - run * groups) * V;
+  const int b = (int)(run / per_row), t0 = (int)(run - (long long)b * per_row) * R, t1 = min(t0 + R, a.L);
+  const T* const x = static_cast<const T*>(a.x.p) + b * a.x.sb + c;
+  T* const y = static_cast<T*>(a.y) + (size_t)b * a.L * a.D + c;
+  Raws<V, T> rows[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) rows[i] = load<V>(x + min(t0 + i, t1 - 1) * a.x.sl);
+  Cursor s(a.cu, a.n_seq, a.L, b, t0);
+  const Taps<V, K> taps(a.weight, a.bias, c);
+  Vals<V> past[K - 1];
+  enter<V, K, T>(a, s, t0, c, past);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int t = t0 + i;
+    if (t >= t1) break;
+    if (a.cu && t >= s.end) {
+      s.find(t);
+      enter<V, K, T>(a, s, t, c, past);
+    }
+    const Vals<V> xt = widen<V>(rows[i]);
+    Vals<V> p = pre<V, K>(taps, past, xt);
+    push(past, xt);
+    if (a.silu)
+#pragma unroll
+      for (int k = 0; k < V; ++k) p.v[k / 4][k % 4] *= sigmoid(p.v[k / 4][k % 4]);
+    if (!s.inside()) p = zeros<V>();
+    store<V>(y + (size_t)t * a.D, narrowed<V, T>(p));
+  }
+}
+
+// ---- gradient ------------------------------------------------------------------------
+
+constexpr int BV = 4;  // channels per thread
+
+// dy silu'(p)
+__device__ __forceinline__ Vals<BV> through(const Vals<BV>& p, const Vals<BV>& dy, int silu) {
+  if (!silu) return dy;
+  Vals<BV> q;
+#pragma unroll
+  for (int k = 0; k < BV; ++k) {
+    const float v = p.v[0][k], s = sigmoid(v);
+    q.v[0][k] = dy.v[0][k] * (s * (1.f + v * (1.f - s)));
+  }
+  return q;
+}
+
+// A run of `len` rows per thread, walked K - 1 rows further for the q that reach
+// back into it.  dw and db of a run go to `parts` [run][K + 1][D].  The workgroups
+// behind `run_blocks` form the gradients of the kept rows in front of sequences.
+template <int K, typename T>
+__global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, int per_row, long long run_items,
+                                                      unsigned run_blocks, float* parts) {
+  const int groups = a.D / BV;
+  const bool edge = blockIdx.x >= run_blocks;
+  const long long item = (long long)(blockIdx.x - (edge ? run_blocks : 0)) * NT + threadIdx.x;
+  if (edge) {
+    if (item >= (long long)a.n_seq * groups) return;
+    const int seq = (int)(item / groups), c = (int)(item - (long long)seq * groups) * BV;
+    Cursor s(nullptr, a.n_seq, a.L, a.cu ? 0 : seq, 0);
+    s.seq = seq;
+    if (a.cu) {
+      s.begin = min(max(a.cu[seq], 0), a.L);
+      s.end = min(max(a.cu[seq + 1], s.begin), a.L);
+    }
+    const int n = s.end - s.begin;
+    const Taps<BV, K> taps(a.weight, a.bias, c);
+    Vals<BV> past[K - 1], d[K - 1];
+    enter<BV, K, T>(a, s, s.begin, c, past);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      d[j] = zeros<BV>();
+      // A kept row that is still kept behind a short sequence.
+      if (a.dstate && j >= n) d[j] = widen<BV>(load<BV>(static_cast<const T*>(a.dstate) + ((size_t)seq * (K - 1) + j - n) * a.D + c));
+    }
+    const T* const dy = static_cast<const T*>(a.dy) + (size_t)s.batch * a.L * a.D + c;
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+      if (i >= n) break;
+      const Vals<BV> x = widen<BV>(row_of<BV, T>(a, s, s.begin + i, c));
+      const Vals<BV> q = through(pre<BV, K>(taps, past, x), widen<BV>(load<BV>(dy + (size_t)(s.begin + i) * a.D)), a.silu);
+      push(past, x);
+      // q_i reads kept rows i .. K - 2 with taps 0 .. K - 2 - i.
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+        if (i + j < K - 1) add_product(d[i + j], taps.w[j], q);
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+      store<BV>(static_cast<T*>(a.dstate0) + ((size_t)seq * (K - 1) + j) * a.D + c, narrowed<BV, T>(d[j]));
+    return;
+  }
+  if (item >= run_items) return;
+  const long long run = item / groups;
+  const int c = (int)(item - run * groups) * BV;
+  const int b = (int)(run / per_row), t0 = (int)(run - (long long)b * per_row) * len, t1 = min(t0 + len, a.L);
+  const int stop = min(t1 + K - 1, a.L);
+  const T* const x = static_cast<const T*>(a.x.p) + b * a.x.sb + c;
+  const T* const dy = static_cast<const T*>(a.dy) + (size_t)b * a.L * a.D + c;
+  T* const dx = static_cast<T*>(a.dx) + (size_t)b * a.L * a.D + c;
+  const Taps<BV, K> taps(a.weight, a.bias, c);
+  Cursor s(a.cu, a.n_seq, a.L, b, t0);  // of the row whose q is formed
+  Cursor o = s;                         // of the row whose dx is finished
+  Vals<BV> past[K - 1], q[K], dw[K], db = zeros<BV>();
+  enter<BV, K, T>(a, s, t0, c, past);
+#pragma unroll
+  for (int j = 0; j < K; ++j) q[j] = dw[j] = zeros<BV>();
+  constexpr int U = 4;  // rows whose loads are under way
+  Raws<BV, T> rx[U], ry[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int t = min(t0 + i, stop - 1);
+    rx[i] = load<BV>(x + t * a.x.sl);
+    ry[i] = load<BV>(dy + (size_t)t * a.D);
+  }
+  // Row t forms q_t and finishes dx of row t - K + 1.
+  for (int base = t0; base < t1 + K - 1; base += U) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int t = base + i;
+      const Vals<BV> xt = widen<BV>(rx[i]), dyt = widen<BV>(ry[i]);
+      const int ahead = min(t + U, stop - 1);
+      rx[i] = load<BV>(x + ahead * a.x.sl);
+      ry[i] = load<BV>(dy + (size_t)ahead * a.D);
+      Vals<BV> qt = zeros<BV>();
+      if (t < stop) {
+        if (a.cu && t >= s.end) {
+          s.find(t);
+          enter<BV, K, T>(a, s, t, c, past);
+        }
+        if (s.inside()) {
+          qt = through(pre<BV, K>(taps, past, xt), dyt, a.silu);
+          if (t < t1) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) add_product(dw[j], past[j], qt);
+            add_product(dw[K - 1], xt, qt);
+            db.v[0] += qt.v[0];
+          }
+        }
+        push(past, xt);
+      }
+      push(q, qt);
+      const int r = t - (K - 1);
+      if (r >= t0 && r < t1) {
+        if (a.cu && r >= o.end) o.find(r);
+        Vals<BV> d = zeros<BV>();
+        if (o.inside()) {
+          // q[j] is of row r + j, which reads row r with tap K - 1 - j.
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (r + j < o.end) add_product(d, taps.w[K - 1 - j], q[j]);
+          const int kept = r - (o.end - (K - 1));
+          if (a.dstate && kept >= 0) {
+            const Vals<BV> e = widen<BV>(load<BV>(static_cast<const T*>(a.dstate) + ((size_t)o.seq * (K - 1) + kept) * a.D + c));
+            d.v[0] += e.v[0];
+          }
+        }
+        store<BV>(dx + (size_t)r * a.D, narrowed<BV, T>(d));
+      }
+    }
+  }
+  float* const to = parts + (size_t)run * (K + 1) * a.D + c;
+#pragma unroll
+  for (int j = 0; j < K; ++j) *reinterpret_cast<f32x4*>(to + (size_t)j * a.D) = dw[j].v[0];
+  *reinterpret_cast<f32x4*>(to + (size_t)K * a.D) = db.v[0];
+}
+
+// The runs' parts [run][K + 1][D] added in order, 16 columns per workgroup.
+static __global__ __launch_bounds__(NT) void weight_kernel(const float* parts, int runs, int D, int K, float* dweight, float* dbias) {
+  __shared__ double red[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int e = blockIdx.x * 16 + c, columns = (K + 1) * D;
+  double s = 0.0;
+  if (e < columns) {
+#pragma unroll 8
+    for (int i = r; i < runs; i += 16) s += (double)parts[(size_t)i * columns + e];
+  }
+  red[r][c] = s;
+  __syncthreads();
+  if (r || e >= columns) return;
+  for (int i = 1; i < 16; ++i) s += red[i][c];
+  const int j = e / D, d = e - j * D;
+  if (j < K) dweight[(size_t)d * K + j] = (float)s;
+  else if (dbias) dbias[d] = (float)s;
+}
+
+// ---- one token ------------------------------------------------------------------------
+
+template <int K, int V, typename T>
+__global__ __launch_bounds__(NT) void step_kernel(ShortConvArgs a, long long items) {
+  const long long item = (long long)blockIdx.x * NT + threadIdx.x;
+  if (item >= items) return;
+  const int groups = a.D / V, b = (int)(item / groups), c = (int)(item - (long long)b * groups) * V;
+  T* const kept = static_cast<T*>(a.state) + (size_t)b * (K - 1) * a.D + c;
+  const Raws<V, T> x = load<V>(static_cast<const T*>(a.x.p) + b * a.x.sb + c);
+  Raws<V, T> rows[K - 1];
+  Vals<V> past[K - 1];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) rows[j] = load<V>(kept + (size_t)j * a.D);
+  const Taps<V, K> taps(a.weight, a.bias, c);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) past[j] = widen<V>(rows[j]);
+  Vals<V> p = pre<V, K>(taps, past, widen<V>(x));
+  if (a.silu)
+#pragma unroll
+    for (int k = 0; k < V; ++k) p.v[k / 4][k % 4] *= sigmoid(p.v[k / 4][k % 4]);
+#pragma unroll
+  for (int j = 0; j + 1 < K - 1; ++j) store<V>(kept + (size_t)j * a.D, rows[j + 1]);
+  store<V>(kept + (size_t)(K - 2) * a.D, x);
+  store<V>(static_cast<T*>(a.y) + (size_t)b * a.D + c, narrowed<V, T>(p));
+}
+
+// ---- launches -------------------------------------------------------------------------
+
+constexpr int kRun = 16;
+
+static unsigned blocks_for(long long items) { return (unsigned)((items + NT - 1) / NT); }
+
+template <int K, typename T>
+static hipError_t forward(const ShortConvArgs& a) {
+  constexpr int V = 16 / sizeof(T);
+  const int per_row = (int)(((long long)a.L + kRun - 1) / kRun);
+  const long long items = (long long)a.B * per_row * (a.D / V), kept = a.state ? (long long)a.n_seq * (K - 1) * (a.D / V) : 0;
+  const unsigned n = blocks_for(items), m = blocks_for(kept);
+  if (n + m == 0) return hipSuccess;
+  prof_mark(kSlotShortConv, false, a.stream);
+  hipLaunchKernelGGL((forward_kernel<K, V, kRun, T>), dim3(n + m), dim3(NT), 0, a.stream, a, per_row, items, n);
+  const hipError_t e = hipGetLastError();
+  prof_mark(kSlotShortConv, true, a.stream);
+  return e;
+}
+
+// Rows per run of the backward: about 1024 threads for every CU, runs of 16 to 256 rows.
+struct Runs {
+  int len, per_row;
+  long long n;
+};
+static Runs backward_runs(int B, int L, int D) {
+  const long long groups = D / BV, want = 262144 / groups + 1;
+  long long len = ((long long)B * L + want - 1) / want;
+  len = len < 16 ? 16 : len > 256 ? 256 : len;
+  Runs r;
+  r.len = (int)len;
+  r.per_row = (int)((L + len - 1) / len);
+  r.n = (long long)B * r.per_row;
+  return r;
+}
+
+template <int K, typename T>
+static hipError_t backward(const ShortConvArgs& a) {
+  const Runs r = backward_runs(a.B, a.L, a.D);
+  const long long groups = a.D / BV, items = r.n * groups;
+  const unsigned n = blocks_for(items), m = a.dstate0 ? blocks_for(a.n_seq * groups) : 0;
+  float* const parts = static_cast<float*>(a.workspace);
+  prof_mark(kSlotShortConvBwd, false, a.stream);
+  hipError_t e = hipSuccess;
+  if (n + m > 0) {
+    hipLaunchKernelGGL((backward_kernel<K, T>), dim3(n + m), dim3(NT), 0, a.stream, a, r.len, r.per_row, items, n, parts);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess) {
+    hipLaunchKernelGGL(weight_kernel, dim3((unsigned)(((K + 1) * a.D + 15) / 16)), dim3(NT), 0, a.stream, parts, (int)r.n, a.D, K,
+                       a.dweight, a.dbias);
+    e = hipGetLastError();
+  }
+  prof_mark(kSlotShortConvBwd, true, a.stream);
+  return e;
+}
+
+template <int K, typename T>
+static hipError_t step(const ShortConvArgs& a) {
+  constexpr int V = 16 / sizeof(T);
+  const long long items = (long long)a.B * (a.D / V);
+  prof_mark(kSlotShortConv, false, a.stream);
+  hipLaunchKernelGGL((step_kernel<K, V, T>), dim3(blocks_for(items)), dim3(NT), 0, a.stream, a, items);
+  const hipError_t e = hipGetLastError();
+  prof_mark(kSlotShortConv, true, a.stream);
+  return e;
+}
+
+}  // namespace conv
+
+// Whether the forward's and backward's launches hold these sizes.
+bool short_conv_fits(int B, int L, int D, int n_seq, int dtype) {
+  const long long v = dtype == 1 ? 8 : 4, most = max_blocks(conv::NT) - 1;
+  const long long runs = (long long)B * (((long long)L + conv::kRun - 1) / conv::kRun);
+  // (Either product may be beyond 64 bits only where its first factor is already too much.)
+  if (runs > (most << 8) || n_seq > (1 << 24)) return false;
+  const long long items = runs * (D / v), kept = (long long)n_seq * 3 * (D / v), edge = (long long)n_seq * (D / 4);
+  return (items >> 8) + (kept >> 8) + 2 <= most && ((runs * (D / 4)) >> 8) + (edge >> 8) + 2 <= most;
+}
+
+hipError_t launch_short_conv(const ShortConvArgs& a) {
+  if (a.dtype == 1) return a.K == 2 ? conv::forward<2, bf16>(a) : a.K == 3 ? conv::forward<3, bf16>(a) : conv::forward<4, bf16>(a);
+  return a.K == 2 ? conv::forward<2, float>(a) : a.K == 3 ? conv::forward<3, float>(a) : conv::forward<4, float>(a);
+}
+
+size_t short_conv_bwd_workspace_bytes(int B, int L, int D, int K) {
+  return (size_t)conv::backward_runs(B, L, D).n * (K + 1) * D * sizeof(float);
+}
+
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a) {
+  if (a.dtype == 1) return a.K == 2 ? conv::backward<2, bf16>(a) : a.K == 3 ? conv::backward<3, bf16>(a) : conv::backward<4, bf16>(a);
+  return a.K == 2 ? conv::backward<2, float>(a) : a.K == 3 ? conv::backward<3, float>(a) : conv::backward<4, float>(a);
+}
+
+hipError_t launch_short_conv_step(const ShortConvArgs& a) {
+  if (a.dtype == 1) return a.K == 2 ? conv::step<2, bf16>(a) : a.K == 3 ? conv::step<3, bf16>(a) : conv::step<4, bf16>(a);
+  return a.K == 2 ? conv::step<2, float>(a) : a.K == 3 ? conv::step<3, float>(a) : conv::step<4, float>(a);
+}
+
+}  // namespace dn

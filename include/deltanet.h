@@ -449,6 +449,131 @@ int deltanet_qk_norm_rope_bwd(const void* q_raw, const long long* q_strides,
 size_t deltanet_qk_norm_rope_bwd_workspace_bytes(int B, int H_q, int H_k, int L, int d_k,
                                                  dn_dtype dtype);
 
+/*
+ * Short causal convolution: each channel's last K tokens, in front of a layer's
+ * recurrence.  With x_e the K - 1 rows kept from before a sequence followed by its rows,
+ *     p_t = bias + sum_j weight[:, j] o x_e[t + j],  j = 0 .. K - 1
+ *     y_t = silu(p_t)   (silu = 0: p_t)
+ * and the rows kept behind the sequence are x_e's last K - 1 (so a sequence may be
+ * taken in pieces, and by single tokens).
+ *
+ *   x      : rows of [B, L, D] dtype at x_strides[0] b + x_strides[1] t elements
+ *            (x_strides: HOST array of 2, or NULL: dense), e.g. a part of a fused
+ *            projection's rows.  Strides are >= 0 and keep rows 16-byte aligned.
+ *   weight : [D, K] fp32;  bias: [D] fp32 or NULL
+ *   state0 : [n, K - 1, D] dtype, the kept rows in front, oldest first, or NULL (zeros)
+ *   cu_seqlens: NULL: B sequences of L tokens (n = B, n_seq is not used).  Or [n_seq + 1]
+ *            int32 on the device, B = 1: sequence i holds rows cu_seqlens[i] to
+ *            cu_seqlens[i + 1] - 1 (none if they are equal), n = n_seq.  They may not
+ *            fall and lie in 0 .. L; where they do not, the results are not defined,
+ *            but nothing outside the tensors is read or written.
+ *   y      : [B, L, D] dtype, dense, written.  Rows that no sequence holds (in front of
+ *            the first, behind the last) become zeros, so that a product over all
+ *            rows stays finite.
+ *   state  : [n, K - 1, D] dtype, the kept rows behind, or NULL (not written); not state0
+ *   D a multiple of 8; K in {2, 3, 4}.  Evaluated in fp32.
+ */
+int deltanet_short_conv_fwd(const void* x, const long long* x_strides, const float* weight, const float* bias,
+                            const void* state0, const int* cu_seqlens, void* y, void* state,
+                            int B, int L, int D, int K, int n_seq, int silu, dn_dtype dtype, hipStream_t stream);
+
+/*
+ * Its gradient, from dy ([B, L, D] dtype, dense) and dstate ([n, K - 1, D] dtype or NULL):
+ *   dx     : [B, L, D] dtype, dense (zeros in rows that no sequence holds)
+ *   dweight: [D, K] fp32;  dbias: [D] fp32 or NULL (not written); both summed in an order
+ *            that does not change from call to call
+ *   dstate0: [n, K - 1, D] dtype or NULL (not written)
+ */
+int deltanet_short_conv_bwd(const void* x, const long long* x_strides, const float* weight, const float* bias,
+                            const void* state0, const int* cu_seqlens, const void* dy, const void* dstate,
+                            void* dx, float* dweight, float* dbias, void* dstate0,
+                            int B, int L, int D, int K, int n_seq, int silu, dn_dtype dtype,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace deltanet_short_conv_bwd needs (0 also if the sizes are invalid or unsupported). */
+size_t deltanet_short_conv_bwd_workspace_bytes(int B, int L, int D, int K);
+
+/* One token of every sequence: x [B, D] (rows at *x_stride elements, NULL: dense), y [B, D];
+ * state [B, K - 1, D] is moved on by a row in place. */
+int deltanet_short_conv_step(const void* x, const long long* x_stride, const float* weight, const float* bias,
+                             void* state, void* y, int B, int D, int K, int silu, dn_dtype dtype, hipStream_t stream);
+
+/*
+ * Selective state space scan: a recurrence with a decay of its own for every channel d
+ * and state n, set by the token.  Per sequence, token t in order:
+ *     dt_t = softplus(raw_t + dt_bias)           (softplus = 0: raw_t + dt_bias)
+ *     h[d, n] = exp(dt_t[d] A[d, n]) h[d, n] + dt_t[d] u_t[d] B_t[n]
+ *     y_t[d]  = (sum_n C_t[n] h[d, n] + D_skip[d] u_t[d]) silu(z_t[d])     (without z: no last factor)
+ *
+ *   u, dt, z: rows of [B, L, D] dtype; dt is raw; z may be NULL.  B, C (Bm, Cm): rows of
+ *            [B, L, N] dtype, shared by all channels.  strides: HOST array of 10, (batch, token)
+ *            of u, dt, Bm, Cm, z in this order, or NULL (all dense); rules as above.
+ *   A      : [D, N] fp32 (negative for states that decay);  D_skip, dt_bias: [D] fp32 or NULL (zeros)
+ *   h0     : [n, D, N] fp32 or NULL (zeros);  cu_seqlens, n_seq, n: as above
+ *   y      : [B, L, D] dtype, dense, written (zeros in rows that no sequence holds)
+ *   hT     : [n, D, N] fp32, the states behind, or NULL; may be h0 (in place)
+ *   D a multiple of 8; N in {8, 16, 32}.  Evaluated in fp32; L = 0 copies h0.
+ * A state that is not finite, and tokens that are not, stay in their own channel and sequence.
+ * A long sequence of few channels is cut into segments whose states are joined: the decay over
+ * a segment is then exp(A sum dt), and a state that overflows inside the sequence need not do
+ * so at the same token as in a walk from its start.
+ */
+int deltanet_selective_scan_fwd(const void* u, const void* dt, const void* Bm, const void* Cm, const void* z,
+                                const long long* strides, const float* A, const float* D_skip, const float* dt_bias,
+                                const float* h0, const int* cu_seqlens, void* y, float* hT,
+                                int B, int L, int D, int N, int n_seq, int softplus, dn_dtype dtype,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace deltanet_selective_scan_fwd needs (packed: whether cu_seqlens is given; 0
+ * also if the sizes are invalid or unsupported). */
+size_t deltanet_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, int packed, int n_seq);
+
+/*
+ * Its gradient, from dy ([B, L, D] dtype, dense) and dhT ([n, D, N] fp32 or NULL):
+ *   du, ddt (of raw), dz: [B, L, D] dtype, dense; dB, dC: [B, L, N] dtype, dense (zeros in rows that
+ *            no sequence holds); dz is not used without z
+ *   dA     : [D, N] fp32;  dD_skip, ddt_bias: [D] fp32 or NULL (not written);  dh0: [n, D, N] fp32 or NULL
+ * Nothing from a forward call is needed.  All sums run in an order that does not change from
+ * call to call.  The workspace holds a state for every 16 tokens.
+ */
+int deltanet_selective_scan_bwd(const void* u, const void* dt, const void* Bm, const void* Cm, const void* z,
+                                const long long* strides, const float* A, const float* D_skip, const float* dt_bias,
+                                const float* h0, const int* cu_seqlens, const void* dy, const float* dhT,
+                                void* du, void* ddt, void* dB, void* dC, void* dz,
+                                float* dA, float* dD_skip, float* ddt_bias, float* dh0,
+                                int B, int L, int D, int N, int n_seq, int softplus, dn_dtype dtype,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t deltanet_selective_scan_bwd_workspace_bytes(int B, int L, int D, int N, int packed, int n_seq);
+
+/* One token of every sequence: u, dt, z, y [B, D], Bm, Cm [B, N] (strides: HOST array of 5 row strides
+ * in the same order, or NULL); h [B, D, N] fp32 updated in place. */
+int deltanet_selective_scan_step(const void* u, const void* dt, const void* Bm, const void* Cm, const void* z,
+                                 const long long* strides, const float* A, const float* D_skip, const float* dt_bias,
+                                 float* h, void* y, int B, int D, int N, int softplus, dn_dtype dtype, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of rows with the residual's addition, in front of a layer's projections:
+ *     total = x + residual, rounded to residual_dtype;   y = total / sqrt(mean(total^2) + eps) o weight
+ *   x      : [rows, D] dtype;  residual, total: [rows, D] residual_dtype, both NULL for the norm of x
+ *            alone.  total may be residual, or x where the types agree (in place).
+ *   weight : [D] fp32 or NULL (ones)
+ *   y      : [rows, D] dtype;  or, with scale ([rows] fp32), 8-bit e4m3 values with
+ *            y = value * scale: scale is the row's largest magnitude / 448 (1 for a row of zeros)
+ *   D a multiple of 8, up to 32768; dtype = DN_F32 needs residual_dtype = DN_F32.  Evaluated in fp32.
+ */
+int deltanet_add_rms_norm(const void* x, const void* residual, const float* weight, void* total, void* y, float* scale,
+                          int rows, int D, float eps, dn_dtype dtype, dn_dtype residual_dtype, hipStream_t stream);
+
+/*
+ * Its gradient, from dy ([rows, D] dtype) and dtotal ([rows, D] residual_dtype, what reaches total from
+ * elsewhere, or NULL); total as the forward wrote it (the norm of x alone: x, with residual_dtype = dtype):
+ *   dx     : [rows, D] dtype;  dresidual: the same in residual_dtype, or NULL (not written)
+ *   dweight: [D] fp32 or NULL (not written), summed in an order that does not change from call to call
+ */
+int deltanet_add_rms_norm_bwd(const void* total, const float* weight, const void* dy, const void* dtotal,
+                              void* dx, void* dresidual, float* dweight, int rows, int D, float eps,
+                              dn_dtype dtype, dn_dtype residual_dtype,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t deltanet_add_rms_norm_bwd_workspace_bytes(int rows, int D);
+
 /* Static, NUL-terminated description of a status code. */
 const char* deltanet_status_string(int status);
 
@@ -469,7 +594,9 @@ int deltanet_last_hip_error(void);
  * kernel computes both the matrix gradients and dq / dk and is counted in
  * slot 8; the gated linear recurrence's: 9 = segment sums and their
  * combination, 10 = outputs, 11 = the backward's walks and decay gradient,
- * 12 = decode; the q / k norm with rotation: 13 = forward, 14 = backward).
+ * 12 = decode; the q / k norm with rotation: 13 = forward, 14 = backward; the
+ * short convolution: 15 = forward and step, 16 = backward; the selective scan:
+ * 17 = forward, 18 = backward, 19 = step; the norm with addition: 20, 21).
  * Recording adds two event records per launch.
  * deltanet_profile_start() creates the thread's events up front (4096,
  * enough for 2048 launches; more are created as needed), so it can take a
