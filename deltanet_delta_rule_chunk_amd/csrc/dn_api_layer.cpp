@@ -173,8 +173,8 @@ int deltanet_short_conv_bwd(const void* x, const long long* x_strides, const flo
   const Span in[] = {{x, rows.bytes}, {weight, wb}, {bias, (size_t)D * 4}, {state0, kept}, {cu_seqlens, cu_bytes(cu_seqlens, a.n_seq)},
                      {dy, tokens}, {dstate, kept}};
   const Span out[] = {{dx, tokens}, {dweight, wb}, {dbias, (size_t)D * 4}, {dstate0, kept}};
-  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   if (workspace && workspace_bytes < need) return DN_ERR_WORKSPACE;
+  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   Workspace w(workspace, need, stream);
   if (w.error() != hipSuccess) return hip_fail(w.error());
   a.dy = dy;
@@ -228,8 +228,8 @@ int deltanet_selective_scan_fwd(const void* u, const void* dt, const void* Bm, c
   const Span in[] = {{u, rows[0].bytes}, {dt, rows[1].bytes}, {Bm, rows[2].bytes}, {Cm, rows[3].bytes}, {z, rows[4].bytes}, {A, state},
                      {D_skip, vec}, {dt_bias, vec}, {hT == h0 ? nullptr : h0, states}, {cu_seqlens, cu_bytes(cu_seqlens, a.n_seq)}};
   const Span out[] = {{y, (size_t)B * L * D * dtype_size(dtype)}, {hT, states}};
-  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   if (workspace && workspace_bytes < need) return DN_ERR_WORKSPACE;
+  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   Workspace w(workspace, need, stream);
   if (w.error() != hipSuccess) return hip_fail(w.error());
   a.y = y;
@@ -264,8 +264,8 @@ int deltanet_selective_scan_bwd(const void* u, const void* dt, const void* Bm, c
                      {D_skip, vec}, {dt_bias, vec}, {h0, states}, {cu_seqlens, cu_bytes(cu_seqlens, a.n_seq)}, {dy, tokens}, {dhT, states}};
   const Span out[] = {{du, tokens}, {ddt, tokens}, {dB, bc}, {dC, bc}, {z ? dz : nullptr, tokens}, {dA, state},
                       {dD_skip, vec}, {ddt_bias, vec}, {dh0, states}};
-  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   if (workspace && workspace_bytes < need) return DN_ERR_WORKSPACE;
+  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   Workspace w(workspace, need, stream);
   if (w.error() != hipSuccess) return hip_fail(w.error());
   a.dy = dy;
@@ -352,8 +352,8 @@ int deltanet_add_rms_norm_bwd(const void* total, const float* weight, const void
   const size_t need = dn::add_norm_bwd_workspace_bytes(rows, D);
   const Span in[] = {{total, n * r}, {weight, wb}, {dy, n * e}, {dtotal, n * r}};
   const Span out[] = {{dx, n * e}, {dresidual, n * r}, {dweight, wb}};
-  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   if (workspace && workspace_bytes < need) return DN_ERR_WORKSPACE;
+  if (any_overlap(in, out, Span{workspace, workspace ? need : 0})) return DN_ERR_ALIASING;
   Workspace w(workspace, need, stream);
   if (w.error() != hipSuccess) return hip_fail(w.error());
   dn::AddNormArgs a{};
