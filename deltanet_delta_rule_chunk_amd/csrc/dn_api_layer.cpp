@@ -25,7 +25,7 @@ int check_tokens(const void* p, const long long* strides, int B, int L, int d, s
   for (int i = 0; i < 2; ++i) {
     if (n[i] == 1) continue;  // this stride is not used
     if (s[i] < 0) return DN_ERR_BAD_SHAPE;
-    if (s[i] > (1LL << 58) / n[i]) return DN_ERR_UNSUPPORTED;
+    if (s[i] > (1LL << 58) / n[i] || (i == 1 && s[i] > dn::kMostTokenStride)) return DN_ERR_UNSUPPORTED;
     if (s[i] * (long long)size % 16) return DN_ERR_MISALIGNED;
     last += (n[i] - 1) * s[i];
   }
@@ -48,7 +48,7 @@ int check_conv(const void* x, const long long* strides, const float* weight, con
   int st = check_sequences(cu, B, n_seq);
   if (st != DN_OK) return st;
   if (!cu) n_seq = B;
-  if (L > 0x7fffffff - 1024 || D > 1 << 28 || !dn::short_conv_fits(B, L, D, n_seq, dtype)) return DN_ERR_UNSUPPORTED;
+  if (L > 0x7fffffff - 1024 || D > dn::kMostTokenStride || !dn::short_conv_fits(B, L, D, n_seq, dtype)) return DN_ERR_UNSUPPORTED;
   if (!weight || (L > 0 && !x)) return DN_ERR_NULL_ARG;
   st = check_tokens(x, strides, B, L, D, dtype_size(dtype), rows);
   if (st != DN_OK) return st;
@@ -84,7 +84,7 @@ int check_scan_sizes(const int* cu, int B, int L, int D, int N, int* n_seq, int 
   const int st = check_sequences(cu, B, *n_seq);
   if (st != DN_OK) return st;
   if (!cu) *n_seq = B;
-  return D <= 1 << 25 && dn::selective_scan_fits(B, L, D, N, cu, *n_seq, backward) ? DN_OK : DN_ERR_UNSUPPORTED;
+  return D <= dn::kMostTokenStride && dn::selective_scan_fits(B, L, D, N, cu, *n_seq, backward) ? DN_OK : DN_ERR_UNSUPPORTED;
 }
 int check_scan(const ScanIn& x, bool backward, dn::ScanArgs* a, Tokens (&rows)[5]) {
   int n_seq = x.n_seq;
@@ -154,7 +154,7 @@ int deltanet_short_conv_fwd(const void* x, const long long* x_strides, const flo
 
 size_t deltanet_short_conv_bwd_workspace_bytes(int B, int L, int D, int K) {
   if (B < 1 || L < 0 || D < 1 || D % 8 || K < 2 || K > 4) return 0;
-  if (L > 0x7fffffff - 1024 || D > 1 << 28 || !dn::short_conv_fits(B, L, D, 1, DN_F32)) return 0;
+  if (L > 0x7fffffff - 1024 || D > dn::kMostTokenStride || !dn::short_conv_fits(B, L, D, 1, DN_F32)) return 0;
   return dn::short_conv_bwd_workspace_bytes(B, L, D, K);
 }
 

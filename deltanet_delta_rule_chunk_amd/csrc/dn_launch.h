@@ -206,7 +206,9 @@ long long qk_norm_rope_max_tokens(int heads, int d);
 size_t qk_norm_rope_bwd_workspace_bytes(int B, int heads, int L, int d);
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeArgs& a);
 
-// Rows of [B, L, D] at strides in elements.
+// Rows of [B, L, D] at strides in elements.  32 rows at the largest token stride lie
+// within 32 bits of bytes, where kernels keep a thread's offsets in a tile.
+constexpr long long kMostTokenStride = 1LL << 24;
 struct TokenRows {
   const void* p;
   long long sb, sl;

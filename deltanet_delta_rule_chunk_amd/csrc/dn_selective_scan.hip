@@ -124,7 +124,7 @@ hipError_t combine(const Plan& p, int n_seq, int D, int N, const float* A, const
 // sequence is cut).  Otherwise: each segment's last state and sum of dt.
 template <int NW, typename T, bool GATE, bool OUT>
 __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int blocks_d, float* states, float* logs) {
-  constexpr int N = 4 * NW;
+  constexpr int N = 4 * NW, R = group_rows<T>();
   using At = Spot<NW>;
   __shared__ float2 sx[OUT ? 1 : 2][kTile][kCh];  // dt, dt u
   __shared__ float sy[OUT ? NW : 1][OUT ? kTile : 1][kCh];
@@ -133,22 +133,22 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
   Segment g;
   if (!segment_of(pl, id, g)) return;
   const At at;
-  const int c = ch0 + at.c;
-  const bool has = c < a.D, on = ch < a.D;
-  T* const y = static_cast<T*>(a.y) + ((size_t)g.batch * a.L + g.row) * a.D + c;
+  const bool has = ch0 + at.c < a.D, on = ch < a.D;
+  const int c = has ? ch0 + at.c : a.D - 4;
+  T* y = static_cast<T*>(a.y) + ((size_t)g.batch * a.L + g.row) * a.D;  // of the tile
   if (g.seq < 0) {
     if (OUT && has)
-      for (int r = at.r; r < g.n; r += At::kRows) put4(y + (size_t)r * a.D, zero4());
+      for (int r = at.r; r < g.n; r += At::kRows) put4(y + (size_t)r * a.D + c, zero4());
     return;
   }
   if (!OUT && g.last) return;  // nothing asks for its last state
-  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
-  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
-  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
-  const T* const Bm = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + g.row * a.Bm.sl + 4 * w;
-  const T* const Cm = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + g.row * a.Cm.sl + 4 * w;
-  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
-  const f32x4 skip = OUT && has && a.skip ? get4(a.skip + c) : zero4();
+  Feed<NW, T> u(a.u.p, g.batch * a.u.sb + g.row * a.u.sl, a.u.sl, at, c);
+  Feed<NW, T> dt(a.dt.p, g.batch * a.dt.sb + g.row * a.dt.sl, a.dt.sl, at, c);
+  Feed<NW, T> z(a.z.p, g.batch * a.z.sb + g.row * a.z.sl, a.z.sl, at, c);
+  const T* Bt = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + g.row * a.Bm.sl + 4 * w;  // of the tile
+  const T* Ct = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + g.row * a.Cm.sl + 4 * w;
+  const f32x4 bias = a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  const f32x4 skip = OUT && a.skip ? get4(a.skip + c) : zero4();
   f32x4 A2 = zero4(), h = zero4();
   if (on) {
     A2 = get4(a.A + (size_t)ch * N + 4 * w) * kLog2e;
@@ -157,75 +157,90 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
     if (from) h = get4(from + (size_t)ch * N + 4 * w);
   }
   float sum = 0.f;
-
-  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses];
-  const auto fetch = [&](int t0) {
-#pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      const int r = t0 + at.row(p);
-      ru[p] = rd[p] = rz[p] = narrow<T>(zero4());
-      if (has && at.in_tile(p) && r < g.n) {
-        ru[p] = raw4(u + r * a.u.sl);
-        rd[p] = raw4(dt + r * a.dt.sl);
-        if (OUT && GATE) rz[p] = raw4(z + r * a.z.sl);
-      }
-    }
+  const auto fetch = [&](int n) {
+    if (n <= 0) return;
+    u.fetch(at, c, n);
+    dt.fetch(at, c, n);
+    if (OUT && GATE) z.fetch(at, c, n);
   };
-  fetch(0);
+  fetch(g.n);
   int buf = 0;
-  for (int t0 = 0; t0 < g.n; t0 += kTile) {
-    f32x4 uu[At::kPasses], zz[At::kPasses];
+  for (int left = g.n; left > 0; left -= kTile) {
+    Raw4<T> uu[At::kPasses], zz[At::kPasses];
+    if (at.in_tile()) {
 #pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      if (!at.in_tile(p)) continue;
-      uu[p] = wide(ru[p]);
-      zz[p] = wide(rz[p]);
-      const f32x4 d = softplus4(wide(rd[p]) + bias, a.softplus), x = d * uu[p];
-      f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
-      out[0] = f32x4{d[0], x[0], d[1], x[1]};
-      out[1] = f32x4{d[2], x[2], d[3], x[3]};
-    }
-    fetch(t0 + kTile);
-    __syncthreads();
-    const int n = min(kTile, g.n - t0);
-    float part = 0.f;
-    const auto step = [&](int t) {
-      const f32x4 b = uniform4(Bm + (t0 + t) * a.Bm.sl);
-      const float2 x = sx[buf][t][lane];
-      if (OUT) {
-        const f32x4 cc = uniform4(Cm + (t0 + t) * a.Cm.sl);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[i] = fmaf(exp2_fast(x.x * A2[i]), h[i], x.y * b[i]);
-          s = fmaf(h[i], cc[i], s);
-        }
-        sy[w][t][lane] = s;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_fast(x.x * A2[i]), h[i], x.y * b[i]);
-        part += x.x;
+      for (int p = 0; p < At::kPasses; ++p) {
+        uu[p] = u.raw[p];
+        if (OUT && GATE) zz[p] = z.raw[p];
+        const f32x4 d = softplus4(wide(dt.raw[p]) + bias, a.softplus), x = d * wide(uu[p]);
+        f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
+        out[0] = f32x4{d[0], x[0], d[1], x[1]};
+        out[1] = f32x4{d[2], x[2], d[3], x[3]};
       }
-    };
-    if (n == kTile) {
-#pragma unroll
-      for (int t = 0; t < kTile; ++t) step(t);
-    } else {
-      for (int t = 0; t < n; ++t) step(t);
     }
+    u.move(1);
+    dt.move(1);
+    if (OUT && GATE) z.move(1);
+    fetch(left - kTile);
+    float part = 0.f;
+    const auto step = [&](int t, f32x4 b, f32x4 cc, float2 x) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = fmaf(exp2_fast(x.x * A2[i]), h[i], x.y * b[i]);
+        if (OUT) s = fmaf(h[i], cc[i], s);
+      }
+      if (OUT) sy[w][t][lane] = s;
+      else part += x.x;
+    };
+    if (left >= kTile) {
+      Group<T> gb[2], gc[2];
+      float2 x[2][R];
+      gb[0].load(Bt, a.Bm.sl);
+      if (OUT) gc[0].load(Ct, a.Cm.sl);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < R; ++i) x[0][i] = sx[buf][i][lane];
+      wait_reads();
+#pragma unroll
+      for (int q = 0; q < kTile / R; ++q) {
+        const int now = q & 1, next = now ^ 1;
+        if (q + 1 < kTile / R) {
+          gb[next].load(Bt + (q + 1) * R * a.Bm.sl, a.Bm.sl);
+          if (OUT) gc[next].load(Ct + (q + 1) * R * a.Cm.sl, a.Cm.sl);
+#pragma unroll
+          for (int i = 0; i < R; ++i) x[next][i] = sx[buf][(q + 1) * R + i][lane];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) step(q * R + i, wide(gb[now].r[i]), OUT ? wide(gc[now].r[i]) : zero4(), x[now][i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      __syncthreads();
+      for (int t = 0; t < left; ++t)
+        step(t, wide(uniform4(Bt + t * a.Bm.sl)), OUT ? wide(uniform4(Ct + t * a.Cm.sl)) : zero4(), sx[buf][t][lane]);
+    }
+    Bt += kTile * a.Bm.sl;
+    Ct += kTile * a.Cm.sl;
     sum += part;
     if (OUT) {
       __syncthreads();
+      if (at.in_tile()) {
 #pragma unroll
-      for (int p = 0; p < At::kPasses; ++p) {
-        if (!at.in_tile(p)) continue;
-        const int r = at.row(p);
-        f32x4 s = skip * uu[p];
+        for (int p = 0; p < At::kPasses; ++p) {
+          const int r = at.row(p);
+          f32x4 s = skip * wide(uu[p]);
 #pragma unroll
-        for (int i = 0; i < NW; ++i) s += get4(&sy[i][r][at.c]);
-        if (GATE) s *= zz[p] * sigmoid4(zz[p]);
-        if (has && r < n) put4(y + (size_t)(t0 + r) * a.D, s);
+          for (int i = 0; i < NW; ++i) s += get4(&sy[i][r][at.c]);
+          if (GATE) {
+            const f32x4 v = wide(zz[p]);
+            s *= v * sigmoid4(v);
+          }
+          if (has && r < left) put4(const_cast<T*>(at_bytes(y, offset_of<T>(r, a.D, c))), s);
+        }
       }
+      y += (size_t)kTile * a.D;
     } else {
       buf ^= 1;
     }

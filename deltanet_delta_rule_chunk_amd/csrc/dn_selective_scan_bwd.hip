@@ -41,110 +41,126 @@ struct BwdSpace {
 // ---- states in front of tiles; what segments make from zero in both directions ----------------
 
 // blockIdx.y = 0: forward.  1 (cut sequences only): backward.
-template <int NW, typename T, bool GATE, bool SPLIT>
-__global__ __launch_bounds__(64 * NW) void sums_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
-  constexpr int N = 4 * NW;
+template <int NW, typename T, bool GATE, bool SPLIT, bool BACK>
+__device__ __forceinline__ void sums(const ScanArgs& a, const Plan& pl, int blocks_d, const BwdSpace& ws,
+                                     float2 (&sx)[2][kTile][kCh]) {
+  constexpr int N = 4 * NW, R = group_rows<T>();
   using At = Spot<NW>;
-  __shared__ float2 sx[2][kTile][kCh];  // dt, and dt u or g
   const int id = blockIdx.x / blocks_d, ch0 = (blockIdx.x - id * blocks_d) * kCh;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ch = ch0 + lane;
   Segment g;
   if (!segment_of(pl, id, g) || g.seq < 0) return;
-  const bool back = SPLIT && blockIdx.y;
-  if (back && g.first) return;  // nothing asks for what arrives at its front
+  if (BACK && g.first) return;  // nothing asks for what arrives at its front
   const At at;
-  const int c = ch0 + at.c;
-  const bool has = c < a.D, on = ch < a.D;
-  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
-  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
-  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
-  const T* const dy = static_cast<const T*>(a.dy) + ((size_t)g.batch * a.L + g.row) * a.D + c;
-  const TokenRows& m = back ? a.Cm : a.Bm;
-  const T* const M = static_cast<const T*>(m.p) + g.batch * m.sb + g.row * m.sl + 4 * w;
-  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  const bool on = ch < a.D;
+  const int c = ch0 + at.c < a.D ? ch0 + at.c : a.D - 4;
+  const int tiles = (g.n + kTile - 1) / kTile;
+  const int begin = BACK ? (tiles - 1) * kTile : 0;  // first row of the first tile
+  const long long row = g.row + begin;
+  Feed<NW, T> x(BACK ? a.dy : a.u.p, BACK ? ((long long)g.batch * a.L + row) * a.D : g.batch * a.u.sb + row * a.u.sl,
+                BACK ? a.D : a.u.sl, at, c);
+  Feed<NW, T> dt(a.dt.p, g.batch * a.dt.sb + row * a.dt.sl, a.dt.sl, at, c);
+  Feed<NW, T> z(a.z.p, g.batch * a.z.sb + row * a.z.sl, a.z.sl, at, c);
+  const TokenRows& m = BACK ? a.Cm : a.Bm;
+  const T* M = static_cast<const T*>(m.p) + g.batch * m.sb + row * m.sl + 4 * w;  // of the tile
+  const f32x4 bias = a.dt_bias ? get4(a.dt_bias + c) : zero4();
   f32x4 A2 = zero4(), h = zero4();
   const size_t place = (size_t)ch * N + 4 * w, state = (size_t)a.D * N;
   if (on) {
     A2 = get4(a.A + place) * kLog2e;
-    if (back ? g.last && a.dhT : g.first && a.h0) h = get4((back ? a.dhT : a.h0) + (size_t)g.seq * state + place);
+    if (BACK ? g.last && a.dhT : g.first && a.h0) h = get4((BACK ? a.dhT : a.h0) + (size_t)g.seq * state + place);
   }
   const long long tile0 = first_tile(pl, g, id);
-  const int tiles = (g.n + kTile - 1) / kTile;
   float sum = 0.f;
-
-  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses];
-  const auto fetch = [&](int tile) {
-#pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      const int r = tile * kTile + at.row(p);
-      ru[p] = rd[p] = rz[p] = narrow<T>(zero4());
-      if (has && at.in_tile(p) && tile >= 0 && r < g.n) {
-        rd[p] = raw4(dt + r * a.dt.sl);
-        ru[p] = back ? raw4(dy + (size_t)r * a.D) : raw4(u + r * a.u.sl);
-        if (GATE && back) rz[p] = raw4(z + r * a.z.sl);
-      }
-    }
+  const auto fetch = [&](int n) {
+    x.fetch(at, c, n);
+    dt.fetch(at, c, n);
+    if (GATE && BACK) z.fetch(at, c, n);
   };
-  const int step = back ? -1 : 1;
-  int tile = back ? tiles - 1 : 0, buf = 0;
-  fetch(tile);
-  for (int i = 0; i < tiles; ++i, tile += step, buf ^= 1) {
+  constexpr int kStep = BACK ? -1 : 1;
+  int tile = BACK ? tiles - 1 : 0, buf = 0;
+  if (tiles > 0) fetch(g.n - begin);
+  for (int i = 0; i < tiles; ++i, tile += kStep, buf ^= 1) {
+    if (at.in_tile()) {
 #pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      if (!at.in_tile(p)) continue;
-      const f32x4 d = softplus4(wide(rd[p]) + bias, a.softplus);
-      f32x4 x = wide(ru[p]);
-      if (!back) x *= d;
-      if (GATE && back) {
-        const f32x4 zz = wide(rz[p]);
-        x *= zz * sigmoid4(zz);
+      for (int p = 0; p < At::kPasses; ++p) {
+        const f32x4 d = softplus4(wide(dt.raw[p]) + bias, a.softplus);
+        f32x4 v = wide(x.raw[p]);
+        if (!BACK) v *= d;
+        if (GATE && BACK) {
+          const f32x4 zz = wide(z.raw[p]);
+          v *= zz * sigmoid4(zz);
+        }
+        f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
+        out[0] = f32x4{d[0], v[0], d[1], v[1]};
+        out[1] = f32x4{d[2], v[2], d[3], v[3]};
       }
-      f32x4* const out = reinterpret_cast<f32x4*>(&sx[buf][at.row(p)][at.c]);
-      out[0] = f32x4{d[0], x[0], d[1], x[1]};
-      out[1] = f32x4{d[2], x[2], d[3], x[3]};
     }
-    fetch(i + 1 < tiles ? tile + step : -1);
-    __syncthreads();
+    x.move(kStep);
+    dt.move(kStep);
+    if (GATE && BACK) z.move(kStep);
+    if (i + 1 < tiles) fetch(g.n - (tile + kStep) * kTile);
     const int n = min(kTile, g.n - tile * kTile);
-    if (!back) {
-      if (on) {
-        *reinterpret_cast<f32x4*>(ws.tiles + (size_t)(tile0 + tile) * state + place) = h;
-        if (SPLIT && w == 0) ws.before[(size_t)(tile0 + tile) * a.D + ch] = sum;
-      }
-      float part = 0.f;
-      const auto one = [&](int t) {
-        const f32x4 b = uniform4(M + (tile * kTile + t) * m.sl);
-        const float2 x = sx[buf][t][lane];
+    float part = 0.f;
+    const auto step = [&](f32x4 b, float2 v) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) h[s] = fmaf(exp2_fast(x.x * A2[s]), h[s], x.y * b[s]);
-        part += x.x;
-      };
-      if (n == kTile) {
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) one(t);
-      } else {
-        for (int t = 0; t < n; ++t) one(t);
+      for (int s = 0; s < 4; ++s) {
+        if (BACK) h[s] = exp2_fast(v.x * A2[s]) * fmaf(b[s], v.y, h[s]);
+        else h[s] = fmaf(exp2_fast(v.x * A2[s]), h[s], v.y * b[s]);
       }
-      sum += part;
+      if (!BACK) part += v.x;
+    };
+    if (!BACK && on) {
+      *reinterpret_cast<f32x4*>(ws.tiles + (size_t)(tile0 + tile) * state + place) = h;
+      if (SPLIT && w == 0) ws.before[(size_t)(tile0 + tile) * a.D + ch] = sum;
+    }
+    if (n == kTile) {
+      // Groups of rows in the walk's direction.
+      constexpr int Q = kTile / R;
+      Group<T> gm[2];
+      float2 v[2][R];
+      const int q0 = BACK ? Q - 1 : 0;
+      gm[0].load(M + q0 * R * m.sl, m.sl);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < R; ++j) v[0][j] = sx[buf][q0 * R + j][lane];
+      wait_reads();
+#pragma unroll
+      for (int k = 0; k < Q; ++k) {
+        const int now = k & 1, next = now ^ 1, q = BACK ? Q - 2 - k : k + 1;
+        if (k + 1 < Q) {
+          gm[next].load(M + q * R * m.sl, m.sl);
+#pragma unroll
+          for (int j = 0; j < R; ++j) v[next][j] = sx[buf][q * R + j][lane];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const int r = BACK ? R - 1 - j : j;
+          step(wide(gm[now].r[r]), v[now][r]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
-      const auto one = [&](int t) {
-        const f32x4 cc = uniform4(M + (tile * kTile + t) * m.sl);
-        const float2 x = sx[buf][t][lane];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) h[s] = exp2_fast(x.x * A2[s]) * fmaf(cc[s], x.y, h[s]);
-      };
-      if (n == kTile) {
-#pragma unroll
-        for (int t = kTile - 1; t >= 0; --t) one(t);
-      } else {
-        for (int t = n - 1; t >= 0; --t) one(t);
+      __syncthreads();
+      for (int j = 0; j < n; ++j) {
+        const int t = BACK ? n - 1 - j : j;
+        step(wide(uniform4(M + t * m.sl)), sx[buf][t][lane]);
       }
     }
+    M += kStep * kTile * m.sl;
+    sum += part;
   }
   if (SPLIT && on) {
-    *reinterpret_cast<f32x4*>((back ? ws.back : ws.ahead) + (size_t)id * state + place) = h;
-    if (!back && w == 0) ws.logs[(size_t)id * a.D + ch] = sum;
+    *reinterpret_cast<f32x4*>((BACK ? ws.back : ws.ahead) + (size_t)id * state + place) = h;
+    if (!BACK && w == 0) ws.logs[(size_t)id * a.D + ch] = sum;
   }
+}
+template <int NW, typename T, bool GATE, bool SPLIT>
+__global__ __launch_bounds__(64 * NW) void sums_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
+  __shared__ float2 sx[2][kTile][kCh];  // dt, and dt u or g
+  if (SPLIT && blockIdx.y) sums<NW, T, GATE, SPLIT, true>(a, pl, blocks_d, ws, sx);
+  else sums<NW, T, GATE, SPLIT, false>(a, pl, blocks_d, ws, sx);
 }
 
 // ---- sums over lanes ---------------------------------------------------------------------------
@@ -179,9 +195,14 @@ __device__ __forceinline__ float lanes_sum(float (&v)[16], int lane) {
 
 // ---- the walk back -------------------------------------------------------------------------------
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 template <int NW, typename T, bool GATE, bool SPLIT>
-__global__ __launch_bounds__(64 * NW) void back_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
-  constexpr int N = 4 * NW;
+__global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
+  constexpr int N = 4 * NW, R = group_rows<T>(), Q = kTile / R;
   using At = Spot<NW>;
   __shared__ float2 sx[kTile][kCh];                    // dt, dt u
   __shared__ float sg[kTile][kCh];                     // g
@@ -193,38 +214,42 @@ __global__ __launch_bounds__(64 * NW) void back_kernel(ScanArgs a, Plan pl, int 
   Segment g;
   if (!segment_of(pl, id, g)) return;
   const At at;
-  const int c = ch0 + at.c;
-  const bool has = c < a.D, on = ch < a.D;
+  const bool has = ch0 + at.c < a.D, on = ch < a.D;
+  const int c = has ? ch0 + at.c : a.D - 4;
   const size_t token = (size_t)g.batch * a.L + g.row;  // of the segment's first row
-  T* const du = static_cast<T*>(a.du) + token * a.D + c;
-  T* const ddt = static_cast<T*>(a.ddt) + token * a.D + c;
-  T* const dz = GATE ? static_cast<T*>(a.dz) + token * a.D + c : nullptr;
   const size_t tokens = (size_t)a.B * a.L;
-  float* const dB = ws.dBC + ((size_t)block * tokens + token) * N;
-  float* const dC = dB + (size_t)blocks_d * tokens * N;
   const size_t place = (size_t)ch * N + 4 * w, state = (size_t)a.D * N;
   float* const dA_to = ws.dA + (size_t)id * state + place;
   float* const dvec = ws.dvec + (size_t)id * 2 * a.D;
+  const int tiles = (g.n + kTile - 1) / kTile, begin = max(tiles - 1, 0) * kTile;
+  // Of the tile, from the segment's last on.
+  T* du = static_cast<T*>(a.du) + (token + begin) * a.D;
+  T* ddt = static_cast<T*>(a.ddt) + (token + begin) * a.D;
+  T* dz = static_cast<T*>(a.dz) + (GATE ? (token + begin) * a.D : 0);
+  float* dB = ws.dBC + ((size_t)block * tokens + token + begin) * N;
+  float* dC = dB + (size_t)blocks_d * tokens * N;
   if (g.seq < 0) {
-    for (int r = at.r; r < g.n; r += At::kRows) {
-      if (!has) break;
-      put4(du + (size_t)r * a.D, zero4());
-      put4(ddt + (size_t)r * a.D, zero4());
-      if (GATE) put4(dz + (size_t)r * a.D, zero4());
+    const size_t back = (size_t)begin * a.D;
+    for (int r = at.r; r < g.n && has; r += At::kRows) {
+      const size_t o = (size_t)r * a.D + c;
+      put4(du - back + o, zero4());
+      put4(ddt - back + o, zero4());
+      if (GATE) put4(dz - back + o, zero4());
     }
-    for (int i = threadIdx.x; i < g.n * N; i += 64 * NW) dB[i] = dC[i] = 0.f;
+    for (int i = threadIdx.x; i < g.n * N; i += 64 * NW) (dB - begin * N)[i] = (dC - begin * N)[i] = 0.f;
     if (on) *reinterpret_cast<f32x4*>(dA_to) = zero4();
     if (on && w == 0) dvec[ch] = dvec[a.D + ch] = 0.f;
     return;
   }
-  const T* const u = static_cast<const T*>(a.u.p) + g.batch * a.u.sb + g.row * a.u.sl + c;
-  const T* const dt = static_cast<const T*>(a.dt.p) + g.batch * a.dt.sb + g.row * a.dt.sl + c;
-  const T* const z = GATE ? static_cast<const T*>(a.z.p) + g.batch * a.z.sb + g.row * a.z.sl + c : nullptr;
-  const T* const dy = static_cast<const T*>(a.dy) + token * a.D + c;
-  const T* const Bm = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + g.row * a.Bm.sl + 4 * w;
-  const T* const Cm = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + g.row * a.Cm.sl + 4 * w;
-  const f32x4 bias = has && a.dt_bias ? get4(a.dt_bias + c) : zero4();
-  const f32x4 skip = has && a.skip ? get4(a.skip + c) : zero4();
+  const long long row = g.row + begin;
+  Feed<NW, T> u(a.u.p, g.batch * a.u.sb + row * a.u.sl, a.u.sl, at, c);
+  Feed<NW, T> dt(a.dt.p, g.batch * a.dt.sb + row * a.dt.sl, a.dt.sl, at, c);
+  Feed<NW, T> z(a.z.p, g.batch * a.z.sb + row * a.z.sl, a.z.sl, at, c);
+  Feed<NW, T> dy(a.dy, (long long)(token + begin) * a.D, a.D, at, c);
+  const T* Bt = static_cast<const T*>(a.Bm.p) + g.batch * a.Bm.sb + row * a.Bm.sl + 4 * w;  // of the tile
+  const T* Ct = static_cast<const T*>(a.Cm.p) + g.batch * a.Cm.sb + row * a.Cm.sl + 4 * w;
+  const f32x4 bias = a.dt_bias ? get4(a.dt_bias + c) : zero4();
+  const f32x4 skip = a.skip ? get4(a.skip + c) : zero4();
   f32x4 A2 = zero4(), G = zero4(), enter = zero4();
   if (on) {
     A2 = get4(a.A + place) * kLog2e;
@@ -233,142 +258,199 @@ __global__ __launch_bounds__(64 * NW) void back_kernel(ScanArgs a, Plan pl, int 
     if (g.last && a.dhT) G = get4(a.dhT + (size_t)g.seq * state + place);
   }
   const long long tile0 = first_tile(pl, g, id);
-  const int tiles = (g.n + kTile - 1) / kTile;
   f32x4 dA = zero4(), dskip = zero4(), dbias = zero4();
-
-  Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses], ry[At::kPasses];
-  f32x4 held = zero4();
+  f32x4 held = zero4();  // the next tile's state
   float since = 0.f;
   const auto fetch = [&](int tile) {
-#pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      const int r = tile * kTile + at.row(p);
-      ru[p] = rd[p] = rz[p] = ry[p] = narrow<T>(zero4());
-      if (has && at.in_tile(p) && tile >= 0 && r < g.n) {
-        ru[p] = raw4(u + r * a.u.sl);
-        rd[p] = raw4(dt + r * a.dt.sl);
-        ry[p] = raw4(dy + (size_t)r * a.D);
-        if (GATE) rz[p] = raw4(z + r * a.z.sl);
-      }
-    }
-    if (on && tile >= 0) {
+    const int n = g.n - tile * kTile;
+    u.fetch(at, c, n);
+    dt.fetch(at, c, n);
+    dy.fetch(at, c, n);
+    if (GATE) z.fetch(at, c, n);
+    if (on) {
       held = get4(ws.tiles + (size_t)(tile0 + tile) * state + place);
       if (SPLIT && !g.first) since = ws.before[(size_t)(tile0 + tile) * a.D + ch];
     }
   };
-  fetch(tiles - 1);
-  for (int tile = tiles - 1; tile >= 0; --tile) {
-    const int n = min(kTile, g.n - tile * kTile);
-    f32x4 uu[At::kPasses], dd[At::kPasses], slope[At::kPasses], zz[At::kPasses], yy[At::kPasses], gg[At::kPasses];
+  if (tiles > 0) fetch(tiles - 1);
+  // One tile; only the segment's last may be short.
+  const auto one = [&](int tile, auto full) {
+    constexpr bool kFull = decltype(full)::value;
+    const int n = kFull ? kTile : g.n - tile * kTile;
+    Raw4<T> ru[At::kPasses], rd[At::kPasses], rz[At::kPasses], ry[At::kPasses];
+    if (at.in_tile()) {
 #pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      if (!at.in_tile(p)) continue;
-      const int r = at.row(p);
-      uu[p] = wide(ru[p]);
-      zz[p] = wide(rz[p]);
-      yy[p] = wide(ry[p]);
-      const f32x4 raw = wide(rd[p]) + bias;
-      dd[p] = r < n ? softplus4(raw, a.softplus) : zero4();  // rows behind the segment change nothing
-      slope[p] = a.softplus ? sigmoid4(raw) : f32x4{1.f, 1.f, 1.f, 1.f};
-      const f32x4 x = dd[p] * uu[p];
-      gg[p] = yy[p];
-      if (GATE) gg[p] *= zz[p] * sigmoid4(zz[p]);
-      f32x4* const out = reinterpret_cast<f32x4*>(&sx[r][at.c]);
-      out[0] = f32x4{dd[p][0], x[0], dd[p][1], x[1]};
-      out[1] = f32x4{dd[p][2], x[2], dd[p][3], x[3]};
-      *reinterpret_cast<f32x4*>(&sg[r][at.c]) = gg[p];
+      for (int p = 0; p < At::kPasses; ++p) {
+        const int r = at.row(p);
+        ru[p] = u.raw[p];
+        rd[p] = dt.raw[p];
+        ry[p] = dy.raw[p];
+        if (GATE) rz[p] = z.raw[p];
+        f32x4 d = softplus4(wide(rd[p]) + bias, a.softplus), x = d * wide(ru[p]), gy = wide(ry[p]);
+        if (GATE) {
+          const f32x4 zz = wide(rz[p]);
+          gy *= zz * sigmoid4(zz);
+        }
+        // Channels behind D add nothing to the sums over channels, rows behind the segment
+        // change nothing.
+        if (!has || (!kFull && r >= n)) d = x = gy = zero4();
+        f32x4* const out = reinterpret_cast<f32x4*>(&sx[r][at.c]);
+        out[0] = f32x4{d[0], x[0], d[1], x[1]};
+        out[1] = f32x4{d[2], x[2], d[3], x[3]};
+        *reinterpret_cast<f32x4*>(&sg[r][at.c]) = gy;
+      }
     }
-    f32x4 h = held;
-    if (SPLIT && !g.first) {
+    float h[kTile + 1][4];  // states in front of the tile's tokens, and behind the last
 #pragma unroll
-      for (int s = 0; s < 4; ++s) h[s] = fmaf(exp2_fast(since * A2[s]), enter[s], h[s]);
-    }
-    fetch(tile - 1);
-    __syncthreads();
-    // Rows behind the segment: their B and C are taken as 0.
-    const auto rows4 = [&](const T* m, long long stride, int t) {
-      const f32x4 v = uniform4(m + (tile * kTile + min(t, n - 1)) * stride);
-      return t < n ? v : zero4();
-    };
-    float decay[kTile][4], kept[kTile][4];
-#pragma unroll
-    for (int t = 0; t < kTile; ++t) {
-      const f32x4 b = rows4(Bm, a.Bm.sl, t);
-      const float2 x = sx[t][lane];
+    for (int s = 0; s < 4; ++s) h[0][s] = SPLIT && !g.first ? fmaf(exp2_fast(since * A2[s]), enter[s], held[s]) : held[s];
+    u.move(-1);
+    dt.move(-1);
+    dy.move(-1);
+    if (GATE) z.move(-1);
+    if (tile > 0) fetch(tile - 1);
+    float decay[kTile][4];
+    float lB[kTile], lC[kTile];
+    f32x4 dAt = zero4();
+    const auto ahead = [&](int t, f32x4 b, float2 x) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         decay[t][s] = exp2_fast(x.x * A2[s]);
-        kept[t][s] = decay[t][s] * h[s];
-        h[s] = fmaf(x.y, b[s], kept[t][s]);
+        h[t + 1][s] = fmaf(decay[t][s], h[t][s], x.y * b[s]);
       }
-    }
-    float lB[kTile], lC[kTile];
-    f32x4 dAt = zero4();
-#pragma unroll
-    for (int t = kTile - 1; t >= 0; --t) {
-      const f32x4 b = rows4(Bm, a.Bm.sl, t), cc = rows4(Cm, a.Cm.sl, t);
-      const float2 x = sx[t][lane];
-      const float gy = sg[t][lane];
+    };
+    const auto back = [&](int t, f32x4 b, f32x4 cc, float2 x, float gy) {
       f32x4 vB, vC;
       float px = 0.f, pa = 0.f, py = 0.f;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const float ht = fmaf(x.y, b[s], kept[t][s]);
         G[s] = fmaf(cc[s], gy, G[s]);
-        vC[s] = ht * gy;
+        vC[s] = h[t + 1][s] * gy;
         vB[s] = G[s] * x.y;
         px = fmaf(G[s], b[s], px);
-        if (GATE) py = fmaf(ht, cc[s], py);
-        const float thr = G[s] * kept[t][s];
+        if (GATE) py = fmaf(h[t + 1][s], cc[s], py);
+        G[s] *= decay[t][s];
+        const float thr = G[s] * h[t][s];
         pa = fmaf(thr, A2[s], pa);
         dAt[s] = fmaf(thr, x.x, dAt[s]);
-        G[s] *= decay[t][s];
       }
       lB[t] = rows_sum(vB);
       lC[t] = rows_sum(vC);
       sdx[w][t][lane] = px;
       sda[w][t][lane] = pa;
       if (GATE) sy[w][t][lane] = py;
+    };
+    // Rows behind the segment are read at its last row and count as 0.
+    const auto load = [&](Group<T>& to, const T* rows, long long stride, int q) {
+      if (kFull) {
+        to.load(rows + q * R * stride, stride);
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          to.r[i] = uniform4(rows + min(q * R + i, n - 1) * stride);
+          if (q * R + i >= n) to.r[i] = Uniform4<T>{};
+        }
+      }
+    };
+    Group<T> gb[2], gc[2];
+    float2 x[2][R];
+    float gy[2][R];
+    load(gb[0], Bt, a.Bm.sl, 0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[0][i] = sx[i][lane];
+    wait_reads();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int now = q & 1, next = now ^ 1;
+      if (q + 1 < Q) {
+        load(gb[next], Bt, a.Bm.sl, q + 1);
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[next][i] = sx[(q + 1) * R + i][lane];
+      } else {
+        // The last group is the first of the way back.
+        load(gc[now], Ct, a.Cm.sl, q);
+#pragma unroll
+        for (int i = 0; i < R; ++i) gy[now][i] = sg[q * R + i][lane];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) ahead(q * R + i, wide(gb[now].r[i]), x[now][i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int q = Q - 1; q >= 0; --q) {
+      const int now = q & 1, next = now ^ 1;
+      if (q > 0) {
+        load(gb[next], Bt, a.Bm.sl, q - 1);
+        load(gc[next], Ct, a.Cm.sl, q - 1);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          x[next][i] = sx[(q - 1) * R + i][lane];
+          gy[next][i] = sg[(q - 1) * R + i][lane];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = R - 1; i >= 0; --i) back(q * R + i, wide(gb[now].r[i]), wide(gc[now].r[i]), x[now][i], gy[now][i]);
+      // (Formed here, or their 64 terms are kept in registers to the end of the tile.)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) asm volatile("" : "+v"(dAt[s]));
+      __builtin_amdgcn_sched_barrier(0);
     }
     dA += dAt;
     const float tB = lanes_sum(lB, lane), tC = lanes_sum(lC, lane);
-    if ((lane & 15) < n) {
-      const size_t o = (size_t)(tile * kTile + (lane & 15)) * N + 4 * w + (lane >> 4);
+    if (kFull || (lane & 15) < n) {
+      const int o = (lane & 15) * N + 4 * w + (lane >> 4);
       dB[o] = tB;
       dC[o] = tC;
     }
     __syncthreads();
+    if (at.in_tile()) {
 #pragma unroll
-    for (int p = 0; p < At::kPasses; ++p) {
-      if (!at.in_tile(p)) continue;
-      const int r = at.row(p);
-      f32x4 dx = zero4(), da = zero4(), yv = skip * uu[p];
+      for (int p = 0; p < At::kPasses; ++p) {
+        const int r = at.row(p);
+        const f32x4 uu = wide(ru[p]);
+        f32x4 dx = zero4(), da = zero4(), yv = skip * uu;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        dx += get4(&sdx[i][r][at.c]);
-        da += get4(&sda[i][r][at.c]);
-        if (GATE) yv += get4(&sy[i][r][at.c]);
-      }
-      if (!has || r >= n) continue;
-      const size_t o = (size_t)(tile * kTile + r) * a.D;
-      const f32x4 draw = (da * kLn2 + dx * uu[p]) * slope[p];
-      put4(du + o, dx * dd[p] + skip * gg[p]);
-      put4(ddt + o, draw);
-      dskip += gg[p] * uu[p];
-      dbias += draw;
-      if (GATE) {
-        const f32x4 sig = sigmoid4(zz[p]);
-        put4(dz + o, yy[p] * yv * (sig + zz[p] * sig * (1.f - sig)));
+        for (int i = 0; i < NW; ++i) {
+          dx += get4(&sdx[i][r][at.c]);
+          da += get4(&sda[i][r][at.c]);
+          if (GATE) yv += get4(&sy[i][r][at.c]);
+        }
+        if (!has || (!kFull && r >= n)) continue;
+        const f32x4 p0 = get4(&sx[r][at.c].x), p1 = get4(&sx[r][at.c + 2].x), gg = get4(&sg[r][at.c]);
+        const f32x4 d{p0[0], p0[2], p1[0], p1[2]};
+        f32x4 draw = da * kLn2 + dx * uu;
+        if (a.softplus) draw *= sigmoid4(wide(rd[p]) + bias);
+        const uint32_t o = offset_of<T>(r, a.D, c);
+        put4(const_cast<T*>(at_bytes(du, o)), dx * d + skip * gg);
+        put4(const_cast<T*>(at_bytes(ddt, o)), draw);
+        dskip += gg * uu;
+        dbias += draw;
+        if (GATE) {
+          const f32x4 zz = wide(rz[p]), sig = sigmoid4(zz);
+          put4(const_cast<T*>(at_bytes(dz, o)), wide(ry[p]) * yv * (sig + zz * sig * (1.f - sig)));
+        }
       }
     }
-  }
+    Bt -= kTile * a.Bm.sl;
+    Ct -= kTile * a.Cm.sl;
+    du -= kTile * (size_t)a.D;
+    ddt -= kTile * (size_t)a.D;
+    if (GATE) dz -= kTile * (size_t)a.D;
+    dB -= kTile * N;
+    dC -= kTile * N;
+    __syncthreads();  // sx and sg are the next tile's from here on
+  };
+  int tile = tiles - 1;
+  if (g.n % kTile) one(tile--, Flag<false>{});
+  for (; tile >= 0; --tile) one(tile, Flag<true>{});
   if (on) {
     *reinterpret_cast<f32x4*>(dA_to) = dA;
     if (g.first && a.dh0) *reinterpret_cast<f32x4*>(a.dh0 + (size_t)g.seq * state + place) = G;
   }
-  // The rows' parts of D's and the bias's gradients, through the waves' parts' place.
+  // The rows' parts of D's and the bias's gradients.
   constexpr int kSum = At::kRows < kTile ? At::kRows : kTile;
-  __syncthreads();
   if (at.r < kSum) {
     *reinterpret_cast<f32x4*>(&sg[at.r][at.c]) = dskip;
     *reinterpret_cast<f32x4*>(&sdx[0][at.r][at.c]) = dbias;
