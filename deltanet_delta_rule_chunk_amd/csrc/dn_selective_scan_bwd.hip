@@ -27,9 +27,11 @@
 namespace dn {
 namespace ssm {
 
+constexpr int kHalf = kTile / 2;
+
 struct BwdSpace {
-  float* tiles;   // [tile][D][N] state in front of a tile (cut sequences: from the segment's zero)
-  float* before;  // cut sequences: [tile][D] sum of dt from the segment's first token to the tile
+  float* tiles;   // [half tile][D][N] state in front of a half (cut sequences: from the segment's zero)
+  float* before;  // cut sequences: [half tile][D] sum of dt from the segment's first token to the half
   float* ahead;   // cut sequences: [seg][D][N] states in front of segments
   float* back;    // cut sequences: [seg][D][N] gradients of the states behind segments
   float* logs;    // cut sequences: [seg][D] sum of dt
@@ -110,10 +112,13 @@ __device__ __forceinline__ void sums(const ScanArgs& a, const Plan& pl, int bloc
       }
       if (!BACK) part += v.x;
     };
-    if (!BACK && on) {
-      *reinterpret_cast<f32x4*>(ws.tiles + (size_t)(tile0 + tile) * state + place) = h;
-      if (SPLIT && w == 0) ws.before[(size_t)(tile0 + tile) * a.D + ch] = sum;
-    }
+    const auto keep = [&](int half) {
+      if (BACK || !on) return;
+      const size_t at_ = (size_t)(tile0 + tile) * 2 + half;
+      *reinterpret_cast<f32x4*>(ws.tiles + at_ * state + place) = h;
+      if (SPLIT && w == 0) ws.before[at_ * a.D + ch] = sum + part;
+    };
+    keep(0);
     if (n == kTile) {
       // Groups of rows in the walk's direction.
       constexpr int Q = kTile / R;
@@ -134,6 +139,7 @@ __device__ __forceinline__ void sums(const ScanArgs& a, const Plan& pl, int bloc
           for (int j = 0; j < R; ++j) v[next][j] = sx[buf][q * R + j][lane];
         }
         __builtin_amdgcn_sched_barrier(0);
+        if (k == Q / 2) keep(1);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
           const int r = BACK ? R - 1 - j : j;
@@ -145,6 +151,7 @@ __device__ __forceinline__ void sums(const ScanArgs& a, const Plan& pl, int bloc
       __syncthreads();
       for (int j = 0; j < n; ++j) {
         const int t = BACK ? n - 1 - j : j;
+        if (t == kHalf) keep(1);
         step(wide(uniform4(M + t * m.sl)), sx[buf][t][lane]);
       }
     }
@@ -181,16 +188,15 @@ __device__ __forceinline__ float fold(float a, float b, bool bit) {
   const float keep = bit ? b : a, send = bit ? a : b;
   return keep + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(send), CTRL, 0xf, 0xf, true));
 }
-// 16 values per lane: lane i of 16 gets the sum of v[i] over the 16.
-__device__ __forceinline__ float lanes_sum(float (&v)[16], int lane) {
-  constexpr int kMirror16 = 0x140, kMirror8 = 0x141, kMirror4 = 0x1b, kMirror2 = 0xb1;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fold<kMirror16>(v[i], v[i + 8], lane & 8);
+// 8 values per lane: lanes i and i + 8 of 16 get the sum of v[i] over the 16.
+__device__ __forceinline__ float lanes_sum(float (&v)[8], int lane) {
+  constexpr int kMirror8 = 0x141, kMirror4 = 0x1b, kMirror2 = 0xb1, kTurn8 = 0x128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = fold<kMirror8>(v[i], v[i + 4], lane & 4);
 #pragma unroll
   for (int i = 0; i < 2; ++i) v[i] = fold<kMirror4>(v[i], v[i + 2], lane & 2);
-  return fold<kMirror2>(v[0], v[1], lane & 1);
+  const float x = fold<kMirror2>(v[0], v[1], lane & 1);
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), kTurn8, 0xf, 0xf, true));
 }
 
 // ---- the walk back -------------------------------------------------------------------------------
@@ -202,7 +208,7 @@ struct Flag {
 
 template <int NW, typename T, bool GATE, bool SPLIT>
 __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
-  constexpr int N = 4 * NW, R = group_rows<T>(), Q = kTile / R;
+  constexpr int N = 4 * NW, R = group_rows<T>(), Q = kHalf / R;
   using At = Spot<NW>;
   __shared__ float2 sx[kTile][kCh];                    // dt, dt u
   __shared__ float sg[kTile][kCh];                     // g
@@ -259,8 +265,8 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
   }
   const long long tile0 = first_tile(pl, g, id);
   f32x4 dA = zero4(), dskip = zero4(), dbias = zero4();
-  f32x4 held = zero4();  // the next tile's state
-  float since = 0.f;
+  f32x4 held[2] = {zero4(), zero4()};  // the next tile's states
+  float since[2] = {0.f, 0.f};
   const auto fetch = [&](int tile) {
     const int n = g.n - tile * kTile;
     u.fetch(at, c, n);
@@ -268,8 +274,13 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
     dy.fetch(at, c, n);
     if (GATE) z.fetch(at, c, n);
     if (on) {
-      held = get4(ws.tiles + (size_t)(tile0 + tile) * state + place);
-      if (SPLIT && !g.first) since = ws.before[(size_t)(tile0 + tile) * a.D + ch];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i * kHalf >= n) break;
+        const size_t at_ = (size_t)(tile0 + tile) * 2 + i;
+        held[i] = get4(ws.tiles + at_ * state + place);
+        if (SPLIT && !g.first) since[i] = ws.before[at_ * a.D + ch];
+      }
     }
   };
   if (tiles > 0) fetch(tiles - 1);
@@ -300,110 +311,122 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
         *reinterpret_cast<f32x4*>(&sg[r][at.c]) = gy;
       }
     }
-    float h[kTile + 1][4];  // states in front of the tile's tokens, and behind the last
+    f32x4 start[2];  // states in front of the halves
 #pragma unroll
-    for (int s = 0; s < 4; ++s) h[0][s] = SPLIT && !g.first ? fmaf(exp2_fast(since * A2[s]), enter[s], held[s]) : held[s];
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        start[i][s] = SPLIT && !g.first ? fmaf(exp2_fast(since[i] * A2[s]), enter[s], held[i][s]) : held[i][s];
     u.move(-1);
     dt.move(-1);
     dy.move(-1);
     if (GATE) z.move(-1);
     if (tile > 0) fetch(tile - 1);
-    float decay[kTile][4];
-    float lB[kTile], lC[kTile];
-    f32x4 dAt = zero4();
-    const auto ahead = [&](int t, f32x4 b, float2 x) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        decay[t][s] = exp2_fast(x.x * A2[s]);
-        h[t + 1][s] = fmaf(decay[t][s], h[t][s], x.y * b[s]);
-      }
-    };
-    const auto back = [&](int t, f32x4 b, f32x4 cc, float2 x, float gy) {
-      f32x4 vB, vC;
-      float px = 0.f, pa = 0.f, py = 0.f;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        G[s] = fmaf(cc[s], gy, G[s]);
-        vC[s] = h[t + 1][s] * gy;
-        vB[s] = G[s] * x.y;
-        px = fmaf(G[s], b[s], px);
-        if (GATE) py = fmaf(h[t + 1][s], cc[s], py);
-        G[s] *= decay[t][s];
-        const float thr = G[s] * h[t][s];
-        pa = fmaf(thr, A2[s], pa);
-        dAt[s] = fmaf(thr, x.x, dAt[s]);
-      }
-      lB[t] = rows_sum(vB);
-      lC[t] = rows_sum(vC);
-      sdx[w][t][lane] = px;
-      sda[w][t][lane] = pa;
-      if (GATE) sy[w][t][lane] = py;
-    };
-    // Rows behind the segment are read at its last row and count as 0.
-    const auto load = [&](Group<T>& to, const T* rows, long long stride, int q) {
-      if (kFull) {
-        to.load(rows + q * R * stride, stride);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          to.r[i] = uniform4(rows + min(q * R + i, n - 1) * stride);
-          if (q * R + i >= n) to.r[i] = Uniform4<T>{};
-        }
-      }
-    };
-    Group<T> gb[2], gc[2];
-    float2 x[2][R];
-    float gy[2][R];
-    load(gb[0], Bt, a.Bm.sl, 0);
     __syncthreads();
+    f32x4 dAt = zero4();
 #pragma unroll
-    for (int i = 0; i < R; ++i) x[0][i] = sx[i][lane];
-    wait_reads();
+    for (int half = 1; half >= 0; --half) {
+      const int t0 = half * kHalf;
+      if (!kFull && t0 >= n) continue;
+      // Rows behind the segment are read at its last row and count as 0.
+      const auto load = [&](Group<T>& to, const T* rows, long long stride, int q) {
+        if (kFull) {
+          to.load(rows + (t0 + q * R) * stride, stride);
+        } else {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int now = q & 1, next = now ^ 1;
-      if (q + 1 < Q) {
-        load(gb[next], Bt, a.Bm.sl, q + 1);
-#pragma unroll
-        for (int i = 0; i < R; ++i) x[next][i] = sx[(q + 1) * R + i][lane];
-      } else {
-        // The last group is the first of the way back.
-        load(gc[now], Ct, a.Cm.sl, q);
-#pragma unroll
-        for (int i = 0; i < R; ++i) gy[now][i] = sg[q * R + i][lane];
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < R; ++i) ahead(q * R + i, wide(gb[now].r[i]), x[now][i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int q = Q - 1; q >= 0; --q) {
-      const int now = q & 1, next = now ^ 1;
-      if (q > 0) {
-        load(gb[next], Bt, a.Bm.sl, q - 1);
-        load(gc[next], Ct, a.Cm.sl, q - 1);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          x[next][i] = sx[(q - 1) * R + i][lane];
-          gy[next][i] = sg[(q - 1) * R + i][lane];
+          for (int i = 0; i < R; ++i) {
+            const int t = t0 + q * R + i;
+            to.r[i] = uniform4(rows + min(t, n - 1) * stride);
+            if (t >= n) to.r[i] = Uniform4<T>{};
+          }
         }
+      };
+      float h[kHalf + 1][4], decay[kHalf][4];  // states in front of the tokens and behind the last
+      float lB[kHalf], lC[kHalf];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) h[0][s] = start[half][s];
+      const auto ahead = [&](int t, f32x4 b, float2 x) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          decay[t][s] = exp2_fast(x.x * A2[s]);
+          h[t + 1][s] = fmaf(decay[t][s], h[t][s], x.y * b[s]);
+        }
+      };
+      const auto back = [&](int t, f32x4 b, f32x4 cc, float2 x, float gy) {
+        f32x4 vB, vC;
+        float px = 0.f, pa = 0.f, py = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          G[s] = fmaf(cc[s], gy, G[s]);
+          vC[s] = h[t + 1][s] * gy;
+          vB[s] = G[s] * x.y;
+          px = fmaf(G[s], b[s], px);
+          if (GATE) py = fmaf(h[t + 1][s], cc[s], py);
+          G[s] *= decay[t][s];
+          const float thr = G[s] * h[t][s];
+          pa = fmaf(thr, A2[s], pa);
+          dAt[s] = fmaf(thr, x.x, dAt[s]);
+        }
+        lB[t] = rows_sum(vB);
+        lC[t] = rows_sum(vC);
+        sdx[w][t0 + t][lane] = px;
+        sda[w][t0 + t][lane] = pa;
+        if (GATE) sy[w][t0 + t][lane] = py;
+      };
+      Group<T> gb[2], gc[2];
+      float2 x[2][R];
+      float gy[2][R];
+      load(gb[0], Bt, a.Bm.sl, 0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) x[0][i] = sx[t0 + i][lane];
+      wait_reads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int now = q & 1, next = now ^ 1;
+        if (q + 1 < Q) {
+          load(gb[next], Bt, a.Bm.sl, q + 1);
+#pragma unroll
+          for (int i = 0; i < R; ++i) x[next][i] = sx[t0 + (q + 1) * R + i][lane];
+        } else {
+          // The last group is the first of the way back.
+          load(gc[now], Ct, a.Cm.sl, q);
+#pragma unroll
+          for (int i = 0; i < R; ++i) gy[now][i] = sg[t0 + q * R + i][lane];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) ahead(q * R + i, wide(gb[now].r[i]), x[now][i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = R - 1; i >= 0; --i) back(q * R + i, wide(gb[now].r[i]), wide(gc[now].r[i]), x[now][i], gy[now][i]);
-      // (Formed here, or their 64 terms are kept in registers to the end of the tile.)
+      for (int q = Q - 1; q >= 0; --q) {
+        const int now = q & 1, next = now ^ 1;
+        if (q > 0) {
+          load(gb[next], Bt, a.Bm.sl, q - 1);
+          load(gc[next], Ct, a.Cm.sl, q - 1);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) asm volatile("" : "+v"(dAt[s]));
-      __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < R; ++i) {
+            x[next][i] = sx[t0 + (q - 1) * R + i][lane];
+            gy[next][i] = sg[t0 + (q - 1) * R + i][lane];
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i) back(q * R + i, wide(gb[now].r[i]), wide(gc[now].r[i]), x[now][i], gy[now][i]);
+        // (Formed here, or their terms are kept in registers to the end of the tile.)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) asm volatile("" : "+v"(dAt[s]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const float tB = lanes_sum(lB, lane), tC = lanes_sum(lC, lane);
+      const int t = t0 + (lane & 7);
+      if ((lane & 8) == 0 && (kFull || t < n)) {
+        const int o = t * N + 4 * w + (lane >> 4);
+        dB[o] = tB;
+        dC[o] = tC;
+      }
     }
     dA += dAt;
-    const float tB = lanes_sum(lB, lane), tC = lanes_sum(lC, lane);
-    if (kFull || (lane & 15) < n) {
-      const int o = (lane & 15) * N + 4 * w + (lane >> 4);
-      dB[o] = tB;
-      dC[o] = tC;
-    }
     __syncthreads();
     if (at.in_tile()) {
 #pragma unroll
@@ -440,7 +463,7 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
     if (GATE) dz -= kTile * (size_t)a.D;
     dB -= kTile * N;
     dC -= kTile * N;
-    __syncthreads();  // sx and sg are the next tile's from here on
+    // (What a thread reads of sx and sg here it wrote itself, so the next tile's may follow.)
   };
   int tile = tiles - 1;
   if (g.n % kTile) one(tile--, Flag<false>{});
@@ -451,6 +474,7 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
   }
   // The rows' parts of D's and the bias's gradients.
   constexpr int kSum = At::kRows < kTile ? At::kRows : kTile;
+  __syncthreads();
   if (at.r < kSum) {
     *reinterpret_cast<f32x4*>(&sg[at.r][at.c]) = dskip;
     *reinterpret_cast<f32x4*>(&sdx[0][at.r][at.c]) = dbias;
@@ -511,7 +535,7 @@ static size_t up(size_t n) { return (n + 3) / 4 * 4; }  // floats, to 16 bytes
 // Places the parts in a workspace; returns its size in bytes (ws may be null).
 static size_t place(int B, int L, int D, int N, bool packed, int n_seq, const Sizes& s, void* ws, BwdSpace* out) {
   const size_t table = table_bytes(packed, n_seq, s), state = (size_t)D * N, tokens = (size_t)B * L;
-  const size_t tiles = tokens / kTile + s.segments + 1, seg = s.segments;
+  const size_t tiles = 2 * (tokens / kTile + s.segments + 1), seg = s.segments;
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + table);
   size_t at = 0;
   const auto take = [&](size_t n) {
