@@ -927,18 +927,28 @@ def _check_optional(t, name, shape, dtype, device):
         _check(t, name, shape, dtype, device)
 
 
+def _dense(t, shape, dtype, device) -> bool:
+    """Whether an optional tensor is what a call takes as it lies (None: it is)."""
+    return t is None or (t.shape == shape and t.dtype is dtype and t.device == device
+                         and t.is_contiguous())
+
+
 def _conv_setup(x, weight, bias, state0, cu_seqlens, dims):
-    """Checks shared by the short convolution's calls; (sequences, K)."""
-    if x.dim() != dims or weight.dim() != 2:
+    """Checks shared by the short convolution's calls; (sequences, K, x's strides)."""
+    xs, ws, strides = x.shape, weight.shape, x.stride()
+    if len(xs) != dims or len(ws) != 2:
         raise ValueError(f"x must have {dims} dimensions and weight 2 "
-                         f"(got {tuple(x.shape)}, {tuple(weight.shape)})")
-    dev, dt, D, K = x.device, x.dtype, x.shape[-1], weight.shape[1]
-    _check_rows(x, "x", x.shape, dt, dev)
-    _check(weight, "weight", (D, K), torch.float32, dev)
-    _check_optional(bias, "bias", (D,), torch.float32, dev)
-    n = _check_cu(cu_seqlens, x.shape[0], dev)
-    _check_optional(state0, "state0", (n, K - 1, D), dt, dev)
-    return n, K
+                         f"(got {tuple(xs)}, {tuple(ws)})")
+    dev, dt, D, K = x.device, x.dtype, xs[-1], ws[1]
+    n = xs[0] if cu_seqlens is None else _check_cu(cu_seqlens, xs[0], dev)
+    # One look at everything; the reasons only where something is wrong.
+    if not (x.is_cuda and strides[-1] == 1 and _dense(weight, (D, K), torch.float32, dev)
+            and _dense(bias, (D,), torch.float32, dev) and _dense(state0, (n, K - 1, D), dt, dev)):
+        _check_rows(x, "x", xs, dt, dev)
+        _check(weight, "weight", (D, K), torch.float32, dev)
+        _check_optional(bias, "bias", (D,), torch.float32, dev)
+        _check_optional(state0, "state0", (n, K - 1, D), dt, dev)
+    return n, K, _ll_array(*strides[:-1])
 
 
 def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -954,7 +964,7 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     none of them holds become zeros.  Returns ``(y, state)``: y dense, state the
     rows kept behind each sequence (None when ``want_state`` is False)."""
     lib = _lib or load()
-    n, K = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
+    n, K, strides = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
     dev, dt, (B, L, D) = x.device, x.dtype, x.shape
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -965,7 +975,7 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     else:
         _check(y, "y", (B, L, D), dt, dev)
     state = _alloc((n, K - 1, D), dt, dev, stream) if want_state else None
-    st = lib.deltanet_short_conv_fwd(x.data_ptr(), _ll_array(*x.stride()[:2]), weight.data_ptr(),
+    st = lib.deltanet_short_conv_fwd(x.data_ptr(), strides, weight.data_ptr(),
                                      _ptr(bias), _ptr(state0), _ptr(cu_seqlens), y.data_ptr(),
                                      _ptr(state), B, L, D, K, n, int(silu), _code(dt),
                                      _stream(dev, stream))
@@ -990,7 +1000,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     ``want_dstate0`` is False) in x's dtype, dweight and dbias (None without a
     bias) fp32."""
     lib = _lib or load()
-    n, K = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
+    n, K, strides = _conv_setup(x, weight, bias, state0, cu_seqlens, 3)
     dev, dt, (B, L, D) = x.device, x.dtype, x.shape
     _check(dy, "dy", (B, L, D), dt, dev)
     _check_optional(dstate, "dstate", (n, K - 1, D), dt, dev)
@@ -1003,7 +1013,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     db = None if bias is None else _alloc((D,), torch.float32, dev, stream)
     ds = _alloc((n, K - 1, D), dt, dev, stream) if want_dstate0 else None
     keep, ws, ws_bytes = _workspace(workspace, _conv_bwd_workspace_bytes(B, L, D, K), dev, stream)
-    st = lib.deltanet_short_conv_bwd(x.data_ptr(), _ll_array(*x.stride()[:2]), weight.data_ptr(),
+    st = lib.deltanet_short_conv_bwd(x.data_ptr(), strides, weight.data_ptr(),
                                      _ptr(bias), _ptr(state0), _ptr(cu_seqlens), dy.data_ptr(),
                                      _ptr(dstate), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds),
                                      B, L, D, K, n, int(silu), _code(dt), ws, ws_bytes,
@@ -1045,7 +1055,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
     """One token of the short convolution (``deltanet_short_conv_step``): x ``[B,D]``
     (rows at any stride), state ``[B,K-1,D]`` moved on in place; returns y ``[B,D]``."""
     lib = _lib or load()
-    _, K = _conv_setup(x, weight, bias, state, None, 2)
+    _, K, strides = _conv_setup(x, weight, bias, state, None, 2)
     dev, dt, (B, D) = x.device, x.dtype, x.shape
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -1054,7 +1064,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
         y = _alloc((B, D), dt, dev, stream)
     else:
         _check(y, "y", (B, D), dt, dev)
-    st = lib.deltanet_short_conv_step(x.data_ptr(), _ll_array(x.stride(0)), weight.data_ptr(),
+    st = lib.deltanet_short_conv_step(x.data_ptr(), strides, weight.data_ptr(),
                                       _ptr(bias), state.data_ptr(), y.data_ptr(), B, D, K,
                                       int(silu), _code(dt), _stream(dev, stream))
     if st != DN_OK:
@@ -1064,25 +1074,31 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
 
 def _scan_setup(u, dt, A, B, C, D, z, dt_bias, state, cu_seqlens, dims):
     """Checks shared by the selective scan's calls; (sequences, N, leading arguments)."""
-    if u.dim() != dims or A.dim() != 2:
-        raise ValueError(f"u must have {dims} dimensions and A 2 "
-                         f"(got {tuple(u.shape)}, {tuple(A.shape)})")
-    dev, ty, width, N = u.device, u.dtype, u.shape[-1], A.shape[1]
-    few = (*u.shape[:-1], N)
-    _check_rows(u, "u", u.shape, ty, dev)
-    _check_rows(dt, "dt", u.shape, ty, dev)
-    _check_rows(B, "B", few, ty, dev)
-    _check_rows(C, "C", few, ty, dev)
-    if z is not None:
-        _check_rows(z, "z", u.shape, ty, dev)
-    _check(A, "A", (width, N), torch.float32, dev)
-    _check_optional(D, "D", (width,), torch.float32, dev)
-    _check_optional(dt_bias, "dt_bias", (width,), torch.float32, dev)
-    n = _check_cu(cu_seqlens, u.shape[0], dev)
-    _check_optional(state, "the state", (n, width, N), torch.float32, dev)
-    gate = u if z is None else z
-    strides = _ll_array(*u.stride()[:-1], *dt.stride()[:-1], *B.stride()[:-1], *C.stride()[:-1],
-                        *gate.stride()[:-1])
+    us, As = u.shape, A.shape
+    if len(us) != dims or len(As) != 2:
+        raise ValueError(f"u must have {dims} dimensions and A 2 (got {tuple(us)}, {tuple(As)})")
+    dev, ty, width, N = u.device, u.dtype, us[-1], As[1]
+    n = us[0] if cu_seqlens is None else _check_cu(cu_seqlens, us[0], dev)
+    few, f32 = (*us[:-1], N), torch.float32
+    s_u, s_dt, s_B, s_C = u.stride(), dt.stride(), B.stride(), C.stride()
+    s_z = s_u if z is None else z.stride()
+    # One look at everything; the reasons only where something is wrong.
+    if not (u.is_cuda and dt.shape == us and B.shape == few and C.shape == few and dt.dtype is ty
+            and B.dtype is ty and C.dtype is ty and dt.device == dev and B.device == dev
+            and C.device == dev and s_u[-1] == 1 and s_dt[-1] == 1 and s_B[-1] == 1
+            and s_C[-1] == 1 and s_z[-1] == 1
+            and (z is None or (z.shape == us and z.dtype is ty and z.device == dev))
+            and _dense(A, (width, N), f32, dev) and _dense(D, (width,), f32, dev)
+            and _dense(dt_bias, (width,), f32, dev) and _dense(state, (n, width, N), f32, dev)):
+        for t, name, shape in ((u, "u", us), (dt, "dt", us), (B, "B", few), (C, "C", few),
+                               (z, "z", us)):
+            if t is not None:
+                _check_rows(t, name, shape, ty, dev)
+        _check(A, "A", (width, N), f32, dev)
+        _check_optional(D, "D", (width,), f32, dev)
+        _check_optional(dt_bias, "dt_bias", (width,), f32, dev)
+        _check_optional(state, "the state", (n, width, N), f32, dev)
+    strides = _ll_array(*s_u[:-1], *s_dt[:-1], *s_B[:-1], *s_C[:-1], *s_z[:-1])
     return n, N, (u.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(z), strides,
                   A.data_ptr(), _ptr(D), _ptr(dt_bias))
 
@@ -1241,16 +1257,15 @@ def _add_norm(x, residual, weight, eps, total, y, out8, stream):
     dev, dt, shape = x.device, x.dtype, x.shape
     if not shape:
         raise ValueError("x must have rows")
-    D = shape[-1]
-    _check(x, "x", shape, dt, dev)
-    rdt = dt
-    if residual is not None:
-        rdt = residual.dtype
-        _check(residual, "residual", shape, rdt, dev)
-    elif total is not None:
+    D, rdt = shape[-1], dt if residual is None else residual.dtype
+    if residual is None and total is not None:
         raise ValueError("total is only written with a residual")
-    _check_optional(weight, "weight", (D,), torch.float32, dev)
-    _check_optional(total, "total", shape, rdt, dev)
+    if not (x.is_cuda and x.is_contiguous() and _dense(residual, shape, rdt, dev)
+            and _dense(weight, (D,), torch.float32, dev) and _dense(total, shape, rdt, dev)):
+        _check(x, "x", shape, dt, dev)
+        _check_optional(residual, "residual", shape, rdt, dev)
+        _check_optional(weight, "weight", (D,), torch.float32, dev)
+        _check_optional(total, "total", shape, rdt, dev)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return _add_norm(x, residual, weight, eps, total, y, out8, stream)

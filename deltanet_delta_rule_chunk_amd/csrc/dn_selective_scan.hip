@@ -256,8 +256,12 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
   if (to) *reinterpret_cast<f32x4*>(to + (size_t)ch * N + 4 * w) = h;
 }
 
+// 1024 workgroups need no cut (16 x 2048 tokens of 2048 channels, 512 of them: 445 us uncut,
+// 405 cut; 32 x 1024, 1024 of them: 294 and 385).  With one, 4096: 65536 tokens of 4096 channels
+// take 1974 us with 1024, 1765 with 1536, 1710 with 2048, 1630 with 4096, 1604 with 8192, which
+// costs shorter sequences as much; pieces below 64 tokens gain nothing.
 static Sizes forward_sizes(int B, int L, int D, bool packed, int n_seq) {
-  return sizes_of(packed, B, L, n_seq, D, 512, 1024, 64);
+  return sizes_of(packed, B, L, n_seq, D, 1024, 4096, 64);
 }
 
 template <int NW, typename T, bool GATE>

@@ -216,16 +216,20 @@ __device__ __forceinline__ Vals<BV> through(const Vals<BV>& p, const Vals<BV>& d
   return q;
 }
 
-// A run of `len` rows per thread, walked K - 1 rows further for the q that reach
-// back into it.  dw and db of a run go to `parts` [run][K + 1][D].  The workgroups
-// behind `run_blocks` form the gradients of the kept rows in front of sequences.
+constexpr int WAVES = NT / 64;
+
+// A wave takes 64 groups of channels and a run of `len` rows, walked K - 1 rows
+// further for the q that reach back into it; the workgroup's waves take runs that
+// follow each other and add up dw and db, which go to `parts` [workgroup's runs][K + 1][D].
+// The workgroups behind `run_blocks` form the gradients of the kept rows in front of
+// sequences.
 template <int K, typename T>
-__global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, int per_row, long long run_items,
+__global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, int per_row, long long runs, int blocks_d,
                                                       unsigned run_blocks, float* parts) {
+  __shared__ f32x4 sums[WAVES][K + 1][64];
   const int groups = a.D / BV;
-  const bool edge = blockIdx.x >= run_blocks;
-  const long long item = (long long)(blockIdx.x - (edge ? run_blocks : 0)) * NT + threadIdx.x;
-  if (edge) {
+  if (blockIdx.x >= run_blocks) {
+    const long long item = (long long)(blockIdx.x - run_blocks) * NT + threadIdx.x;
     if (item >= (long long)a.n_seq * groups) return;
     const int seq = (int)(item / groups), c = (int)(item - (long long)seq * groups) * BV;
     Cursor s(nullptr, a.n_seq, a.L, a.cu ? 0 : seq, 0);
@@ -261,11 +265,14 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
       store<BV>(static_cast<T*>(a.dstate0) + ((size_t)seq * (K - 1) + j) * a.D + c, narrowed<BV, T>(d[j]));
     return;
   }
-  if (item >= run_items) return;
-  const long long run = item / groups;
-  const int c = (int)(item - run * groups) * BV;
-  const int b = (int)(run / per_row), t0 = (int)(run - (long long)b * per_row) * len, t1 = min(t0 + len, a.L);
-  const int stop = min(t1 + K - 1, a.L);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long set = blockIdx.x / blocks_d, run = set * WAVES + wave;
+  const int group = (int)(blockIdx.x - set * blocks_d) * 64 + lane;
+  const bool on = group < groups && run < runs;
+  const int c = (group < groups ? group : groups - 1) * BV;
+  const long long r0 = run < runs ? run : 0;
+  const int b = (int)(r0 / per_row), t0 = (int)(r0 - (long long)b * per_row) * len, t1 = on ? min(t0 + len, a.L) : t0;
+  const int stop = min(t0 + len + K - 1, a.L);  // (not below t0 + 1)
   const T* const x = static_cast<const T*>(a.x.p) + b * a.x.sb + c;
   const T* const dy = static_cast<const T*>(a.dy) + (size_t)b * a.L * a.D + c;
   T* const dx = static_cast<T*>(a.dx) + (size_t)b * a.L * a.D + c;
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
     ry[i] = load<BV>(dy + (size_t)t * a.D);
   }
   // Row t forms q_t and finishes dx of row t - K + 1.
-  for (int base = t0; base < t1 + K - 1; base += U) {
+  for (int base = t0; base < t1 + K - 1 && t1 > t0; base += U) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int t = base + i;
@@ -330,13 +337,20 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
       }
     }
   }
-  float* const to = parts + (size_t)run * (K + 1) * a.D + c;
 #pragma unroll
-  for (int j = 0; j < K; ++j) *reinterpret_cast<f32x4*>(to + (size_t)j * a.D) = dw[j].v[0];
-  *reinterpret_cast<f32x4*>(to + (size_t)K * a.D) = db.v[0];
+  for (int j = 0; j < K; ++j) sums[wave][j][lane] = dw[j].v[0];
+  sums[wave][K][lane] = db.v[0];
+  __syncthreads();
+  if (group >= groups) return;
+  for (int j = wave; j < K + 1; j += WAVES) {
+    f32x4 s = sums[0][j][lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) s += sums[i][j][lane];
+    *reinterpret_cast<f32x4*>(parts + ((size_t)set * (K + 1) + j) * a.D + c) = s;
+  }
 }
 
-// The runs' parts [run][K + 1][D] added in order, 16 columns per workgroup.
+// The parts [runs][K + 1][D] added in order, 16 columns per workgroup.
 static __global__ __launch_bounds__(NT) void weight_kernel(const float* parts, int runs, int D, int K, float* dweight, float* dbias) {
   __shared__ double red[16][17];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
@@ -383,55 +397,61 @@ __global__ __launch_bounds__(NT) void step_kernel(ShortConvArgs a, long long ite
 
 // ---- launches -------------------------------------------------------------------------
 
-constexpr int kRun = 16;
+// Rows per run of the forward: each re-reads K - 1 rows.
+constexpr int kRun = 16, kShortRun = 8;
 
 static unsigned blocks_for(long long items) { return (unsigned)((items + NT - 1) / NT); }
 
-template <int K, typename T>
-static hipError_t forward(const ShortConvArgs& a) {
+template <int K, int R, typename T>
+static hipError_t forward_run(const ShortConvArgs& a) {
   constexpr int V = 16 / sizeof(T);
-  const int per_row = (int)(((long long)a.L + kRun - 1) / kRun);
+  const int per_row = (int)(((long long)a.L + R - 1) / R);
   const long long items = (long long)a.B * per_row * (a.D / V), kept = a.state ? (long long)a.n_seq * (K - 1) * (a.D / V) : 0;
   const unsigned n = blocks_for(items), m = blocks_for(kept);
   if (n + m == 0) return hipSuccess;
   prof_mark(kSlotShortConv, false, a.stream);
-  hipLaunchKernelGGL((forward_kernel<K, V, kRun, T>), dim3(n + m), dim3(NT), 0, a.stream, a, per_row, items, n);
+  hipLaunchKernelGGL((forward_kernel<K, V, R, T>), dim3(n + m), dim3(NT), 0, a.stream, a, per_row, items, n);
   const hipError_t e = hipGetLastError();
   prof_mark(kSlotShortConv, true, a.stream);
   return e;
 }
+template <int K, typename T>
+static hipError_t forward(const ShortConvArgs& a) {
+  const bool few = (long long)a.B * a.L * a.D * (int)sizeof(T) < kRun * 16LL * NT * 1536;
+  return few ? forward_run<K, kShortRun, T>(a) : forward_run<K, kRun, T>(a);
+}
 
-// Rows per run of the backward: about 1024 threads for every CU, runs of 16 to 256 rows.
+// Rows per run of the backward: 8192 waves, runs of 16 to 64 rows.
 struct Runs {
-  int len, per_row;
-  long long n;
+  int len, per_row, blocks_d;
+  long long n, sets;  // runs, and sets of them that a workgroup adds up
 };
 static Runs backward_runs(int B, int L, int D) {
-  const long long groups = D / BV, want = 262144 / groups + 1;
-  long long len = ((long long)B * L + want - 1) / want;
-  len = len < 16 ? 16 : len > 256 ? 256 : len;
   Runs r;
+  r.blocks_d = (D / BV + 63) / 64;
+  long long len = (long long)B * L * r.blocks_d / 8192;
+  len = len < 16 ? 16 : len > 64 ? 64 : len;
   r.len = (int)len;
   r.per_row = (int)((L + len - 1) / len);
   r.n = (long long)B * r.per_row;
+  r.sets = (r.n + WAVES - 1) / WAVES;
   return r;
 }
 
 template <int K, typename T>
 static hipError_t backward(const ShortConvArgs& a) {
   const Runs r = backward_runs(a.B, a.L, a.D);
-  const long long groups = a.D / BV, items = r.n * groups;
-  const unsigned n = blocks_for(items), m = a.dstate0 ? blocks_for(a.n_seq * groups) : 0;
+  const unsigned n = (unsigned)(r.sets * r.blocks_d), m = a.dstate0 ? blocks_for((long long)a.n_seq * (a.D / BV)) : 0;
   float* const parts = static_cast<float*>(a.workspace);
   prof_mark(kSlotShortConvBwd, false, a.stream);
   hipError_t e = hipSuccess;
   if (n + m > 0) {
-    hipLaunchKernelGGL((backward_kernel<K, T>), dim3(n + m), dim3(NT), 0, a.stream, a, r.len, r.per_row, items, n, parts);
+    hipLaunchKernelGGL((backward_kernel<K, T>), dim3(n + m), dim3(NT), 0, a.stream, a, r.len, r.per_row, r.n, r.blocks_d, n, parts);
     e = hipGetLastError();
   }
   if (e == hipSuccess) {
-    hipLaunchKernelGGL(weight_kernel, dim3((unsigned)(((K + 1) * a.D + 15) / 16)), dim3(NT), 0, a.stream, parts, (int)r.n, a.D, K,
-                       a.dweight, a.dbias);
+    hipLaunchKernelGGL(weight_kernel, dim3((unsigned)(((K + 1) * a.D + 15) / 16)), dim3(NT), 0, a.stream, parts, (int)r.sets, a.D,
+                       K, a.dweight, a.dbias);
     e = hipGetLastError();
   }
   prof_mark(kSlotShortConvBwd, true, a.stream);
@@ -458,7 +478,9 @@ bool short_conv_fits(int B, int L, int D, int n_seq, int dtype) {
   // (Either product may be beyond 64 bits only where its first factor is already too much.)
   if (runs > (most << 8) || n_seq > (1 << 24)) return false;
   const long long items = runs * (D / v), kept = (long long)n_seq * 3 * (D / v), edge = (long long)n_seq * (D / 4);
-  return (items >> 8) + (kept >> 8) + 2 <= most && ((runs * (D / 4)) >> 8) + (edge >> 8) + 2 <= most;
+  // (A workgroup of the backward takes 64 rows or more of 64 groups of channels.)
+  const long long sets = (runs + conv::WAVES - 1) / conv::WAVES * ((D / 4 + 63) / 64);
+  return (items >> 8) + (kept >> 8) + 2 <= most && sets + (edge >> 8) + 2 <= most;
 }
 
 hipError_t launch_short_conv(const ShortConvArgs& a) {
@@ -467,7 +489,7 @@ hipError_t launch_short_conv(const ShortConvArgs& a) {
 }
 
 size_t short_conv_bwd_workspace_bytes(int B, int L, int D, int K) {
-  return (size_t)conv::backward_runs(B, L, D).n * (K + 1) * D * sizeof(float);
+  return (size_t)conv::backward_runs(B, L, D).sets * (K + 1) * D * sizeof(float);
 }
 
 hipError_t launch_short_conv_bwd(const ShortConvArgs& a) {
