@@ -21,47 +21,58 @@ namespace conv {
 
 constexpr int NT = 256;
 
-// The sequence that holds a row, followed from row to row.
-struct Cursor {
-  const int* cu;  // null: every batch row is a sequence
-  int n, L, batch;
-  int seq, begin, end;  // seq < 0 or >= n: rows between begin and end are in none
-
-  __device__ __forceinline__ Cursor(const int* cu, int n, int L, int batch, int row) : cu(cu), n(n), L(L), batch(batch) {
-    seq = batch;
-    begin = 0;
-    end = L;
-    if (cu) find(row);
-  }
-  __device__ __forceinline__ void find(int row) {
-    int lo = -1, hi = n;  // cu[lo] <= row < cu[hi], with cu[-1] = 0 and nothing at n + 1
-    if (row >= cu[n]) {
-      lo = n;
-    } else {
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= row) lo = mid; else hi = mid;
-      }
-    }
-    seq = lo;
-    begin = lo < 0 ? 0 : cu[lo];
-    end = lo < n ? cu[lo + 1] : L;
-    // Whatever cu holds, the row is between the two.
-    begin = min(max(begin, 0), row);
-    end = min(max(end, row + 1), L);
-  }
-  __device__ __forceinline__ bool inside() const { return !cu || (seq >= 0 && seq < n); }
+// A sequence, or rows that are in none (seq < 0 or >= n), from begin to end.
+struct Place {
+  int n, batch;
+  int seq, begin, end;
+  bool packed;
+  __device__ __forceinline__ bool inside() const { return !packed || (seq >= 0 && seq < n); }
 };
-
-// The sequences' cuts in LDS where they fit: a search in memory is a chain of loads
-// (7 prompts in 6001 rows of 2304 channels: 21.9 us in memory, 19.0 in LDS).
-constexpr int kCuts = 512;
-__device__ __forceinline__ const int* cuts_at_hand(const int* cu, int n, int (&lds)[kCuts]) {
-  if (!cu || n >= kCuts) return cu;
-  for (int i = threadIdx.x; i <= n; i += NT) lds[i] = cu[i];
-  __syncthreads();
-  return lds;
+// The whole of sequence `seq`.
+__device__ __forceinline__ Place sequence(const ShortConvArgs& a, int seq) {
+  Place s{a.n_seq, a.cu ? 0 : seq, seq, 0, a.L, a.cu != nullptr};
+  if (a.cu) {
+    s.begin = min(max(a.cu[seq], 0), a.L);
+    s.end = min(max(a.cu[seq + 1], s.begin), a.L);
+  }
+  return s;
 }
+
+// The sequences' cuts, in LDS where they fit: a search in memory is a chain of loads
+// (7 prompts in 6001 rows of 2304 channels: 21.9 us in memory, 19.0 in LDS).  The two are
+// never one pointer: a generic address into LDS may not start below it, which `cut + 1`
+// as an offset would have it do.
+constexpr int kCuts = 512;
+struct Cuts {
+  const int* cu;
+  int n, L;
+  bool at_hand;
+  // Every thread of the workgroup calls this.
+  __device__ __forceinline__ Cuts(const ShortConvArgs& a, int (&lds)[kCuts]) : cu(a.cu), n(a.n_seq), L(a.L) {
+    at_hand = cu && n < kCuts;
+    if (at_hand) {
+      for (int i = threadIdx.x; i <= n; i += NT) lds[i] = cu[i];
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ int cut(const int (&lds)[kCuts], int i) const {
+    typedef const __attribute__((address_space(3))) int* local_ptr;
+    typedef const __attribute__((address_space(1))) int* global_ptr;
+    return at_hand ? ((local_ptr)lds)[i] : ((global_ptr)(uintptr_t)cu)[i];
+  }
+  __device__ __forceinline__ Place find(const int (&lds)[kCuts], int batch, int row) const {
+    if (!cu) return Place{n, batch, batch, 0, L, false};
+    int lo = 0, hi = n + 1;  // as many cuts, at least and at most, are not behind the row
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (cut(lds, mid) <= row) lo = mid + 1;
+      else hi = mid;
+    }
+    const int begin = lo > 0 ? cut(lds, lo - 1) : 0, end = lo <= n ? cut(lds, lo) : L;
+    // Whatever the cuts are, the row is between the two.
+    return Place{n, batch, lo - 1, min(max(begin, 0), row), min(max(end, row + 1), L), true};
+  }
+};
 
 template <int V> struct Vals { f32x4 v[V / 4]; };
 template <int V>
@@ -144,7 +155,7 @@ __device__ __forceinline__ void push(Vals<V> (&past)[K], const Vals<V>& x) {
 
 // Row `t` of the sequence's extended rows (t may lie up to K - 1 before its begin).
 template <int V, typename T>
-__device__ __forceinline__ Raws<V, T> row_of(const ShortConvArgs& a, const Cursor& s, int t, int c) {
+__device__ __forceinline__ Raws<V, T> row_of(const ShortConvArgs& a, const Place& s, int t, int c) {
   if (!s.inside()) return none<V, T>();
   if (t >= s.begin) return load<V>(static_cast<const T*>(a.x.p) + s.batch * a.x.sb + t * a.x.sl + c);
   const int kept = a.K - 1 + t - s.begin;
@@ -152,7 +163,7 @@ __device__ __forceinline__ Raws<V, T> row_of(const ShortConvArgs& a, const Curso
   return load<V>(static_cast<const T*>(a.state0) + ((size_t)s.seq * (a.K - 1) + kept) * a.D + c);
 }
 template <int V, int K, typename T>
-__device__ __forceinline__ void enter(const ShortConvArgs& a, const Cursor& s, int t, int c, Vals<V> (&past)[K - 1]) {
+__device__ __forceinline__ void enter(const ShortConvArgs& a, const Place& s, int t, int c, Vals<V> (&past)[K - 1]) {
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) past[j] = widen<V>(row_of<V, T>(a, s, t - (K - 1) + j, c));
 }
@@ -169,12 +180,7 @@ __global__ __launch_bounds__(NT) void forward_kernel(ShortConvArgs a, int per_ro
     if (item >= (long long)a.n_seq * (K - 1) * groups) return;
     const long long row = item / groups;
     const int c = (int)(item - row * groups) * V, seq = (int)(row / (K - 1)), j = (int)(row - (long long)seq * (K - 1));
-    Cursor s(nullptr, a.n_seq, a.L, a.cu ? 0 : seq, 0);
-    s.seq = seq;
-    if (a.cu) {
-      s.begin = min(max(a.cu[seq], 0), a.L);
-      s.end = min(max(a.cu[seq + 1], s.begin), a.L);
-    }
+    const Place s = sequence(a, seq);
     store<V>(static_cast<T*>(a.state) + row * a.D + c, row_of<V, T>(a, s, s.end - (K - 1) + j, c));
     return;
   }
@@ -189,7 +195,8 @@ __global__ __launch_bounds__(NT) void forward_kernel(ShortConvArgs a, int per_ro
 #pragma unroll
   for (int i = 0; i < R; ++i) rows[i] = load<V>(x + min(t0 + i, t1 - 1) * a.x.sl);
   const Taps<V, K> taps(a.weight, a.bias, c);
-  Cursor s(cuts_at_hand(a.cu, a.n_seq, cuts), a.n_seq, a.L, b, t0);
+  const Cuts cu(a, cuts);
+  Place s = cu.find(cuts, b, t0);
   if (!on) return;
   Vals<V> past[K - 1];
   enter<V, K, T>(a, s, t0, c, past);
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(NT) void forward_kernel(ShortConvArgs a, int per_ro
     const int t = t0 + i;
     if (t >= t1) break;
     if (a.cu && t >= s.end) {
-      s.find(t);
+      s = cu.find(cuts, b, t);
       enter<V, K, T>(a, s, t, c, past);
     }
     const Vals<V> xt = widen<V>(rows[i]);
@@ -245,12 +252,7 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
     const long long item = (long long)(blockIdx.x - run_blocks) * NT + threadIdx.x;
     if (item >= (long long)a.n_seq * groups) return;
     const int seq = (int)(item / groups), c = (int)(item - (long long)seq * groups) * BV;
-    Cursor s(nullptr, a.n_seq, a.L, a.cu ? 0 : seq, 0);
-    s.seq = seq;
-    if (a.cu) {
-      s.begin = min(max(a.cu[seq], 0), a.L);
-      s.end = min(max(a.cu[seq + 1], s.begin), a.L);
-    }
+    const Place s = sequence(a, seq);
     const int n = s.end - s.begin;
     const Taps<BV, K> taps(a.weight, a.bias, c);
     Vals<BV> past[K - 1], d[K - 1];
@@ -290,8 +292,9 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
   const T* const dy = static_cast<const T*>(a.dy) + (size_t)b * a.L * a.D + c;
   T* const dx = static_cast<T*>(a.dx) + (size_t)b * a.L * a.D + c;
   const Taps<BV, K> taps(a.weight, a.bias, c);
-  Cursor s(cuts_at_hand(a.cu, a.n_seq, cuts), a.n_seq, a.L, b, t0);  // of the row whose q is formed
-  Cursor o = s;                         // of the row whose dx is finished
+  const Cuts cu(a, cuts);
+  Place s = cu.find(cuts, b, t0);  // of the row whose q is formed
+  Place o = s;                         // of the row whose dx is finished
   Vals<BV> past[K - 1], q[K], dw[K], db = zeros<BV>();
   enter<BV, K, T>(a, s, t0, c, past);
 #pragma unroll
@@ -316,7 +319,7 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
       Vals<BV> qt = zeros<BV>();
       if (t < stop) {
         if (a.cu && t >= s.end) {
-          s.find(t);
+          s = cu.find(cuts, b, t);
           enter<BV, K, T>(a, s, t, c, past);
         }
         if (s.inside()) {
@@ -333,7 +336,7 @@ __global__ __launch_bounds__(NT) void backward_kernel(ShortConvArgs a, int len, 
       push(q, qt);
       const int r = t - (K - 1);
       if (r >= t0 && r < t1) {
-        if (a.cu && r >= o.end) o.find(r);
+        if (a.cu && r >= o.end) o = cu.find(cuts, b, r);
         Vals<BV> d = zeros<BV>();
         if (o.inside()) {
           // q[j] is of row r + j, which reads row r with tap K - 1 - j.
