@@ -135,12 +135,12 @@ __device__ __forceinline__ f32x4 wide(const Uniform4<float>& u) {
 // to the compiler, every row's load is waited for where it is used: 3.4 ms instead of
 // 2.1 for 65536 tokens of 4096 channels; with groups of 8 rows 2.09.)
 template <typename T> constexpr int group_rows() { return 8 / (int)sizeof(T); }
-template <typename T>
+template <typename T, int R = group_rows<T>()>
 struct Group {
-  Uniform4<T> r[group_rows<T>()];
+  Uniform4<T> r[R];
   __device__ __forceinline__ void load(const T* p, long long stride) {
 #pragma unroll
-    for (int i = 0; i < group_rows<T>(); ++i, p += stride) r[i] = uniform4(p);
+    for (int i = 0; i < R; ++i, p += stride) r[i] = uniform4(p);
   }
 };
 // Scalar loads and LDS reads share a counter and come back in any order, so what is

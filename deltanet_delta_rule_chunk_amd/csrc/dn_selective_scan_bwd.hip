@@ -208,7 +208,7 @@ struct Flag {
 
 template <int NW, typename T, bool GATE, bool SPLIT>
 __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, int blocks_d, BwdSpace ws) {
-  constexpr int N = 4 * NW, R = group_rows<T>(), Q = kHalf / R;
+  constexpr int N = 4 * NW, R = 2 * group_rows<T>(), Q = kHalf / R;
   using At = Spot<NW>;
   __shared__ float2 sx[kTile][kCh];                    // dt, dt u
   __shared__ float sg[kTile][kCh];                     // g
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
       const int t0 = half * kHalf;
       if (!kFull && t0 >= n) continue;
       // Rows behind the segment are read at its last row and count as 0.
-      const auto load = [&](Group<T>& to, const T* rows, long long stride, int q) {
+      const auto load = [&](Group<T, R>& to, const T* rows, long long stride, int q) {
         if (kFull) {
           to.load(rows + (t0 + q * R) * stride, stride);
         } else {
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
         sda[w][t0 + t][lane] = pa;
         if (GATE) sy[w][t0 + t][lane] = py;
       };
-      Group<T> gb[2], gc[2];
+      Group<T, R> gb[2], gc[2];
       float2 x[2][R];
       float gy[2][R];
       load(gb[0], Bt, a.Bm.sl, 0);
