@@ -119,7 +119,10 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
   }
   if (!E4M3) return;
   most = row_all<LPR, Max>(most, red);
-  const float scale = most > 0.f || most != most ? most / kE4m3Max : 1.f;
+  // (Not below the smallest normal number, so that quotients by it are numbers.)
+  float scale = most / kE4m3Max;
+  if (most == 0.f) scale = 1.f;
+  else if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;
   if (on && lane == 0) a.scale[row] = scale;
   unsigned char* const y = static_cast<unsigned char*>(a.y) + base;
 #pragma unroll

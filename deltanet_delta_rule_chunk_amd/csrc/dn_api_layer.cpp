@@ -349,7 +349,7 @@ int deltanet_add_rms_norm_bwd(const void* total, const float* weight, const void
   if (rows > 0 && (!total || !dy || !dx)) return DN_ERR_NULL_ARG;
   if (any_misaligned({total, weight, dy, dtotal, dx, dresidual, dweight, workspace})) return DN_ERR_MISALIGNED;
   const size_t n = (size_t)rows * D, e = dtype_size(dtype), r = dtype_size(residual_dtype), wb = (size_t)D * 4;
-  const size_t need = dn::add_norm_bwd_workspace_bytes(rows, D);
+  const size_t need = dweight ? dn::add_norm_bwd_workspace_bytes(rows, D) : 0;
   const Span in[] = {{total, n * r}, {weight, wb}, {dy, n * e}, {dtotal, n * r}};
   const Span out[] = {{dx, n * e}, {dresidual, n * r}, {dweight, wb}};
   if (workspace && workspace_bytes < need) return DN_ERR_WORKSPACE;

@@ -18,12 +18,13 @@ namespace ssm {
 // One workgroup.  Sequence i holds the rows from cu[i] to cu[i + 1]; whatever
 // cu holds, begins and ends are brought into 0 .. L and never fall, so the rows
 // of all segments lie in the tensors and their number is at most L / len + n_seq + 2.
+__device__ __forceinline__ int pieces_of(int n, int len) { return n > 0 ? (n - 1) / len + 1 : 0; }
 static __global__ __launch_bounds__(256) void segment_table_kernel(const int* cu, int n_seq, int L, int len, int* used,
                                                                    int* first_of, int4* table) {
   __shared__ int ends[256], counts[256];
   const int tid = threadIdx.x;
   int end = min(max(cu[0], 0), L);  // of the sequence before
-  int at = (end + len - 1) / len;   // segments so far: the rows in front of the first sequence
+  int at = pieces_of(end, len);     // segments so far: the rows in front of the first sequence
   for (int i = tid; i < at; i += 256) table[i] = make_int4(i * len, min(len, end - i * len), -1, 3);
   for (int base = 0; base < n_seq; base += 256) {
     const int i = base + tid;
@@ -37,7 +38,7 @@ static __global__ __launch_bounds__(256) void segment_table_kernel(const int* cu
     }
     const int my_end = max(ends[tid], end), begin = tid ? max(ends[tid - 1], end) : end;
     const int next_end = max(ends[255], end);
-    const int n = my_end - begin, pieces = i < n_seq ? max(1, (n + len - 1) / len) : 0;
+    const int n = my_end - begin, pieces = i < n_seq ? max(1, pieces_of(n, len)) : 0;
     counts[tid] = pieces;
     __syncthreads();
     for (int off = 1; off < 256; off <<= 1) {
@@ -54,7 +55,7 @@ static __global__ __launch_bounds__(256) void segment_table_kernel(const int* cu
     end = next_end;
     __syncthreads();
   }
-  const int behind = (L - end + len - 1) / len;
+  const int behind = pieces_of(L - end, len);
   for (int i = tid; i < behind; i += 256) table[at + i] = make_int4(end + i * len, min(len, L - end - i * len), -1, 3);
   if (tid == 0) {
     first_of[n_seq] = at;

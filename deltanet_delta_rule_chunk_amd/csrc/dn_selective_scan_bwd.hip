@@ -242,7 +242,8 @@ __global__ __launch_bounds__(64 * NW, 2) void back_kernel(ScanArgs a, Plan pl, i
       put4(ddt - back + o, zero4());
       if (GATE) put4(dz - back + o, zero4());
     }
-    for (int i = threadIdx.x; i < g.n * N; i += 64 * NW) (dB - begin * N)[i] = (dC - begin * N)[i] = 0.f;
+    const size_t first = (size_t)begin * N;
+    for (size_t i = threadIdx.x; i < (size_t)g.n * N; i += 64 * NW) (dB - first)[i] = (dC - first)[i] = 0.f;
     if (on) *reinterpret_cast<f32x4*>(dA_to) = zero4();
     if (on && w == 0) dvec[ch] = dvec[a.D + ch] = 0.f;
     return;

@@ -507,7 +507,8 @@ int deltanet_short_conv_step(const void* x, const long long* x_stride, const flo
  *   u, dt, z: rows of [B, L, D] dtype; dt is raw; z may be NULL.  B, C (Bm, Cm): rows of
  *            [B, L, N] dtype, shared by all channels.  strides: HOST array of 10, (batch, token)
  *            of u, dt, Bm, Cm, z in this order, or NULL (all dense); rules as above.
- *   A      : [D, N] fp32 (negative for states that decay);  D_skip, dt_bias: [D] fp32 or NULL (zeros)
+ *   A      : [D, N] fp32, negative (with a positive one no state may grow by more than 2^127 over
+ *            a call);  D_skip, dt_bias: [D] fp32 or NULL (zeros)
  *   h0     : [n, D, N] fp32 or NULL (zeros);  cu_seqlens, n_seq, n: as above
  *   y      : [B, L, D] dtype, dense, written (zeros in rows that no sequence holds)
  *   hT     : [n, D, N] fp32, the states behind, or NULL; may be h0 (in place)
@@ -557,7 +558,9 @@ int deltanet_selective_scan_step(const void* u, const void* dt, const void* Bm, 
  *   weight : [D] fp32 or NULL (ones)
  *   y      : [rows, D] dtype;  or, with scale ([rows] fp32), 8-bit e4m3 values with
  *            y = value * scale: scale is the row's largest magnitude / 448 (1 for a row of zeros)
- *   D a multiple of 8, up to 32768; dtype = DN_F32 needs residual_dtype = DN_F32.  Evaluated in fp32.
+ *   D a multiple of 8, up to 32768; dtype = DN_F32 needs residual_dtype = DN_F32.  Evaluated in fp32:
+ * rows beyond ~1e19 overflow their sum of squares (y is then zeros); with eps = 0 a row of
+ * zeros is not finite.  What is not finite stays in its row.
  */
 int deltanet_add_rms_norm(const void* x, const void* residual, const float* weight, void* total, void* y, float* scale,
                           int rows, int D, float eps, dn_dtype dtype, dn_dtype residual_dtype, hipStream_t stream);
@@ -567,6 +570,7 @@ int deltanet_add_rms_norm(const void* x, const void* residual, const float* weig
  * elsewhere, or NULL); total as the forward wrote it (the norm of x alone: x, with residual_dtype = dtype):
  *   dx     : [rows, D] dtype;  dresidual: the same in residual_dtype, or NULL (not written)
  *   dweight: [D] fp32 or NULL (not written), summed in an order that does not change from call to call
+ * The workspace is used for dweight alone.
  */
 int deltanet_add_rms_norm_bwd(const void* total, const float* weight, const void* dy, const void* dtotal,
                               void* dx, void* dresidual, float* dweight, int rows, int D, float eps,

@@ -172,3 +172,14 @@ def test_refusals(gpu_lib):
         N.add_rms_norm(x, None, None, y=x)
     with pytest.raises(TypeError, match="dtype"):
         N.add_rms_norm(x.half(), None, None)
+
+
+def test_smallest_rows_in_8_bits(gpu_lib):
+    """Rows whose scale would be below fp32's normal numbers: quotients stay numbers."""
+    x = torch.zeros((3, 64), device=DEV)
+    x[0, 1], x[1, 2], x[2] = 1e-38, 1e-42, 3e-39
+    y8, scale, _ = N.add_rms_norm_fp8(x, None, None, eps=1.0)
+    y = y8.float() * scale[:, None]
+    assert torch.isfinite(y8.float()).all() and (scale >= 2.0 ** -126).all()
+    # Half of the smallest step of e4m3, 2^-10, of the scale (sums of squares underflow: r = 1).
+    assert float((y - x).abs().max()) <= 2.0 ** -10 * float(scale.max()) + 2.0 ** -4 * 1e-38

@@ -139,6 +139,14 @@ def test_cuts_that_fall_or_leave_the_rows_stay_in_bounds(gpu_lib):
         assert all(torch.isfinite(t.float()).all() for t in (y, *d))
 
 
+def test_no_tokens(gpu_lib):
+    x = gpu(conv_inputs(15, 2, 0, 64, 4, "bf16", 2))
+    y, state = N.short_conv_fwd(x["x"], x["weight"], x["bias"], x["state0"])
+    assert y.shape == (2, 0, 64) and torch.equal(state, x["state0"])
+    dx, dw, db, ds = N.short_conv_bwd(x["x"], x["weight"], x["bias"], x["state0"], x["dy"], x["dstate"])
+    assert dx.shape == (2, 0, 64) and not dw.any() and not db.any() and torch.equal(ds, x["dstate"])
+
+
 def test_autograd(gpu_lib):
     x = conv_inputs(13, 2, 19, 24, 4, "f32", 2)
     g = gpu(x)
