@@ -158,11 +158,14 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
     if (from) h = get4(from + (size_t)ch * N + 4 * w);
   }
   float sum = 0.f;
+  Ahead<NW, T> nB(a.Bm.p, g.batch * a.Bm.sb + g.row * a.Bm.sl, a.Bm.sl), nC(a.Cm.p, g.batch * a.Cm.sb + g.row * a.Cm.sl, a.Cm.sl);
   const auto fetch = [&](int n) {
     if (n <= 0) return;
     u.fetch(at, c, n);
     dt.fetch(at, c, n);
     if (OUT && GATE) z.fetch(at, c, n);
+    nB.fetch(n);
+    if (OUT) nC.fetch(n);
   };
   fetch(g.n);
   int buf = 0;
@@ -179,9 +182,13 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
         out[1] = f32x4{d[2], x[2], d[3], x[3]};
       }
     }
+    nB.arrived();
+    if (OUT) nC.arrived();
     u.move(1);
     dt.move(1);
     if (OUT && GATE) z.move(1);
+    nB.move(1);
+    if (OUT) nC.move(1);
     fetch(left - kTile);
     float part = 0.f;
     const auto step = [&](int t, f32x4 b, f32x4 cc, float2 x) {
