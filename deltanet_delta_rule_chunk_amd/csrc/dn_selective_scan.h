@@ -200,14 +200,16 @@ struct Feed {
 // channels: 236 us with it, 254 without).
 template <int NW, typename T>
 struct Ahead {
+  static constexpr int N = 4 * NW;
   const T* tile;
   long long stride;
+  uint32_t off;
   T value;
   __device__ __forceinline__ Ahead(const void* p, long long first, long long stride)
-      : tile(static_cast<const T*>(p) + first), stride(stride), value{} {}
+      : tile(static_cast<const T*>(p) + first), stride(stride), off(offset_of<T>((int)threadIdx.x / N, stride, (int)threadIdx.x % N)),
+        value{} {}
   __device__ __forceinline__ void fetch(int n) {
-    constexpr int N = 4 * NW;
-    value = *at_bytes(tile, offset_of<T>(min((int)threadIdx.x / N, n - 1), stride, (int)threadIdx.x % N));
+    value = *at_bytes(tile, n >= kTile ? off : offset_of<T>(min((int)threadIdx.x / N, n - 1), stride, (int)threadIdx.x % N));
   }
   __device__ __forceinline__ void arrived() { asm volatile("" ::"v"(to_f32(value))); }
   __device__ __forceinline__ void move(int tiles) { tile += tiles * kTile * stride; }
