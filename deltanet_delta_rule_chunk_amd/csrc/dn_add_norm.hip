@@ -11,7 +11,7 @@
 //
 // Bound by HBM.  A row's elements stay in the registers of a group of LPR lanes
 // (pieces of 8) between the sum of squares and the result, so each is read once: 65536 rows
-// of 4096 bf16 elements into 8 bits 325 us (5.8 TB/s), 16385 of 2072 with an fp32 stream
+// of 4096 bf16 elements into 8 bits 330 us (5.7 TB/s), 16385 of 2072 with an fp32 stream
 // 74 us (5.5 TB/s) and their gradient 113 (4.8).
 
 #include "dn_launch.h"
@@ -41,14 +41,27 @@ __device__ __forceinline__ float dot8(const Eight& x, const Eight& y) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+__device__ __forceinline__ float at(const Eight& x, int k) { return k < 4 ? x.a[k] : x.b[k - 4]; }
+
 struct Sum { static __device__ __forceinline__ float of(float a, float b) { return a + b; } };
 // (A NaN stays one: the other side of a comparison with it is never taken.)
-struct Max { static __device__ __forceinline__ float of(float a, float b) { return a > b || a != a ? a : b; } };
+struct Max { static __device__ __forceinline__ double of(double a, double b) { return a > b || a != a ? a : b; } };
+
+// A value as a sum of two; a product of two fp32 is one exactly.
+struct Pair { float hi, lo; };
+__device__ __forceinline__ Pair product(float a, float b) {
+  const float p = a * b;
+  return {p, fmaf(a, b, -p)};
+}
+__device__ __forceinline__ Pair larger(Pair a, Pair b) {
+  const bool second = b.hi > a.hi || (b.hi == a.hi && b.lo > a.lo);
+  return {second ? b.hi : a.hi, second ? b.lo : a.lo};
+}
 
 // Over the LPR lanes of a row, the same for all of them.  `red` has a place for
 // every wave; rows of more than a wave use it and every thread of the workgroup calls this.
-template <int LPR, typename Op>
-__device__ __forceinline__ float row_all(float x, float* red) {
+template <int LPR, typename Op, typename F>
+__device__ __forceinline__ F row_all(F x, F* red) {
 #pragma unroll
   for (int off = (LPR < 64 ? LPR : 64) / 2; off > 0; off >>= 1) x = Op::of(x, __shfl_xor(x, off, 64));
   if (LPR > 64) {
@@ -70,6 +83,7 @@ template <int LPR, int P, typename T, typename R, bool E4M3>
 __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) {
   constexpr int NT = threads<LPR>(), RPB = NT / LPR;
   __shared__ float red[NT / 64];
+  __shared__ double red8[E4M3 ? NT / 64 : 1];
   const int lane = threadIdx.x % LPR;
   const long long row = (long long)blockIdx.x * RPB + threadIdx.x / LPR;
   const bool on = row < a.rows;
@@ -78,14 +92,16 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
   const R* const res = a.residual ? static_cast<const R*>(a.residual) + base : nullptr;
   R* const total = a.residual ? static_cast<R*>(a.total) + base : nullptr;
   const int pieces = a.D / 8;
-  Eight v[P];
+  Eight v[P], w[P];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int p = lane + i * LPR;
     v[i] = {zero4(), zero4()};
+    w[i] = {f32x4{1.f, 1.f, 1.f, 1.f}, f32x4{1.f, 1.f, 1.f, 1.f}};
     if (p >= pieces) continue;
     v[i] = load8(x + p * 8);
+    if (a.weight) w[i] = load8(a.weight + p * 8);
     if (res) {
       const Eight r = load8(res + p * 8);
       v[i].a += r.a;
@@ -103,29 +119,50 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
   }
   ss = row_all<LPR, Sum>(ss, red);
   const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
-  float most = 0.f;
+  if (!E4M3) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int p = lane + i * LPR;
-    if (p >= pieces) continue;
-    Eight w{f32x4{1.f, 1.f, 1.f, 1.f}, f32x4{1.f, 1.f, 1.f, 1.f}};
-    if (a.weight) w = load8(a.weight + p * 8);
-    v[i].a = v[i].a * r * w.a;
-    v[i].b = v[i].b * r * w.b;
-    if (E4M3) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) most = Max::of(most, fabsf(v[i].a[k])), most = Max::of(most, fabsf(v[i].b[k]));
-    } else if (on) {
+    for (int i = 0; i < P; ++i) {
+      const int p = lane + i * LPR;
+      if (p >= pieces || !on) continue;
+      v[i].a = v[i].a * r * w[i].a;
+      v[i].b = v[i].b * r * w[i].b;
       store8(static_cast<T*>(a.y) + base + p * 8, v[i]);
     }
+    return;
   }
-  if (!E4M3) return;
-  most = row_all<LPR, Max>(most, red);
-  // (Not below the smallest normal number, so that quotients by it are numbers.)
-  float scale = most / kE4m3Max;
-  if (most == 0.f) scale = 1.f;
-  else if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;
+  // r is in every y of the row and in the scale, so the 8-bit values do not depend on it:
+  // y / scale = (total w) (448 / max |total w|).  With products and quotient held as two fp32
+  // each, e4m3's own rounding is the only one; in single fp32 a few values in a million are a
+  // step off, for the same time (330 us for 65536 rows of 4096; fp64 359).  Of r the power of
+  // two is taken out first, which is exact and keeps the products in range.
+  const float r2 = __uint_as_float(__float_as_uint(r) & 0x7f800000u);
+  Pair top{0.f, 0.f};
+  float odd = 0.f;  // NaN once a product is not finite
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    v[i].a *= r2;
+    v[i].b *= r2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const Pair x = product(at(v[i], k), at(w[i], k));
+      odd = fmaf(x.hi, 0.f, odd);
+      top = larger(top, x.hi < 0.f ? Pair{-x.hi, -x.lo} : x);
+    }
+  }
+  const double most = row_all<LPR, Max>(odd == 0.f ? (double)top.hi + top.lo : (double)odd, red8);
+  float scale = (float)(most * (r / r2) * (1.0 / kE4m3Max));
+  double by = kE4m3Max / most;
+  if (most == 0.0) {
+    scale = 1.f;
+    by = 0.0;
+  } else if (scale < 1.17549435e-38f) {  // (not below the smallest normal number)
+    scale = 1.17549435e-38f;
+    by = (double)(r / r2) / scale;
+  }
   if (on && lane == 0) a.scale[row] = scale;
+  // (A row whose y are all below 2^-90 keeps the quotient in fp64: it is past fp32's range.)
+  const bool small = by > 0x1p99;
+  const float by_hi = (float)by, by_lo = (float)(by - by_hi);
   unsigned char* const y = static_cast<unsigned char*>(a.y) + base;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -134,7 +171,8 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
     float q[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float t = (k < 4 ? v[i].a[k & 3] : v[i].b[k & 3]) / scale;
+      const Pair x = product(at(v[i], k), at(w[i], k));
+      const float t = small ? (float)(((double)x.hi + x.lo) * by) : fmaf(x.hi, by_hi, fmaf(x.hi, by_lo, x.lo * by_hi));
       // The largest may come out a little above 448; a NaN stays one.
       q[k] = t > kE4m3Max ? kE4m3Max : t < -kE4m3Max ? -kE4m3Max : t;
     }

@@ -79,11 +79,35 @@ def test_8_bits(gpu_lib, dtype, wide, D):
     half = np.maximum(np.abs(v) * 2.0 ** -4, s[:, None] * 2.0 ** -10)
     assert (np.abs(got - v) <= half * (1 + 100 * 2.0 ** -24) + 100 * 2.0 ** -24 * np.abs(v)).all()
     assert f64(y8.float())[live].__abs__().max(-1).min() == 448.0
-    # The values are what torch makes of the same quotients, but for ties moved by a rounding.
-    y = N.add_rms_norm(x.to(DEV).float(), res.to(DEV).float(), w.to(DEV))[0] if dtype == "f32" else None
-    if y is not None:
-        q = (y / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
-        assert torch.equal(q.view(torch.uint8), y8.view(torch.uint8))
+    # The values are those of the quotients in 64 bits.
+    vw = f64(total) * f64(w)
+    q = torch.from_numpy(vw[live] * (448 / np.abs(vw[live]).max(-1, keepdims=True))).float().to(torch.float8_e4m3fn)
+    assert torch.equal(q.view(torch.uint8), y8.cpu()[torch.from_numpy(live)].view(torch.uint8))
+
+
+@pytest.mark.parametrize("size,weight", [(1.0, 2.0 ** -100), (2.0 ** 30, 2.0 ** 100), (2.0 ** -60, 1.0), (2.0 ** 55, 1.0)])
+def test_8_bits_of_small_and_large(gpu_lib, size, weight):
+    # (264 squares of 2^60 times a normal number pass 2^128, where the row overflows: 2^55 stays within.)
+    x, _, w, _, _ = _inputs(3, 7, 264, "f32", "f32")
+    x, w = x.double() * size, w.double() * weight   # (scaled by powers of two: exact in fp32)
+    y8, scale, _ = N.add_rms_norm_fp8(x.float().to(DEV), None, w.float().to(DEV), eps=0.0)
+    v = add_norm(f64(x), f64(w), 0.0)
+    top = np.abs(v).max(-1)
+    assert (np.abs(f64(scale) * 448 - top) <= 45 * 2.0 ** -24 * top).all()
+    vw = f64(x) * f64(w)
+    q = torch.from_numpy(vw * (448 / np.abs(vw).max(-1, keepdims=True))).float().to(torch.float8_e4m3fn)
+    assert torch.equal(q.view(torch.uint8), y8.cpu().view(torch.uint8))
+
+
+def test_8_bits_where_a_row_overflows_and_weights_that_are_not_finite(gpu_lib):
+    x, _, w, _, _ = (t.to(DEV) for t in _inputs(4, 5, 264, "f32", "f32"))
+    x[2] *= 2.0 ** 80
+    y8, scale, _ = N.add_rms_norm_fp8(x, None, w)
+    assert float(scale[2]) == 1.0 and not y8[2].float().any() and y8[1].float().any()
+    for bad in (float("nan"), float("inf")):
+        w[9] = bad
+        y8, scale, _ = N.add_rms_norm_fp8(x, None, w)
+        assert scale.isnan().all() and y8.float().isnan().all()
 
 
 def test_without_residual_weight_and_in_place(gpu_lib):
