@@ -7,7 +7,7 @@
 // with a decay of its own, so there is no matrix product in it: the work is a
 // multiplication, an exponential and three more operations on every
 // (token, channel, state) and the vector units bound it: 65536 tokens of 4096 channels
-// with 16 states take 1540 us (two walks, the vector units busy throughout), 458 at the
+// with 16 states take 1560 us (two walks, the vector units busy throughout), 458 at the
 // rate of a copy.
 //
 // A workgroup takes 64 channels, one per lane, and a wave 4 of their states, so
@@ -85,15 +85,23 @@ struct Sizes {
   bool split;          // whether a sequence may have more than one
 };
 inline long long channel_blocks(int D) { return (D + kCh - 1) / kCh; }
-// A length of segment for `streams` sequences of at most L tokens, `most`
-// workgroups or more being enough without a cut, `want` being aimed at with one.
-inline Sizes sizes_of(bool packed, int B, int L, int n_seq, int D, long long enough, long long want, int least) {
+// How sequences are cut: not if there are `enough` workgroups without a cut, or no more than
+// `whole` tokens (where workgroups are many, 1 token per `each` of them); else into `want` workgroups, but pieces of no less than 64 tokens, or 48 or 32 where
+// those give no more than `few` workgroups, or 16 where they give one per CU (then a call waits
+// for a walk's length, not for the units).
+struct Cutting {
+  long long enough, want, few;
+  int whole, each;
+};
+inline Sizes sizes_of(bool packed, int B, int L, int n_seq, int D, const Cutting& k) {
   const long long groups = B * channel_blocks(D);
   Sizes s;
   const long long whole = ((long long)L + kTile - 1) / kTile * kTile;
   s.len = (int)(whole < kTile ? kTile : whole > 0x7fffffe0LL ? 0x7fffffe0LL : whole);
-  if (groups < enough && L > least) {
-    const long long pieces = (want + groups - 1) / groups;
+  if (groups < k.enough && L > k.whole && L > groups / k.each) {
+    int least = kTile;
+    while (least < 64 && groups * ((L - 1) / least + 1) > (least == kTile ? 256 : k.few)) least += kTile;
+    const long long pieces = (k.want + groups - 1) / groups;
     long long len = ((long long)L + pieces - 1) / pieces;
     len = (len + kTile - 1) / kTile * kTile;
     s.len = (int)(len < least ? least : len);

@@ -264,12 +264,16 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
   if (to) *reinterpret_cast<f32x4*>(to + (size_t)ch * N + 4 * w) = h;
 }
 
-// 1024 workgroups need no cut (16 x 2048 tokens of 2048 channels, 512 of them: 445 us uncut,
-// 405 cut; 32 x 1024, 1024 of them: 294 and 385).  With one, 4096: 65536 tokens of 4096 channels
-// take 1974 us with 1024, 1765 with 1536, 1710 with 2048, 1630 with 4096, 1604 with 8192, which
-// costs shorter sequences as much; pieces below 64 tokens gain nothing.
+// 512 workgroups need no cut (bf16, 32 x 2048 tokens of 1024 channels, 512 of them: 354 us uncut,
+// 402 cut; 384 of them 349 and 323; 256, 1024 tokens: 145 and 121), and short sequences
+// need it later the more there are (256 tokens of 1024 channels: 16 of them, 256 workgroups, 41 us
+// uncut, 42 cut; 8 of them 41 and 31; one 40 and 18).  With a cut, 4096: 65536 tokens of 4096
+// channels take 1974 us with 1024, 1765 with 1536, 1710 with 2048, 1630 with 4096, 1604 with 8192,
+// which costs shorter sequences as much.  Pieces: 512 tokens of 1024 channels, 26 us in pieces
+// of 64, 23 of 48, 21 of 32, 22 of 16; 128 of them 26, 22, 20 and 17; 8192 of 768, 69, 74 and 83
+// of 64, 48, 32.
 static Sizes forward_sizes(int B, int L, int D, bool packed, int n_seq) {
-  return sizes_of(packed, B, L, n_seq, D, 1024, 4096, 64);
+  return sizes_of(packed, B, L, n_seq, D, {512, 4096, 640, 80, 1});
 }
 
 template <int NW, typename T, bool GATE>

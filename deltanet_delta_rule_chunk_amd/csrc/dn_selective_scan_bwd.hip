@@ -549,11 +549,13 @@ static __global__ __launch_bounds__(256) void segments_kernel(const int* used, i
 
 // ---- launches --------------------------------------------------------------------------------------
 
-// 512 workgroups need no cut here, as a cut adds the walk back from zero (forward + backward of
-// 16 x 2048 tokens of 2048 channels, 512 of them: 840 us uncut, 906 cut).  With one, 4096: 2 x 8192
-// tokens of 4096 channels take 1873 us with 1024, 1790 with 2048, 1771 with 4096, 1811 with 8192.
+// 512 workgroups need no cut here either (forward + backward of 16 x 2048 tokens of 2048
+// channels, 512 of them: 840 us uncut, 906 cut; 16 x 64 of 1024, 256 of them: 41 uncut and 43).
+// With one, 4096: 2 x 8192 tokens of 4096 channels take 1873 us with 1024, 1790 with 2048, 1771 with
+// 4096, 1811 with 8192.  Pieces: 512 tokens of 768 channels, 46 us in pieces of 64, 40 of 48, 35
+// of 32, 37 of 16; 128 of them 43, 37, 31 and 26 (62 uncut).
 Sizes backward_sizes(int B, int L, int D, bool packed, int n_seq) {
-  return sizes_of(packed, B, L, n_seq, D, 512, 4096, 64);
+  return sizes_of(packed, B, L, n_seq, D, {512, 4096, 512, 32, 4});
 }
 static size_t up(size_t n) { return (n + 3) / 4 * 4; }  // floats, to 16 bytes
 

@@ -70,6 +70,13 @@ def test_batch(gpu_lib, dtype, S, B, L, D):
     _check(x, gpu(x))
 
 
+@pytest.mark.parametrize("B,L,D", [(1, 80, 256), (1, 81, 256), (2, 33, 264), (1, 400, 1024), (1, 700, 1024), (5, 300, 1024), (9, 130, 1024), (33, 40, 1024)])
+def test_lengths_of_segments(gpu_lib, B, L, D):
+    """Around the rules that choose whether, and into pieces of how many tokens, sequences are cut."""
+    x = scan_inputs(L, B, L, D, 8, "f32", B)
+    _check(x, gpu(x))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("where", PACKED)
 @pytest.mark.parametrize("S", [8, 16])
