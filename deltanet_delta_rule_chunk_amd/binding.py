@@ -918,6 +918,12 @@ def _ll_array(*x):
     return (ctypes.c_longlong * len(x))(*x)
 
 
+def _check_sizes(what: str, sizes) -> None:
+    """The library takes sizes as C ints, to which ctypes would cut larger ones without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise DeltaNetError(3, what, f"sizes up to 2^31 - 1 (got {tuple(sizes)})")
+
+
 def _check_cu(cu_seqlens, B: int, device) -> int:
     """Number of sequences: B of equal length, or what ``cu_seqlens`` packs in one row."""
     if cu_seqlens is None:
@@ -949,6 +955,7 @@ def _conv_setup(x, weight, bias, state0, cu_seqlens, dims):
                          f"(got {tuple(xs)}, {tuple(ws)})")
     dev, dt, D, K = x.device, x.dtype, xs[-1], ws[1]
     n = xs[0] if cu_seqlens is None else _check_cu(cu_seqlens, xs[0], dev)
+    _check_sizes("short convolution", (*xs, K, n))
     # One look at everything; the reasons only where something is wrong.
     if not (x.is_cuda and strides[-1] == 1 and _dense(weight, (D, K), torch.float32, dev)
             and _dense(bias, (D,), torch.float32, dev) and _dense(state0, (n, K - 1, D), dt, dev)):
@@ -1087,6 +1094,7 @@ def _scan_setup(u, dt, A, B, C, D, z, dt_bias, state, cu_seqlens, dims):
         raise ValueError(f"u must have {dims} dimensions and A 2 (got {tuple(us)}, {tuple(As)})")
     dev, ty, width, N = u.device, u.dtype, us[-1], As[1]
     n = us[0] if cu_seqlens is None else _check_cu(cu_seqlens, us[0], dev)
+    _check_sizes("selective scan", (*us, N, n))
     few, f32 = (*us[:-1], N), torch.float32
     s_u, s_dt, s_B, s_C = u.stride(), dt.stride(), B.stride(), C.stride()
     s_z = s_u if z is None else z.stride()
@@ -1266,6 +1274,8 @@ def _add_norm(x, residual, weight, eps, total, y, out8, stream):
     if not shape:
         raise ValueError("x must have rows")
     D, rdt = shape[-1], dt if residual is None else residual.dtype
+    rows = x.numel() // D if D else 0
+    _check_sizes("norm", (rows, D))
     if residual is None and total is not None:
         raise ValueError("total is only written with a residual")
     if not (x.is_cuda and x.is_contiguous() and _dense(residual, shape, rdt, dev)
@@ -1285,7 +1295,6 @@ def _add_norm(x, residual, weight, eps, total, y, out8, stream):
     else:
         _check(y, "y", shape, ydt, dev)
     scale = _alloc(shape[:-1], torch.float32, dev, stream) if out8 else None
-    rows = x.numel() // D if D else 0
     st = lib.deltanet_add_rms_norm(x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(total),
                                    y.data_ptr(), _ptr(scale), rows, D, eps, _code(dt), _code(rdt),
                                    _stream(dev, stream))
@@ -1334,6 +1343,8 @@ def add_rms_norm_bwd(total: torch.Tensor, weight: Optional[torch.Tensor], dy: to
     if not shape:
         raise ValueError("total must have rows")
     D = shape[-1]
+    rows = total.numel() // D if D else 0
+    _check_sizes("norm", (rows, D))
     _check(total, "total", shape, rdt, dev)
     _check(dy, "dy", shape, dt, dev)
     _check_optional(dtotal, "dtotal", shape, rdt, dev)
@@ -1345,7 +1356,6 @@ def add_rms_norm_bwd(total: torch.Tensor, weight: Optional[torch.Tensor], dy: to
     dx = _alloc_like(dy, stream)
     dres = None if rdt == dt else _alloc_like(total, stream)
     dw = None if weight is None else _alloc((D,), torch.float32, dev, stream)
-    rows = total.numel() // D if D else 0
     need = _norm_bwd_workspace_bytes(rows, D) if dw is not None else 0
     keep, ws, ws_bytes = _workspace(workspace, need, dev, stream)
     st = lib.deltanet_add_rms_norm_bwd(total.data_ptr(), _ptr(weight), dy.data_ptr(), _ptr(dtotal),
