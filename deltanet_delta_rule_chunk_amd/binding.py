@@ -201,6 +201,8 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(device: torch.device, stream) -> int:
     if stream is not None:
+        if stream.device != device:  # its kernels would run there, on this device's addresses
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return stream.cuda_stream
     if _current_raw_stream is not None and device.index is not None:
         return _current_raw_stream(device.index)
