@@ -12,7 +12,10 @@
 // Bound by HBM.  A row's elements stay in the registers of a group of LPR lanes
 // (pieces of 8) between the sum of squares and the result, so each is read once: 65536 rows
 // of 4096 bf16 elements into 8 bits 330 us (5.7 TB/s), 16385 of 2072 with an fp32 stream
-// 74 us (5.5 TB/s) and their gradient 113 (4.8).
+// 74 us (5.5 TB/s) and their gradient 113 (4.8); fp32, 65536 x 4096, 764 and 807 us (5.6 and
+// 5.3).  The gradient is far from that at both ends of the widths: above 16384 elements its rows
+// do not fit 128 registers a lane (2048 x 20480 bf16 260 us, 1.3 TB/s, 16384 70), and narrow rows
+// leave a part of dw per group of lanes (65536 x 16: 59 us, 48 of them the parts' sum).
 
 #include "dn_launch.h"
 #include "dn_vec.h"
@@ -132,8 +135,9 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
   }
   // r is in every y of the row and in the scale, so the 8-bit values do not depend on it:
   // y / scale = (total w) (448 / max |total w|).  With products and quotient held as two fp32
-  // each, e4m3's own rounding is the only one; in single fp32 a few values in a million are a
-  // step off, for the same time (330 us for 65536 rows of 4096; fp64 359).  Of r the power of
+  // each, the quotient is rounded once to fp32 (2^-24) and then to e4m3, as one formed in 64 bits
+  // and converted is; in single fp32 a few values in a million are a step off, for the same
+  // time (330 us for 65536 rows of 4096; fp64 359).  Of r the power of
   // two is taken out first, which is exact and keeps the products in range.
   const float r2 = __uint_as_float(__float_as_uint(r) & 0x7f800000u);
   Pair top{0.f, 0.f};
@@ -184,7 +188,8 @@ __global__ __launch_bounds__(threads<LPR>()) void forward_kernel(AddNormArgs a) 
   }
 }
 
-// Workgroups walk over rows; each leaves a partial row of dw.
+// Workgroups walk over rows; each group of LPR lanes leaves a partial row of dw.  (1024 lanes of 4
+// pieces: 97 to 110 of w, dw, n and g in scratch memory, 264 to 280 bytes a lane.)
 template <int LPR, int P, typename T, typename R>
 __global__ __launch_bounds__(threads<LPR>()) void backward_kernel(AddNormArgs a, float* parts) {
   constexpr int NT = threads<LPR>(), RPB = NT / LPR;

@@ -86,9 +86,11 @@ struct Sizes {
 };
 inline long long channel_blocks(int D) { return (D + kCh - 1) / kCh; }
 // How sequences are cut: not if there are `enough` workgroups without a cut, or no more than
-// `whole` tokens (where workgroups are many, 1 token per `each` of them); else into `want` workgroups, but pieces of no less than 64 tokens, or 48 or 32 where
-// those give no more than `few` workgroups, or 16 where they give one per CU (then a call waits
-// for a walk's length, not for the units).
+// `whole` tokens (where workgroups are many, 1 token per `each` of them); else into `want`
+// workgroups, but pieces of no less than 64 tokens, or 48 or 32 where those give no more than `few`
+// workgroups, or 16 where they give one per CU (then a call waits for a walk's length, not for the
+// units).  Workgroups are counted whatever their waves (N / 4), packed sequences as if they were one, and
+// combine()'s time is not weighed: what that costs is at forward_sizes() and combine_kernel().
 struct Cutting {
   long long enough, want, few;
   int whole, each;

@@ -78,7 +78,9 @@ hipError_t make_plan(const int* cu, int n_seq, int L, const Sizes& s, void* ws, 
 // ---- states between segments -----------------------------------------------------------
 
 // A thread takes one (sequence, channel, state) in one direction; loads of 8 segments
-// are under way at a time.
+// are under way at a time.  Serial over a sequence's segments: 8 us for 32, 14 for 64, but 64 for 512
+// (64 channels x 32768 tokens, whose walks take 11 and 16) and about 490 for 4096 (262144 tokens, walks
+// of 51 and 67).
 static __global__ __launch_bounds__(256) void combine_kernel(Plan pl, long long items, int DN, int N, const float* A,
                                                              const float* logs, const float* h0, float* ahead, float* back) {
   const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -271,7 +273,10 @@ __global__ __launch_bounds__(64 * NW) void walk_kernel(ScanArgs a, Plan pl, int 
 // channels take 1974 us with 1024, 1765 with 1536, 1710 with 2048, 1630 with 4096, 1604 with 8192,
 // which costs shorter sequences as much.  Pieces: 512 tokens of 1024 channels, 26 us in pieces
 // of 64, 23 of 48, 21 of 32, 22 of 16; 128 of them 26, 22, 20 and 17; 8192 of 768, 69, 74 and 83
-// of 64, 48, 32.
+// of 64, 48, 32.  All of these are of batches of equal sequences, with 16 states.  With 8 states a workgroup
+// has half the waves and the cut ends too early: 16 x 1024 tokens of 2048 channels, 512 workgroups, 193 us, 8 of
+// them, cut, 87 (16 states: 177 and 112; 32: 254 and 200).  Packed sequences are cut as one long one: 32 of
+// 1024 tokens, 1024 channels, 230 us, as a batch, uncut, 178; 24 of 4096, 2048 channels, 1171 and 883.
 static Sizes forward_sizes(int B, int L, int D, bool packed, int n_seq) {
   return sizes_of(packed, B, L, n_seq, D, {512, 4096, 640, 80, 1});
 }

@@ -533,7 +533,8 @@ size_t deltanet_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, i
  *            no sequence holds); dz is not used without z
  *   dA     : [D, N] fp32;  dD_skip, ddt_bias: [D] fp32 or NULL (not written);  dh0: [n, D, N] fp32 or NULL
  * Nothing from a forward call is needed.  All sums run in an order that does not change from
- * call to call.  The workspace holds a state for every 16 tokens.
+ * call to call.  The workspace holds two states ([D, N] fp32) for every 16 tokens or part of them in
+ * a segment, and dB's and dC's parts, [B, L, N] fp32 each for every 64 channels.
  */
 int deltanet_selective_scan_bwd(const void* u, const void* dt, const void* Bm, const void* Cm, const void* z,
                                 const long long* strides, const float* A, const float* D_skip, const float* dt_bias,
@@ -559,8 +560,8 @@ int deltanet_selective_scan_step(const void* u, const void* dt, const void* Bm, 
  *   y      : [rows, D] dtype;  or, with scale ([rows] fp32), 8-bit e4m3 values with
  *            y = value * scale: scale is the row's largest magnitude / 448 (1 for a row of zeros)
  *   D a multiple of 8, up to 32768; dtype = DN_F32 needs residual_dtype = DN_F32.  Evaluated in fp32:
- * rows beyond ~1e19 overflow their sum of squares (y is then zeros); with eps = 0 a row of
- * zeros is not finite.  What is not finite stays in its row.
+ * rows beyond ~1e19 overflow their sum of squares (y is then zeros); with eps = 0 rows below ~1e-19
+ * lose digits of theirs, and a row of zeros is not finite.  What is not finite stays in its row.
  */
 int deltanet_add_rms_norm(const void* x, const void* residual, const float* weight, void* total, void* y, float* scale,
                           int rows, int D, float eps, dn_dtype dtype, dn_dtype residual_dtype, hipStream_t stream);
