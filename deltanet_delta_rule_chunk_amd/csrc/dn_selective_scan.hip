@@ -371,7 +371,8 @@ bool selective_scan_fits(int B, int L, int D, int N, bool packed, int n_seq, boo
   if (L > 0x7fffffff - 64 || states > 0x7fffffff || (packed && n_seq > (1 << 24))) return false;
   const ssm::Sizes s = backward ? ssm::backward_sizes(B, L, D, packed, n_seq) : ssm::forward_sizes(B, L, D, packed, n_seq);
   if (s.segments > max_blocks(16 * N) / D64 || (long long)n_seq > max_blocks(256) * 256 / states) return false;
-  return !backward || (long long)B * L <= max_blocks(256) * 1024 / N;
+  // (The gradient's last two launches: 1024 values of dB and dC, 16 columns of dA, dD and the bias's gradient per workgroup.)
+  return !backward || ((long long)B * L <= max_blocks(256) * 1024 / N && states + 2LL * D <= max_blocks(256) * 16);
 }
 
 size_t selective_scan_workspace_bytes(int B, int L, int D, int N, bool packed, int n_seq) {

@@ -533,8 +533,9 @@ size_t deltanet_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, i
  *            no sequence holds); dz is not used without z
  *   dA     : [D, N] fp32;  dD_skip, ddt_bias: [D] fp32 or NULL (not written);  dh0: [n, D, N] fp32 or NULL
  * Nothing from a forward call is needed.  All sums run in an order that does not change from
- * call to call.  The workspace holds two states ([D, N] fp32) for every 16 tokens or part of them in
- * a segment, and dB's and dC's parts, [B, L, N] fp32 each for every 64 channels.
+ * call to call.  D (N + 2) is at most 2^28 - 16.  The workspace holds two states ([D, N] fp32) for
+ * every 16 tokens or part of them in a segment, and dB's and dC's parts, [B, L, N] fp32 each for
+ * every 64 channels.
  */
 int deltanet_selective_scan_bwd(const void* u, const void* dt, const void* Bm, const void* Cm, const void* z,
                                 const long long* strides, const float* A, const float* D_skip, const float* dt_bias,
