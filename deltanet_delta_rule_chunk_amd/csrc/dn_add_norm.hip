@@ -357,7 +357,8 @@ static hipError_t by_type(const AddNormArgs& a) {
 
 bool add_norm_fits(int rows, int D) {
   const norm::Shape s = norm::shape_of(D);
-  return D <= norm::kMostD && rows <= max_blocks(s.lpr > 256 ? s.lpr : 256);
+  const long long rpb = norm::rows_per_block(s);
+  return D <= norm::kMostD && (rows + rpb - 1) / rpb <= max_blocks(s.lpr > 256 ? s.lpr : 256);
 }
 
 hipError_t launch_add_norm(const AddNormArgs& a) { return norm::by_type<false>(a); }
